@@ -1,5 +1,6 @@
 /*
- * muon.h -- C ABI of the MI355X (gfx950) Muon optimizer step.
+ * muon.h -- C ABI of the MI355X (gfx950) Muon optimizer step, and of the
+ * transformer block's operators that train with it (last section).
  *
  * The operation (per hidden weight matrix W with gradient G and momentum
  * buffer M), as the pages describe it:
@@ -277,6 +278,124 @@ int muon_check(muon_plan* plan, void* hip_stream);
  * ever met, so every block of the next fused launch gives up and returns).
  * MUON_E_INVAL for other values or a plan that is not fused. */
 int muon_fused_limits(muon_plan* plan, int32_t spin_limit, int32_t dep_bias);
+
+/* ---- operators of the block whose matrices the step trains ------------------
+ *
+ * A GPT-2-style block needs, besides products with its hidden matrices, a norm
+ * and an attention whose gradients end in those matrices: layer norm, and
+ * causal attention over packed sequences (the overview page "The NanoGPT
+ * speedrun", record #12, trains on documents packed into one long sequence
+ * with document masking).  Both have a forward and a backward call.
+ *
+ * They follow the conventions of the step: the caller owns every buffer, the
+ * library allocates nothing and never waits for the device; every pointer is a
+ * device pointer of the current device, which hip_stream belongs to; calls
+ * may be captured in a graph; errors are codes with a message in
+ * muon_last_error().  A call keeps nothing: calls on different streams or
+ * threads are independent as long as their buffers and workspaces are.
+ * Results are bitwise reproducible (no atomics).  NaN and infinities are not
+ * inspected; they propagate as in the formulas. */
+
+/* Layer norm of `rows` rows of `cols` elements (cols <= 2^20).  Leading
+ * dimensions are in elements (0 is read as cols).  x, y, dy and dx have
+ * x_dtype; weight and bias have p_dtype, and a NULL one counts as ones or
+ * zeros.  Arithmetic is fp32.  Rows that start at multiples of 16 bytes (and
+ * parameters that do) are read and written 16 bytes at a time, others element
+ * by element. */
+typedef struct muon_layernorm_desc {
+  int64_t rows;
+  int64_t cols;
+  int64_t ld_x, ld_y, ld_dy, ld_dx;
+  int32_t x_dtype;
+  int32_t p_dtype;
+  float eps;        /* >= 0 */
+  int32_t reserved; /* must be 0 */
+} muon_layernorm_desc;
+
+/* y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps), with the
+ * row's mean and biased variance; mean[rows] and rstd[rows] (fp32) are written
+ * for the backward call.  y must not be x.  rows == 0 does nothing. */
+int muon_layernorm_forward(const muon_layernorm_desc* desc, const void* x, const void* weight, const void* bias,
+                           void* y, float* mean, float* rstd, void* hip_stream);
+
+/* Bytes of device workspace muon_layernorm_backward needs for its parameter
+ * gradients; 0 on invalid arguments.  Host-only. */
+size_t muon_layernorm_workspace_size(const muon_layernorm_desc* desc);
+
+/* Gradients of the forward call: dx (x_dtype), dweight[cols] and dbias[cols]
+ * (fp32, overwritten; zero when rows == 0).  Any of the three may be NULL, but
+ * not all.  dx must be neither dy nor x.  workspace (256-byte aligned) may be
+ * NULL when dweight and dbias are. */
+int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, const void* x, const void* weight,
+                            const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                            void* workspace, size_t ws_bytes, void* hip_stream);
+
+/* Causal attention over `tokens` packed tokens.  cu_seqlens (device, seqs + 1
+ * int32, cu_seqlens[0] = 0, not decreasing, last one <= tokens) holds the
+ * sequences' offsets; a sequence may be empty.  Token i of a sequence attends
+ * to its tokens 0 .. i.  Query head h reads key/value head
+ * h / (q_heads / kv_heads).  head_dim: a multiple of 8, at most 128.  dtype:
+ * MUON_DTYPE_BF16 or MUON_DTYPE_F32, of every operand.  scale > 0 multiplies
+ * the scores.
+ *
+ * cu_seqlens is not checked (it is read on the device); offsets outside
+ * [0, tokens] are clamped and decreasing ones make empty sequences, so no
+ * access leaves the operands, but rows that two sequences claim are undefined.
+ *
+ * Rows behind the last sequence, cu_seqlens[seqs] .. tokens - 1, are never
+ * read; in each output they are left as they were, or set to zero when the
+ * output's flag is given.
+ *
+ * bf16: products take bf16 operands (probabilities and score gradients are
+ * rounded to bf16 for theirs) and accumulate in fp32, where softmax
+ * statistics are held.  fp32: fp32 throughout.  Keys and values are read in
+ * tiles of up to 128 tokens, and masked ones get weight zero: a NaN or
+ * infinity in a token's k or v can therefore reach the outputs of earlier
+ * tokens of the same sequence (0 * Inf), but never another sequence. */
+typedef struct muon_attention_desc {
+  int64_t tokens;
+  int32_t seqs;
+  int32_t q_heads;
+  int32_t kv_heads; /* divides q_heads */
+  int32_t head_dim;
+  int32_t dtype;
+  float scale;
+  int32_t reserved; /* must be 0 */
+} muon_attention_desc;
+
+/* One (tokens, heads, head_dim) operand: strides in elements, head_dim
+ * contiguous.  data and both strides must be multiples of 16 bytes.  Inputs
+ * may overlap or repeat (slices of one projection, stride 0); the rows of an
+ * output must not overlap. */
+typedef struct muon_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} muon_heads;
+
+#define MUON_ATTENTION_ZERO_OUT 1 /* forward: zero out's rows behind the last sequence */
+#define MUON_ATTENTION_ZERO_LSE 2 /* forward: and lse's */
+#define MUON_ATTENTION_ZERO_DQ 1  /* backward: dq's, dk's, dv's */
+#define MUON_ATTENTION_ZERO_DK 2
+#define MUON_ATTENTION_ZERO_DV 4
+
+/* out = softmax(scale q k^T) v, and lse[h * tokens + t] (fp32), the natural
+ * logarithm of the sum of the exponentials, for the backward call. */
+int muon_attention_forward(const muon_attention_desc* desc, const int32_t* cu_seqlens, const muon_heads* q,
+                           const muon_heads* k, const muon_heads* v, const muon_heads* out, float* lse,
+                           uint32_t flags, void* hip_stream);
+
+/* Bytes of device workspace muon_attention_backward needs; 0 on invalid
+ * arguments.  Host-only. */
+size_t muon_attention_workspace_size(const muon_attention_desc* desc);
+
+/* Gradients of the forward call, from its inputs, its out and lse, and dout.
+ * dq, dk and dv are overwritten (they may be slices of one buffer, but not
+ * inputs); dk and dv sum over the query heads of their group. */
+int muon_attention_backward(const muon_attention_desc* desc, const int32_t* cu_seqlens, const muon_heads* dout,
+                            const muon_heads* q, const muon_heads* k, const muon_heads* v, const muon_heads* out,
+                            const float* lse, const muon_heads* dq, const muon_heads* dk, const muon_heads* dv,
+                            uint32_t flags, void* workspace, size_t ws_bytes, void* hip_stream);
 
 #ifdef __cplusplus
 }

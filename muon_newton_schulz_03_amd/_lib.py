@@ -26,7 +26,12 @@ KIND_NAMES = ("momentum", "gram", "poly", "update", "apply", "norm", "fused")
 
 EXPORTS = ("muon_version", "muon_workspace_size", "muon_init", "muon_step", "muon_step_schedule", "muon_destroy",
            "muon_last_error", "muon_describe", "muon_profile_enable", "muon_profile_select", "muon_profile_read",
-           "muon_step_scratch", "muon_check", "muon_fused_limits")
+           "muon_step_scratch", "muon_check", "muon_fused_limits",
+           "muon_layernorm_forward", "muon_layernorm_workspace_size", "muon_layernorm_backward",
+           "muon_attention_forward", "muon_attention_workspace_size", "muon_attention_backward")
+
+ATTENTION_ZERO_OUT, ATTENTION_ZERO_LSE = 1, 2
+ATTENTION_ZERO_DQ, ATTENTION_ZERO_DK, ATTENTION_ZERO_DV = 1, 2, 4
 
 
 class MatrixDesc(ctypes.Structure):
@@ -47,6 +52,22 @@ class PlanInfo(ctypes.Structure):
                 ("blocks", ctypes.c_int32 * KIND_COUNT), ("x_master_iters", ctypes.c_int32),
                 ("path", ctypes.c_int32), ("n_f32_matrices", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("bf16_tile_rows", ctypes.c_int32), ("bf16_tile_cols", ctypes.c_int32), ("fused", ctypes.c_int32)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_dy", ctypes.c_int64), ("ld_dx", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("p_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class MuonError(RuntimeError):
@@ -103,6 +124,20 @@ def load() -> ctypes.CDLL:
     lib.muon_check.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.muon_fused_limits.restype = ctypes.c_int
     lib.muon_fused_limits.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32]
+    vp, hp = ctypes.c_void_p, P(Heads)
+    lib.muon_layernorm_forward.restype = ctypes.c_int
+    lib.muon_layernorm_forward.argtypes = [P(LayerNormDesc)] + [vp] * 7
+    lib.muon_layernorm_workspace_size.restype = ctypes.c_size_t
+    lib.muon_layernorm_workspace_size.argtypes = [P(LayerNormDesc)]
+    lib.muon_layernorm_backward.restype = ctypes.c_int
+    lib.muon_layernorm_backward.argtypes = [P(LayerNormDesc)] + [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.muon_attention_forward.restype = ctypes.c_int
+    lib.muon_attention_forward.argtypes = [P(AttentionDesc), vp, hp, hp, hp, hp, vp, ctypes.c_uint32, vp]
+    lib.muon_attention_workspace_size.restype = ctypes.c_size_t
+    lib.muon_attention_workspace_size.argtypes = [P(AttentionDesc)]
+    lib.muon_attention_backward.restype = ctypes.c_int
+    lib.muon_attention_backward.argtypes = ([P(AttentionDesc), vp] + [hp] * 5 + [vp] + [hp] * 3 +
+                                            [ctypes.c_uint32, vp, ctypes.c_size_t, vp])
     _lib = lib
     return lib
 

@@ -1,0 +1,251 @@
+"""Python binding of the transformer block's operators: layer norm and packed causal attention.
+
+Each has a forward and a backward call; the caller keeps what the backward
+call needs (its inputs, and the statistics that the forward call returns).
+Every call runs in the HIP library on the current torch stream of the
+tensors' device, which need not be the current device; this module checks
+the tensors, allocates outputs that are not given, and the workspace, with
+torch, and fills descriptors.  There is no fallback: if the library is
+missing, `_lib.load` raises.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from ._lib import AttentionDesc, Heads, LayerNormDesc
+
+_DTYPES = {torch.float32: _lib.MUON_DTYPE_F32, torch.bfloat16: _lib.MUON_DTYPE_BF16}
+
+
+def _check(t: torch.Tensor, name: str, device: torch.device, dtype=None) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} is not a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, cols, leading dimension) of a tensor whose leading dimensions step as one."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = t.shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    rows, ld, step = 1, cols, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size != 1:
+            if step is None:
+                ld = stride
+            elif stride != step:
+                raise ValueError(f"{name}: the leading dimensions do not step as one (call .contiguous())")
+            step = stride * size
+        rows *= size
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld} for {cols} columns)")
+    return rows, cols, ld if rows > 1 else cols
+
+
+def _param(p: Optional[torch.Tensor], name: str, cols: int, device, dtype):
+    if p is None:
+        return dtype, None
+    _check(p, name, device, dtype)
+    if p.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    if p.shape != (cols,) or not p.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {cols} elements")
+    return p.dtype, p.data_ptr()
+
+
+def _stream(device) -> ctypes.c_void_p:
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
+                       eps: float = 1e-5, out: Optional[torch.Tensor] = None
+                       ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm over the last dimension: (y, mean, rstd), the statistics in float32 and of x's leading shape.
+
+    x: float32 or bfloat16, with a contiguous last dimension and rows of one
+    stride.  weight and bias (one dtype, float32 or bfloat16) may be None.
+    """
+    lib = _lib.load()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x is not a device tensor")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    rows, cols, ld = _rows(x, "x")
+    pt, w = _param(weight, "weight", cols, x.device, None)
+    pt, b = _param(bias, "bias", cols, x.device, pt)
+    with torch.cuda.device(x.device):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        _check(y, "out", x.device, x.dtype)
+        if y.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        d = LayerNormDesc(rows, cols, ld, _rows(y, "out")[2], 0, 0, _DTYPES[x.dtype],
+                          _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], eps, 0)
+        _lib.check(lib.muon_layernorm_forward(ctypes.byref(d), x.data_ptr(), w, b, y.data_ptr(), mean.data_ptr(),
+                                              rstd.data_ptr(), _stream(x.device)))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, *, dx: Optional[torch.Tensor] = None,
+                        need_weight: bool = True, need_bias: bool = True
+                        ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of `layer_norm_forward`: (dx, dweight, dbias).
+
+    dx has x's dtype; dweight and dbias are float32, and None where not needed.
+    mean and rstd are the forward call's.
+    """
+    lib = _lib.load()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x is not a device tensor")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    dev = x.device
+    rows, cols, ld = _rows(x, "x")
+    _check(dy, "dy", dev, x.dtype)
+    if dy.shape != x.shape:
+        raise ValueError("dy must have x's shape")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _check(t, name, dev, torch.float32)
+        if t.shape != x.shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and of x's leading shape")
+    pt, w = _param(weight, "weight", cols, dev, None)
+    with torch.cuda.device(dev):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _check(dx, "dx", dev, x.dtype)
+        if dx.shape != x.shape:
+            raise ValueError("dx must have x's shape")
+        d = LayerNormDesc(rows, cols, ld, 0, _rows(dy, "dy")[2], _rows(dx, "dx")[2], _DTYPES[x.dtype],
+                          _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], 0.0, 0)
+        dw = torch.empty(cols, dtype=torch.float32, device=dev) if need_weight else None
+        db = torch.empty(cols, dtype=torch.float32, device=dev) if need_bias else None
+        ws, nbytes = None, 0
+        if need_weight or need_bias:
+            nbytes = lib.muon_layernorm_workspace_size(ctypes.byref(d))
+            if nbytes == 0:
+                raise _lib.MuonError(_lib.MUON_E_INVAL, _lib.last_error())
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _lib.check(lib.muon_layernorm_backward(
+            ctypes.byref(d), dy.data_ptr(), x.data_ptr(), w, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+            None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
+            None if ws is None else ws.data_ptr(), nbytes, _stream(dev)))
+    return dx, dw, db
+
+
+def _heads(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> Heads:
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape (tokens, heads, head_dim)")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _attention(q, k, v, cu_seqlens, scale):
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q is not a device tensor")
+    if q.dtype not in _DTYPES:
+        raise ValueError("q must be float32 or bfloat16")
+    hq = _heads(q, "q")
+    for name, t in (("k", k), ("v", v)):
+        _check(t, name, q.device, q.dtype)
+    hk, hv = _heads(k, "k"), _heads(v, "v", k)
+    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError(f"k has shape {tuple(k.shape)}, which does not go with q's {tuple(q.shape)}")
+    _check(cu_seqlens, "cu_seqlens", q.device, torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous vector of at least one offset")
+    dim = q.shape[2]
+    if scale is None:
+        scale = 1.0 / math.sqrt(dim) if dim else 1.0
+    d = AttentionDesc(q.shape[0], cu_seqlens.numel() - 1, q.shape[1], k.shape[1], dim, _DTYPES[q.dtype], scale, 0)
+    return d, hq, hk, hv
+
+
+def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                             scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention inside each of the packed sequences: (out, lse).
+
+    q (tokens, q_heads, head_dim), k and v (tokens, kv_heads, head_dim):
+    bfloat16 or float32, possibly slices of one projection's output.
+    cu_seqlens: device int32 offsets of the sequences, 0 first.  scale: of the
+    scores, default 1 / sqrt(head_dim).  lse (q_heads, tokens), float32, is for
+    the backward call.  Rows behind the last sequence are zero in results that
+    this call allocates and left as they were in those given.
+    """
+    lib = _lib.load()
+    d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
+    dev, flags = q.device, 0
+    with torch.cuda.device(dev):
+        if out is None:
+            out, flags = torch.empty(q.shape, dtype=q.dtype, device=dev), flags | _lib.ATTENTION_ZERO_OUT
+        if lse is None:
+            lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev)
+            flags |= _lib.ATTENTION_ZERO_LSE
+        _check(out, "out", dev, q.dtype)
+        ho = _heads(out, "out", q)
+        _check_lse(lse, q)
+        _lib.check(lib.muon_attention_forward(
+            ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
+            ctypes.byref(ho), lse.data_ptr(), flags, _stream(dev)))
+    return out, lse
+
+
+def _check_lse(lse, q):
+    _check(lse, "lse", q.device, torch.float32)
+    if lse.shape != (q.shape[1], q.shape[0]) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous (q_heads, tokens) tensor")
+
+
+def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              out: torch.Tensor, lse: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                              scale: Optional[float] = None, dq: Optional[torch.Tensor] = None,
+                              dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None
+                              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of `packed_attention_forward`: (dq, dk, dv), in the inputs' dtype.
+
+    out and lse are the forward call's, under the same scale.  dq, dk and dv
+    may be given, for example as slices of one buffer, and are overwritten.
+    Rows behind the last sequence are zero in gradients that this call
+    allocates and left as they were in those given.
+    """
+    lib = _lib.load()
+    d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
+    dev, flags = q.device, 0
+    _check(dout, "dout", dev, q.dtype)
+    _check(out, "out", dev, q.dtype)
+    _check_lse(lse, q)
+    hdo, ho = _heads(dout, "dout", q), _heads(out, "out", q)
+    with torch.cuda.device(dev):
+        if dq is None:
+            dq, flags = torch.empty(q.shape, dtype=q.dtype, device=dev), flags | _lib.ATTENTION_ZERO_DQ
+        if dk is None:
+            dk, flags = torch.empty(k.shape, dtype=q.dtype, device=dev), flags | _lib.ATTENTION_ZERO_DK
+        if dv is None:
+            dv, flags = torch.empty(k.shape, dtype=q.dtype, device=dev), flags | _lib.ATTENTION_ZERO_DV
+        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            _check(t, name, dev, q.dtype)
+        gq, gk, gv = _heads(dq, "dq", q), _heads(dk, "dk", k), _heads(dv, "dv", k)
+        nbytes = lib.muon_attention_workspace_size(ctypes.byref(d))
+        if nbytes == 0:
+            raise _lib.MuonError(_lib.MUON_E_INVAL, _lib.last_error())
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _lib.check(lib.muon_attention_backward(
+            ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hdo), ctypes.byref(hq), ctypes.byref(hk),
+            ctypes.byref(hv), ctypes.byref(ho), lse.data_ptr(), ctypes.byref(gq), ctypes.byref(gk), ctypes.byref(gv),
+            flags, ws.data_ptr(), nbytes, _stream(dev)))
+    return dq, dk, dv

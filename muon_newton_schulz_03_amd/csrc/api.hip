@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "block_internal.h"
 #include "muon_internal.h"
 
 namespace muon {
@@ -28,11 +29,9 @@ hipError_t launch_fused(const FusedArgs& args, int blocks, hipStream_t stream, h
 hipError_t launch_norm(const DevMat* mats, int n, hipStream_t stream, hipEvent_t ev0, hipEvent_t ev1);
 }  // namespace muon
 
-using namespace muon;
+namespace muon {
 
-namespace {
-
-thread_local std::string g_err;
+static thread_local std::string g_err;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -47,6 +46,14 @@ int fail(int code, const char* fmt, ...) {
 int hip_fail(hipError_t e, const char* what) {
   return fail(MUON_E_HIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
+
+void clear_error() { g_err.clear(); }
+
+}  // namespace muon
+
+using namespace muon;
+
+namespace {
 
 void release(muon_plan* p);
 

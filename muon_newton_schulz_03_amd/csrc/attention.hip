@@ -1,0 +1,638 @@
+// gfx950 (CDNA4) causal attention over packed sequences with grouped heads,
+// forward and backward.
+//
+// Per sequence and query head h (key/value head h / group), with
+// s_ij = scale q_i . k_j for j <= i:
+//   lse_i = log sum_j exp(s_ij),  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
+//   delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j
+//   dk_j = scale sum_{h in group, i >= j} ds_ij q_i,  dv_j = sum_{h in group, i >= j} p_ij do_i
+#include "block_internal.h"
+#include "device_common.h"
+
+namespace muon {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;  // see softmax_tile
+
+// ------------------------------------------------------------ element types --
+// A fragment is one lane's share of 16 contraction steps of a 32x32 product:
+// 8 elements, contraction indices 8 (lane / 32) .. +7 for operands read along
+// their rows.  bf16: one v_mfma_f32_32x32x16_bf16; fp32: eight
+// v_mfma_f32_32x32x2_f32, whose step e pairs element e of both lane halves.
+template <class T>
+struct Elem;
+
+template <>
+struct Elem<__bf16> {
+  typedef u32x4 Frag;
+  static constexpr int kFragChunks = 1;
+  __device__ static __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  }
+  __device__ static __forceinline__ Frag pack(const float* v) { return pack8_bf16(v); }
+  __device__ static __forceinline__ void unpack(Frag f, float* v) { unpack8_bf16(f, v); }
+};
+
+struct F32Frag {
+  f32x4 lo, hi;
+};
+template <>
+struct Elem<float> {
+  typedef F32Frag Frag;
+  static constexpr int kFragChunks = 2;
+  __device__ static __forceinline__ f32x16 mma(Frag a, Frag b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.lo[e], b.lo[e], c, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.hi[e], b.hi[e], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static __forceinline__ Frag pack(const float* v) {
+    return Frag{f32x4{v[0], v[1], v[2], v[3]}, f32x4{v[4], v[5], v[6], v[7]}};
+  }
+  __device__ static __forceinline__ void unpack(Frag f, float* v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f.lo[e], v[4 + e] = f.hi[e];
+  }
+};
+
+// --------------------------------------------------------------- LDS tiles --
+// A tile is `rows` rows of DP elements without padding; 16-byte chunk c of
+// row r sits at chunk c ^ swz(r).  The swizzles make both kinds of fragment
+// read conflict-free (16-byte reads of one chunk of 16 rows; transposing
+// reads of 4 rows x 64 bytes): swz has period 16 in r, takes a row's share of
+// the 256 bytes served per clock into account, and moves 4 consecutive rows
+// to different 64-byte quarters.
+template <int ROW_BYTES>
+__device__ __forceinline__ int swz(int r) {
+  if (ROW_BYTES % 256 == 0) return ((r & 3) << 2) | ((r >> 2) & 3);
+  if (ROW_BYTES % 128 == 0) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  return (r >> 2) & 3;
+}
+
+template <class T, int DP>
+struct Tiles {
+  typedef typename Elem<T>::Frag Frag;
+  static constexpr int kRow = DP * (int)sizeof(T);  // bytes
+  static constexpr int kCpr = kRow / 16;            // chunks a row
+
+  // Row-wise fragment: 16-step s of row `row`, lane half h.
+  __device__ static __forceinline__ Frag row_frag(const char* tile, int row, int s, int h) {
+    if constexpr (sizeof(T) == 2) {
+      return *(const u32x4*)(tile + row * kRow + (((2 * s + h) ^ swz<kRow>(row)) << 4));
+    } else {
+      const int c = 4 * s + 2 * h;
+      return Frag{*(const f32x4*)(tile + row * kRow + ((c ^ swz<kRow>(row)) << 4)),
+                  *(const f32x4*)(tile + row * kRow + (((c + 1) ^ swz<kRow>(row)) << 4))};
+    }
+  }
+  // Column-wise fragment: element (lane & 31) of 32-column group t over the
+  // 16 rows base .. base + 15, in the order in which an accumulator holds
+  // them: rows 4 h .. 4 h + 3, then 8 + 4 h .. 8 + 4 h + 3.  bf16: two
+  // transposing reads (each 16 lanes fetch 4 rows x 16 columns, and lane r
+  // of them gets column r's 4 values).
+  __device__ static __forceinline__ Frag col_frag(const char* tile, int base, int t, int lane) {
+    if constexpr (sizeof(T) == 2) {
+      const int g = lane >> 4, r = lane & 15;
+      const int row = 4 * (g >> 1) + (r >> 2), c = 4 * t + 2 * (g & 1) + ((r & 3) >> 1);
+      typedef short v4i16 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4i16* lds_v4;
+      const char* p0 = tile + (base + row) * kRow + ((c ^ swz<kRow>(row)) << 4) + ((r & 1) << 3);
+      const char* p1 = tile + (base + row + 8) * kRow + ((c ^ swz<kRow>(row + 8)) << 4) + ((r & 1) << 3);
+      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(void*)p0));
+      const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4)(void*)p1));
+      return u32x4{a.x, a.y, b.x, b.y};
+    } else {
+      const int h = lane >> 5, d = 32 * t + (lane & 31);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int row = 8 * (e >> 2) + 4 * h + (e & 3);
+        v[e] = *(const float*)(tile + (base + row) * kRow + (((d >> 2) ^ swz<kRow>(row)) << 4) + ((d & 3) << 2));
+      }
+      return Elem<float>::pack(v);
+    }
+  }
+};
+
+// Moves ROWS rows of one head from global memory to an LDS tile through
+// registers: load() requests them, store() writes them (rows at or past
+// `end` and elements at or past the head dimension as zeros).
+template <class T, int DP, int ROWS>
+struct Stager {
+  static constexpr int kN = ROWS * DP * (int)sizeof(T) / 16 / kThreads;
+  static_assert(kN * kThreads * 16 == ROWS * DP * (int)sizeof(T), "whole chunks per thread");
+  u32x4 buf[kN];
+  __device__ __forceinline__ void load(const T* head, int64_t token_stride, int row0, int end, int dim, int tid) {
+    constexpr int cpr = Tiles<T, DP>::kCpr;
+    constexpr int epc = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int idx = i * kThreads + tid, row = row0 + idx / cpr, c = idx % cpr;
+      buf[i] = u32x4{0, 0, 0, 0};
+      if (row < end && c * epc < dim) buf[i] = *gv<u32x4>(head + row * token_stride + c * epc);
+    }
+  }
+  __device__ __forceinline__ void store(char* tile, int tid) const {
+    constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int idx = i * kThreads + tid, row = idx / cpr, c = idx % cpr;
+      *(u32x4*)(tile + row * kRow + ((c ^ swz<kRow>(row)) << 4)) = buf[i];
+    }
+  }
+};
+
+// Row-wise fragments of one row straight from global memory (the operand that
+// stays in registers); zeros where the row is not valid or past `dim`.
+template <class T, int DP>
+__device__ __forceinline__ void load_frags(typename Elem<T>::Frag (&f)[DP / 16], const T* row, bool valid, int dim,
+                                           int h) {
+  constexpr int epc = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int s = 0; s < DP / 16; ++s) {
+    u32x4 w[Elem<T>::kFragChunks];
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kFragChunks; ++e) {
+      const int at = 16 * s + 8 * h + e * epc;
+      w[e] = u32x4{0, 0, 0, 0};
+      if (valid && at < dim) w[e] = *gv<u32x4>(row + at);
+    }
+    f[s] = __builtin_bit_cast(typename Elem<T>::Frag, w);
+  }
+}
+
+// The lane's columns of an accumulator tile set, acc[t][i] = element
+// d = 32 t + 8 (i / 4) + 4 h + i % 4 of its row, times `f`, as elements.
+template <class T, int DP>
+__device__ __forceinline__ void store_row(T* row, const f32x16 (&acc)[DP / 32], float f, int dim, int h) {
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = 32 * t + 8 * g + 4 * h;
+      if (d >= dim) continue;
+      const float a = acc[t][4 * g] * f, b = acc[t][4 * g + 1] * f, c = acc[t][4 * g + 2] * f,
+                  e = acc[t][4 * g + 3] * f;
+      if constexpr (sizeof(T) == 2)
+        *gv<u32x2>(row + d) = pack4_bf16(a, b, c, e);
+      else
+        *gv<f32x4>(row + d) = f32x4{a, b, c, e};
+    }
+}
+
+// Largest of / sum over the two lanes l, l ^ 32 that share a column.
+__device__ __forceinline__ float halves_max(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// -------------------------------------------------------- sequences, tiles --
+// Sequence i's tiles of `bm` rows take the slots from cu[i] / bm + i on: that
+// many are always free before the next sequence's first slot, so a block
+// finds its sequence by a search in cu alone, with no table built beforehand.
+// The rows behind the last sequence are "sequence" seqs.
+struct SeqTile {
+  int start, len;  // the sequence's first token and its length
+  int row0;        // first row of this tile, within the sequence
+  bool tail;       // rows behind the last sequence
+};
+__device__ __forceinline__ int token_at(const AttnArgs& a, int i) {
+  const int n = (int)a.tokens;
+  return i > a.seqs ? n : min(max(a.cu[i], 0), n);
+}
+__device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int slot, int bm, int lane) {
+  int lo = 0, hi = a.seqs + 1;  // the last i in [lo, hi) whose first slot is at or below `slot`
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64;
+    const int i = lo + lane * step;
+    const bool below = i < hi && token_at(a, i) / bm + i <= slot;
+    const int n = __popcll(__ballot(below));
+    lo += (n > 0 ? n - 1 : 0) * step;
+    hi = min(hi, lo + step);
+  }
+  SeqTile t;
+  t.tail = lo == a.seqs;
+  t.start = token_at(a, lo);
+  t.len = max(token_at(a, lo + 1) - t.start, 0);
+  const int tile = slot - (t.start / bm + lo);
+  t.row0 = tile < 0 || tile >= (t.len + bm - 1) / bm ? t.len : tile * bm;
+  return t;
+}
+inline int64_t slots_of(int64_t tokens, int seqs, int bm) { return tokens / bm + seqs + 1; }
+
+template <class T>
+__device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0, int rows, int dim, int tid) {
+  const int dw = dim * (int)sizeof(T) / 16;
+  for (int i = tid; i < rows * dw; i += kThreads) {
+    T* p = (T*)v.data + (int64_t)(row0 + i / dw) * v.token + head * v.head;
+    gv<u32x4>(p)[i % dw] = u32x4{0, 0, 0, 0};
+  }
+}
+
+// ----------------------------------------------------------------- forward --
+template <class T>
+struct Cfg {
+  static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
+};
+
+template <class T, int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs a) {
+  typedef typename Elem<T>::Frag Frag;
+  typedef Tiles<T, DP> Tl;
+  constexpr int BM = 128, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int kTile = KT * Tl::kRow;
+  __shared__ __align__(256) char lds[2][2][kTile];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, col = lane & 31;
+  const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
+  const int slot = (int)(gridDim.x / a.q_heads) - 1 - (int)(blockIdx.x / a.q_heads);
+  const SeqTile st = find_tile(a, slot, BM, lane);
+  if (st.row0 >= st.len) return;
+  if (st.tail) {
+    const int rows = min(BM, st.len - st.row0), r0 = st.start + st.row0;
+    if (a.zero_tail & kZeroOut) zero_rows<T>(a.o, head, r0, rows, a.dim, tid);
+    if ((a.zero_tail & kZeroLse) && tid < rows) a.lse[(int64_t)head * a.tokens + r0 + tid] = 0.f;
+    return;
+  }
+  const T* kp = (const T*)a.k.data + (int64_t)st.start * a.k.token + kvh * a.k.head;
+  const T* vp = (const T*)a.v.data + (int64_t)st.start * a.v.token + kvh * a.v.head;
+  const int qw = st.row0 + 32 * w, qi = qw + col;
+  const int wend = qw < st.len ? min(st.len, qw + 32) : 0;  // keys this wave looks at
+  const int ntile = (min(st.len, st.row0 + BM) + KT - 1) / KT;
+  const float c = a.scale * kLog2e;
+
+  Frag qf[ST];
+  load_frags<T, DP>(qf, (const T*)a.q.data + (st.start + (int64_t)qi) * a.q.token + head * a.q.head, qi < st.len,
+                    a.dim, h);
+  f32x16 o[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) o[t] = f32x16{};
+  float m = -__builtin_inff(), l = 0.f;
+
+  Stager<T, DP, KT> sk, sv;
+  sk.load(kp, a.k.token, 0, st.len, a.dim, tid);
+  sv.load(vp, a.v.token, 0, st.len, a.dim, tid);
+  sk.store(lds[0][0], tid);
+  sv.store(lds[0][1], tid);
+  __syncthreads();
+  for (int kt = 0; kt < ntile; ++kt) {
+    const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
+    const bool more = kt + 1 < ntile;
+    if (more) {
+      sk.load(kp, a.k.token, (kt + 1) * KT, st.len, a.dim, tid);
+      sv.load(vp, a.v.token, (kt + 1) * KT, st.len, a.dim, tid);
+    }
+    if (kt * KT < wend) {
+      f32x16 s[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        s[j] = f32x16{};
+#pragma unroll
+        for (int q = 0; q < ST; ++q) s[j] = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s[j]);
+      }
+      if (kt * KT + KT - 1 > qw) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (kt * KT + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) s[j][i] = -__builtin_inff();
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[j][i]);
+      top = halves_max(top) * c;
+      // The running maximum only has to keep exp2's arguments small: it is
+      // raised (and the sums rescaled) when a score passes it by more than
+      // kLazy, so p <= 2^kLazy, and most tiles rescale nothing.
+      if (__any(top > m + kLazy)) {
+        const float mn = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[t][i] *= f;
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        float p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -m));
+          l += p[i];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const Frag pf = Elem<T>::pack(p + 8 * u);
+#pragma unroll
+          for (int t = 0; t < DT; ++t) o[t] = Elem<T>::mma(Tl::col_frag(vl, 32 * j + 16 * u, t, lane), pf, o[t]);
+        }
+      }
+    }
+    if (more) {
+      sk.store(lds[(kt + 1) & 1][0], tid);
+      sv.store(lds[(kt + 1) & 1][1], tid);
+    }
+    __syncthreads();
+  }
+  l = halves_sum(l);
+  if (qi < st.len) {
+    const int64_t tok = st.start + (int64_t)qi;
+    store_row<T, DP>((T*)a.o.data + tok * a.o.token + head * a.o.head, o, 1.f / l, a.dim, h);
+    if (h == 0) a.lse[(int64_t)head * a.tokens + tok] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------- backward --
+// dQ, and delta for the next kernel.
+template <class T, int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
+  typedef typename Elem<T>::Frag Frag;
+  typedef Tiles<T, DP> Tl;
+  constexpr int BM = 128, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int kTile = KT * Tl::kRow;
+  __shared__ __align__(256) char lds[2][2][kTile];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, col = lane & 31;
+  const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
+  const int slot = (int)(gridDim.x / a.q_heads) - 1 - (int)(blockIdx.x / a.q_heads);
+  const SeqTile st = find_tile(a, slot, BM, lane);
+  if (st.row0 >= st.len) return;
+  if (st.tail) {
+    if (a.zero_tail & kZeroDq)
+      zero_rows<T>(a.dq, head, st.start + st.row0, min(BM, st.len - st.row0), a.dim, tid);
+    return;
+  }
+  const T* kp = (const T*)a.k.data + (int64_t)st.start * a.k.token + kvh * a.k.head;
+  const T* vp = (const T*)a.v.data + (int64_t)st.start * a.v.token + kvh * a.v.head;
+  const int qw = st.row0 + 32 * w, qi = qw + col;
+  const int wend = qw < st.len ? min(st.len, qw + 32) : 0;
+  const int ntile = (min(st.len, st.row0 + BM) + KT - 1) / KT;
+  const float c = a.scale * kLog2e;
+  const bool valid = qi < st.len;
+  const int64_t tok = st.start + (int64_t)qi;
+
+  Frag qf[ST], df[ST];
+  load_frags<T, DP>(qf, (const T*)a.q.data + tok * a.q.token + head * a.q.head, valid, a.dim, h);
+  load_frags<T, DP>(df, (const T*)a.dout.data + tok * a.dout.token + head * a.dout.head, valid, a.dim, h);
+  float delta = 0.f, lse2 = 0.f;
+  {
+    Frag of[ST];
+    load_frags<T, DP>(of, (const T*)a.o.data + tok * a.o.token + head * a.o.head, valid, a.dim, h);
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      float x[8], y[8];
+      Elem<T>::unpack(of[s], x);
+      Elem<T>::unpack(df[s], y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(x[e], y[e], delta);
+    }
+    delta = halves_sum(delta);
+    if (valid) {
+      lse2 = a.lse[(int64_t)head * a.tokens + tok] * kLog2e;
+      if (h == 0) a.delta[(int64_t)head * a.tokens + tok] = delta;
+    }
+  }
+  f32x16 dq[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
+
+  Stager<T, DP, KT> sk, sv;
+  sk.load(kp, a.k.token, 0, st.len, a.dim, tid);
+  sv.load(vp, a.v.token, 0, st.len, a.dim, tid);
+  sk.store(lds[0][0], tid);
+  sv.store(lds[0][1], tid);
+  __syncthreads();
+  for (int kt = 0; kt < ntile; ++kt) {
+    const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
+    const bool more = kt + 1 < ntile;
+    if (more) {
+      sk.load(kp, a.k.token, (kt + 1) * KT, st.len, a.dim, tid);
+      sv.load(vp, a.v.token, (kt + 1) * KT, st.len, a.dim, tid);
+    }
+    if (kt * KT < wend) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+        for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s);
+#pragma unroll
+        for (int q = 0; q < ST; ++q) dp = Elem<T>::mma(Tl::row_frag(vl, 32 * j + col, q, h), df[q], dp);
+        float ds[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+        if (kt * KT + 32 * j + 31 > qw) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (kt * KT + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) ds[i] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const Frag pf = Elem<T>::pack(ds + 8 * u);
+#pragma unroll
+          for (int t = 0; t < DT; ++t) dq[t] = Elem<T>::mma(Tl::col_frag(kl, 32 * j + 16 * u, t, lane), pf, dq[t]);
+        }
+      }
+    }
+    if (more) {
+      sk.store(lds[(kt + 1) & 1][0], tid);
+      sv.store(lds[(kt + 1) & 1][1], tid);
+    }
+    __syncthreads();
+  }
+  if (valid) store_row<T, DP>((T*)a.dq.data + tok * a.dq.token + head * a.dq.head, dq, a.scale, a.dim, h);
+}
+
+// dK and dV of 128 keys of one key/value head, over the query heads of its
+// group (or of one part of it) and the query rows from the keys on.
+template <class T, int DP>
+__global__ __launch_bounds__(kThreads, DP * sizeof(T) <= 128 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
+  typedef typename Elem<T>::Frag Frag;
+  typedef Tiles<T, DP> Tl;
+  constexpr int BN = 128, QR = Cfg<T>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int kTile = QR * Tl::kRow;
+  __shared__ __align__(256) char lds[2][2][kTile];
+  __shared__ __align__(16) float stat[2][2][QR];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, col = lane & 31;
+  const int per = a.kv_heads * a.splits;
+  const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
+  const SeqTile st = find_tile(a, (int)(blockIdx.x / per), BN, lane);
+  if (st.row0 >= st.len) return;
+  if (st.tail) {
+    const int rows = min(BN, st.len - st.row0), r0 = st.start + st.row0;
+    if (part == 0 && (a.zero_tail & kZeroDk)) zero_rows<T>(a.dk, kvh, r0, rows, a.dim, tid);
+    if (part == 0 && (a.zero_tail & kZeroDv)) zero_rows<T>(a.dv, kvh, r0, rows, a.dim, tid);
+    return;
+  }
+  const int kw = st.row0 + 32 * w, ki = kw + col;
+  const bool valid = ki < st.len;
+  const int64_t tok = st.start + (int64_t)ki;
+  const float c = a.scale * kLog2e;
+  const int hpp = a.group / a.splits, head0 = kvh * a.group + part * hpp;  // this block's query heads
+
+  Frag kf[ST], vf[ST];
+  load_frags<T, DP>(kf, (const T*)a.k.data + tok * a.k.token + kvh * a.k.head, valid, a.dim, h);
+  load_frags<T, DP>(vf, (const T*)a.v.data + tok * a.v.token + kvh * a.v.head, valid, a.dim, h);
+  f32x16 dk[DT], dv[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
+
+  const int qt0 = st.row0 / QR, nq = (st.len + QR - 1) / QR - qt0, total = nq * hpp;
+  Stager<T, DP, QR> sq, sd;
+  float sl = 0.f, sdl = 0.f;
+  auto load = [&](int it) {
+    const int head = head0 + it / nq, row0 = (qt0 + it % nq) * QR;
+    sq.load((const T*)a.q.data + (int64_t)st.start * a.q.token + head * a.q.head, a.q.token, row0, st.len, a.dim, tid);
+    sd.load((const T*)a.dout.data + (int64_t)st.start * a.dout.token + head * a.dout.head, a.dout.token, row0, st.len,
+            a.dim, tid);
+    if (tid < QR) {
+      const bool in = row0 + tid < st.len;
+      const int64_t at = (int64_t)head * a.tokens + st.start + row0 + tid;
+      sl = in ? a.lse[at] * kLog2e : __builtin_inff();  // p = 0 in rows past the end
+      sdl = in ? a.delta[at] : 0.f;
+    }
+  };
+  auto store = [&](int b) {
+    sq.store(lds[b][0], tid);
+    sd.store(lds[b][1], tid);
+    if (tid < QR) stat[b][0][tid] = sl, stat[b][1][tid] = sdl;
+  };
+  load(0);
+  store(0);
+  __syncthreads();
+  for (int it = 0; it < total; ++it) {
+    const char *ql = lds[it & 1][0], *dl = lds[it & 1][1];
+    const float *ll = stat[it & 1][0], *el = stat[it & 1][1];
+    const int q0 = (qt0 + it % nq) * QR;
+    if (it + 1 < total) load(it + 1);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      if (q0 + 32 * j + 31 < kw) continue;  // rows before every key of this wave
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(ql, 32 * j + col, q, h), kf[q], s);
+#pragma unroll
+      for (int q = 0; q < ST; ++q) dp = Elem<T>::mma(Tl::row_frag(dl, 32 * j + col, q, h), vf[q], dp);
+      float p[16], ds[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 lse2 = *(const f32x4*)(ll + 32 * j + 8 * g + 4 * h);
+        const f32x4 del = *(const f32x4*)(el + 32 * j + 8 * g + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * g + e;
+          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2[e]));
+          ds[i] = p[i] * (dp[i] - del[e]);
+        }
+      }
+      if (q0 + 32 * j < kw + 31) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (q0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) < ki) p[i] = ds[i] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          dv[t] = Elem<T>::mma(Tl::col_frag(dl, 32 * j + 16 * u, t, lane), pf, dv[t]);
+          dk[t] = Elem<T>::mma(Tl::col_frag(ql, 32 * j + 16 * u, t, lane), sf, dk[t]);
+        }
+      }
+    }
+    if (it + 1 < total) store((it + 1) & 1);
+    __syncthreads();
+  }
+  if (!valid) return;
+  if (a.splits == 1) {
+    store_row<T, DP>((T*)a.dk.data + tok * a.dk.token + kvh * a.dk.head, dk, a.scale, a.dim, h);
+    store_row<T, DP>((T*)a.dv.data + tok * a.dv.token + kvh * a.dv.head, dv, 1.f, a.dim, h);
+  } else {
+    float* p = a.part + (((int64_t)part * a.tokens + tok) * a.kv_heads + kvh) * 2 * a.dim;
+    store_row<float, DP>(p, dk, a.scale, a.dim, h);
+    store_row<float, DP>(p + a.dim, dv, 1.f, a.dim, h);
+  }
+}
+
+// Sums the parts of a split group in their order: part[split][token][kv head][dK, dV][dim].
+template <class T>
+__global__ __launch_bounds__(kThreads) void attention_sum_kernel(AttnArgs a) {
+  const int per = a.kv_heads * 2 * a.dim / 4;  // groups of 4 elements a token
+  const int64_t total = (int64_t)(token_at(a, a.seqs) - token_at(a, 0)) * per, first = (int64_t)token_at(a, 0) * per;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t tok = (first + i) / per;
+    const int at = (int)((first + i) % per), kvh = at / (a.dim / 2), e = at % (a.dim / 2) * 4;
+    f32x4 s = f32x4{};
+    for (int p = 0; p < a.splits; ++p) {
+      const f32x4 x = *gv<f32x4>(a.part + ((int64_t)p * a.tokens * per + first + i) * 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] += x[q];
+    }
+    const HeadView& v = e < a.dim ? a.dk : a.dv;
+    T* row = (T*)v.data + tok * v.token + kvh * v.head + (e < a.dim ? e : e - a.dim);
+    if constexpr (sizeof(T) == 2)
+      *gv<u32x2>(row) = pack4_bf16(s[0], s[1], s[2], s[3]);
+    else
+      *gv<f32x4>(row) = s;
+  }
+}
+
+template <class T, int DP>
+hipError_t forward_dp(const AttnArgs& a, hipStream_t stream) {
+  return launch_kernel(attention_forward_kernel<T, DP>, slots_of(a.tokens, a.seqs, 128) * a.q_heads, kThreads, a,
+                       stream);
+}
+
+template <class T, int DP>
+hipError_t backward_dp(const AttnArgs& a, hipStream_t stream) {
+  const int64_t slots = slots_of(a.tokens, a.seqs, 128);
+  hipError_t e = launch_kernel(attention_dq_kernel<T, DP>, slots * a.q_heads, kThreads, a, stream);
+  if (e == hipSuccess)
+    e = launch_kernel(attention_dkv_kernel<T, DP>, slots * a.kv_heads * a.splits, kThreads, a, stream);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t blocks = (a.tokens * a.kv_heads * 2 * a.dim / 4 + kThreads - 1) / kThreads;
+  return launch_kernel(attention_sum_kernel<T>, blocks < 4096 ? blocks : 4096, kThreads, a, stream);
+}
+
+template <class T>
+hipError_t by_dim(const AttnArgs& a, bool backward, hipStream_t s) {
+  switch ((a.dim + 31) / 32) {
+    case 1: return backward ? backward_dp<T, 32>(a, s) : forward_dp<T, 32>(a, s);
+    case 2: return backward ? backward_dp<T, 64>(a, s) : forward_dp<T, 64>(a, s);
+    case 3: return backward ? backward_dp<T, 96>(a, s) : forward_dp<T, 96>(a, s);
+    default: return backward ? backward_dp<T, 128>(a, s) : forward_dp<T, 128>(a, s);
+  }
+}
+
+}  // namespace
+
+// Query heads that share a key/value head are split over several blocks when
+// the whole groups give too few blocks for the 256 CUs.
+int attention_splits(int64_t tokens, int seqs, int q_heads, int kv_heads, int dim, bool bf16) {
+  (void)dim, (void)bf16, (void)seqs;
+  const int group = q_heads / kv_heads;
+  const int64_t blocks = (tokens / 128 + 1) * kv_heads;
+  int s = 1;
+  for (int d = 1; d <= group && blocks * s < 1024; ++d)
+    if (group % d == 0) s = d;
+  return s;
+}
+
+hipError_t launch_attention_forward(const AttnArgs& a, bool bf16, hipStream_t stream) {
+  return bf16 ? by_dim<__bf16>(a, false, stream) : by_dim<float>(a, false, stream);
+}
+hipError_t launch_attention_backward(const AttnArgs& a, bool bf16, hipStream_t stream) {
+  return bf16 ? by_dim<__bf16>(a, true, stream) : by_dim<float>(a, true, stream);
+}
+
+}  // namespace muon

@@ -1,0 +1,227 @@
+"""The block operators' C ABI and binding on the host (no GPU): refusals and workspace sizes.
+
+Every call here is rejected by argument checks before any HIP call, or is host-only.
+"""
+import ctypes
+import math
+import os
+
+import pytest
+import torch
+
+import block_reference as R
+from muon_newton_schulz_03_amd import _lib, block
+from muon_newton_schulz_03_amd._lib import AttentionDesc, Heads, LayerNormDesc
+
+INVAL, UNSUP, WORK = _lib.MUON_E_INVAL, _lib.MUON_E_UNSUPPORTED, _lib.MUON_E_WORKSPACE
+P = 0x10000  # a pointer that no call follows
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_lib.LIB_PATH):
+        from muon_newton_schulz_03_amd.build import build_library
+        build_library()
+    return _lib.load()
+
+
+def norm_desc(**kw):
+    d = dict(rows=8, cols=64, ld_x=0, ld_y=0, ld_dy=0, ld_dx=0, x_dtype=1, p_dtype=0, eps=1e-5, reserved=0)
+    d.update(kw)
+    return LayerNormDesc(*d.values())
+
+
+BAD_NORM = [(dict(rows=-1), INVAL), (dict(rows=(1 << 40) + 1), INVAL), (dict(cols=0), INVAL), (dict(cols=-3), INVAL),
+            (dict(cols=(1 << 20) + 1), INVAL), (dict(ld_x=63), INVAL), (dict(ld_y=1), INVAL), (dict(ld_dy=-64), INVAL),
+            (dict(ld_dx=(1 << 31) + 1), INVAL), (dict(x_dtype=2), UNSUP), (dict(p_dtype=-1), UNSUP),
+            (dict(eps=-1e-9), INVAL), (dict(eps=math.nan), INVAL), (dict(eps=math.inf), INVAL),
+            (dict(reserved=1), INVAL)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_NORM, ids=str)
+def test_layer_norm_refuses_descriptors(lib, kw, code):
+    d = ctypes.byref(norm_desc(**kw))
+    assert lib.muon_layernorm_forward(d, P, P, P, 2 * P, P, P, None) == code
+    assert _lib.last_error()
+    assert lib.muon_layernorm_workspace_size(d) == 0
+    assert lib.muon_layernorm_backward(d, P, P, P, P, P, 2 * P, P, P, P, 1 << 40, None) == code
+
+
+def test_layer_norm_refuses_pointers(lib):
+    d = ctypes.byref(norm_desc())
+    fwd, bwd = lib.muon_layernorm_forward, lib.muon_layernorm_backward
+    assert fwd(None, P, P, P, 2 * P, P, P, None) == INVAL
+    good = [P, P, P, 2 * P, P, P]
+    for i, bad in ((0, None), (3, None), (4, None), (5, None), (3, P), (0, P + 1), (1, P + 2), (2, P + 2),
+                   (3, 2 * P + 1), (4, P + 2), (5, P + 1)):
+        args = list(good)
+        args[i] = bad
+        assert fwd(d, *args, None) == INVAL, (i, bad)
+    need = lib.muon_layernorm_workspace_size(d)
+    good = [P, P, P, P, P, 2 * P, P, P, P, need]
+    for i, bad, code in ((0, None, INVAL), (1, None, INVAL), (3, None, INVAL), (4, None, INVAL), (5, P, INVAL),
+                         (0, P + 1, INVAL), (1, P + 1, INVAL), (2, P + 2, INVAL), (5, 2 * P + 1, INVAL),
+                         (6, P + 2, INVAL), (7, P + 2, INVAL), (8, None, WORK), (8, P + 64, WORK), (9, 0, WORK),
+                         (9, need // 4, WORK)):
+        args = list(good)
+        args[i] = bad
+        assert bwd(d, *args, None) == code, (i, bad)
+    assert bwd(d, P, P, P, P, P, None, None, None, P, need, None) == INVAL  # nothing wanted
+    # no rows: nothing is launched, and no pointer is needed
+    assert fwd(ctypes.byref(norm_desc(rows=0)), None, None, None, None, None, None, None) == 0
+
+
+def test_layer_norm_workspace_covers_every_kernel(lib):
+    """One row of 2 cols sums for each block; a block holds at least a row, and at most 1024 run."""
+    for rows in (0, 1, 5, 1023, 1024, 5000, 1 << 33):
+        for cols in (1, 64, 1001, 1 << 20):
+            need = lib.muon_layernorm_workspace_size(ctypes.byref(norm_desc(rows=rows, cols=cols)))
+            assert need >= max(min(rows, 1024) * 2 * cols * 4, 1)
+            assert need <= min(rows, 1024) * 2 * cols * 4 + 1024
+
+
+def attn_desc(**kw):
+    d = dict(tokens=100, seqs=2, q_heads=4, kv_heads=2, head_dim=64, dtype=1, scale=0.125, reserved=0)
+    d.update(kw)
+    return AttentionDesc(*d.values())
+
+
+def heads(n=4, base=P, dim=64, **kw):
+    return Heads(kw.get("data", base), kw.get("token", n * dim), kw.get("head", dim))
+
+
+BAD_ATTN = [(dict(tokens=-1), INVAL), (dict(tokens=1 << 31), INVAL), (dict(seqs=-1), INVAL),
+            (dict(seqs=(1 << 24) + 1), INVAL), (dict(q_heads=0), INVAL), (dict(kv_heads=0), INVAL),
+            (dict(kv_heads=3), INVAL), (dict(q_heads=2, kv_heads=4), INVAL), (dict(q_heads=1 << 17), INVAL),
+            (dict(head_dim=0), UNSUP), (dict(head_dim=-8), UNSUP), (dict(head_dim=68), UNSUP),
+            (dict(head_dim=136), UNSUP), (dict(dtype=2), UNSUP), (dict(scale=0.0), INVAL), (dict(scale=-1.0), INVAL),
+            (dict(scale=math.nan), INVAL), (dict(scale=math.inf), INVAL), (dict(reserved=7), INVAL),
+            (dict(tokens=1 << 30, q_heads=1 << 14, kv_heads=1 << 14), UNSUP)]
+
+
+def attn_call(lib, d, back, flags=0, cu=P, lse=P, ws=P, ws_bytes=1 << 40, **over):
+    h = {n: heads(2 if n in ("k", "v", "dk", "dv") else 4, P * (i + 1)) for i, n in
+         enumerate(("q", "k", "v", "out", "dout", "dq", "dk", "dv"))}
+    h.update(over)
+    r = {n: None if v is None else ctypes.byref(v) for n, v in h.items()}
+    if back:
+        return lib.muon_attention_backward(ctypes.byref(d), cu, r["dout"], r["q"], r["k"], r["v"], r["out"], lse,
+                                           r["dq"], r["dk"], r["dv"], flags, ws, ws_bytes, None)
+    return lib.muon_attention_forward(ctypes.byref(d), cu, r["q"], r["k"], r["v"], r["out"], lse, flags, None)
+
+
+@pytest.mark.parametrize("kw,code", BAD_ATTN, ids=str)
+def test_attention_refuses_descriptors(lib, kw, code):
+    d = attn_desc(**kw)
+    assert attn_call(lib, d, False) == code
+    assert attn_call(lib, d, True) == code
+    assert _lib.last_error()
+    assert lib.muon_attention_workspace_size(ctypes.byref(d)) == 0
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_attention_refuses_operands(lib, back):
+    d = attn_desc()
+    assert attn_call(lib, d, back, cu=None) == INVAL
+    assert attn_call(lib, d, back, cu=P + 2) == INVAL
+    assert attn_call(lib, d, back, lse=None) == INVAL
+    assert attn_call(lib, d, back, lse=P + 1) == INVAL
+    assert attn_call(lib, d, back, flags=8) == INVAL
+    names = ("q", "k", "v", "out") + (("dout", "dq", "dk", "dv") if back else ())
+    for n in names:
+        w = 2 if n in ("k", "v", "dk", "dv") else 4
+        for bad, code in ((None, INVAL), (heads(w, data=None), INVAL), (heads(w, data=P + 8), UNSUP),
+                          (heads(w, token=w * 64 + 4), UNSUP), (heads(w, head=68), UNSUP),
+                          (heads(w, token=-64), INVAL), (heads(w, head=-64), INVAL),
+                          (heads(w, token=(1 << 31) + 8), INVAL)):
+            assert attn_call(lib, d, back, **{n: bad}) == code, (n, bad)
+    for n in (("dq", "dk", "dv") if back else ("out",)):  # rows of an output must not overlap
+        w = 2 if n in ("dk", "dv") else 4
+        for bad in (heads(w, token=64), heads(w, head=0), heads(w, token=0), heads(w, head=32, token=4096)):
+            assert attn_call(lib, d, back, **{n: bad}) == INVAL, n
+    if not back:
+        for n in ("q", "k", "v"):
+            assert attn_call(lib, d, False, out=heads(4, P * (1 + "qkv".index(n)))) == INVAL
+        return
+    for n in ("q", "dq"):
+        assert attn_call(lib, d, True, dk=heads(2, P * (1 if n == "q" else 6))) == INVAL
+    need = lib.muon_attention_workspace_size(ctypes.byref(d))
+    assert attn_call(lib, d, True, ws=None) == WORK
+    assert attn_call(lib, d, True, ws=P + 128) == WORK
+    assert attn_call(lib, d, True, ws_bytes=need // 2) == WORK
+
+
+def test_attention_without_tokens_needs_nothing(lib):
+    d = attn_desc(tokens=0, seqs=0)
+    assert attn_call(lib, d, False, cu=None, lse=None, q=None, out=None) == 0
+    assert attn_call(lib, d, True, cu=None, lse=None, dq=None, ws=None, ws_bytes=0) == 0
+
+
+def test_attention_workspace_holds_delta(lib):
+    for tokens in (1, 1000, 1 << 20):
+        for q, kv in ((12, 12), (16, 4), (32, 1)):
+            need = lib.muon_attention_workspace_size(ctypes.byref(attn_desc(tokens=tokens, q_heads=q, kv_heads=kv)))
+            assert need >= q * tokens * 4
+            assert need <= q * tokens * 4 + q * tokens * 2 * 64 * 4 + 1024  # and at most one partial per query head
+
+
+def test_binding_refuses_tensors_before_any_call():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="device tensor"):
+        block.layer_norm_forward(x)
+    with pytest.raises(ValueError, match="device tensor"):
+        block.layer_norm_backward(x, x, x[:, 0], x[:, 0])
+    q = torch.zeros(4, 2, 8)
+    with pytest.raises(ValueError, match="device tensor"):
+        block.packed_attention_forward(q, q, q, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="device tensor"):
+        block.packed_attention_backward(q, q, q, q, q, q, torch.zeros(2, dtype=torch.int32))
+    rows = block._rows
+    assert rows(torch.zeros(3, 4, 8), "x") == (12, 8, 8)
+    assert rows(torch.zeros(6, 20)[:, :8], "x") == (6, 8, 20)
+    assert rows(torch.zeros(1, 1, 8), "x") == (1, 8, 8)
+    assert rows(torch.zeros(8), "x") == (1, 8, 8)
+    assert rows(torch.zeros(0, 8), "x")[:2] == (0, 8)
+    for bad in (torch.zeros(8, 3).t(), torch.zeros(3, 5, 8).transpose(0, 1), torch.zeros(1, 8).expand(4, 8),
+                torch.tensor(1.0)):
+        with pytest.raises(ValueError):
+            rows(bad, "x")
+
+
+# ------------------------------------------------- the reference's own pins --
+def test_reference_gradients_against_differences():
+    """The fp64 formulas' gradients equal autograd's, and central differences, on the CPU."""
+    torch.manual_seed(0)
+    lengths, H, G, D = [5, 0, 1, 9], 4, 2, 8
+    T = sum(lengths)
+    q, k, v, do = (torch.randn(T, n, D, dtype=torch.float64) for n in (H, G, G, H))
+    ref = R.attention(q, k, v, lengths, 0.3, do, dtype=torch.float32)
+
+    def loss(q, k, v):
+        return (R.attention(q, k, v, lengths, 0.3)["out"][0] * do).sum()
+
+    for name, i in (("dq", 0), ("dk", 1), ("dv", 2)):
+        args = [q, k, v]
+        d = torch.randn_like(args[i])
+        h = 1e-5
+        lo, hi = list(args), list(args)
+        lo[i], hi[i] = args[i] - h * d, args[i] + h * d
+        assert abs((loss(*hi) - loss(*lo)) / (2 * h) - (ref[name][0] * d).sum()) < 1e-8
+    x, w, b, dy = torch.randn(6, 10).double(), torch.randn(10).double(), torch.randn(10).double(), torch.randn(6, 10).double()
+    for t in (x, w, b):
+        t.requires_grad_(True)
+    (torch.nn.functional.layer_norm(x, (10,), w, b, 1e-5) * dy).sum().backward()
+    for got, t in zip(R.norm_backward(dy, x.detach(), w.detach(), 1e-5), (x, w, b)):
+        assert (got - t.grad).abs().max() < 1e-12
+
+
+def test_reference_check_sees_a_wrong_value():
+    """A mistake planted in the reference is outside the bounds (a sequence border one token off, a wrong group)."""
+    torch.manual_seed(1)
+    q, k, v = (torch.randn(40, n, 16) for n in (4, 2, 2))
+    good = R.attention(q, k, v, [17, 23], 0.25, q, dtype=torch.bfloat16)
+    for other in (R.attention(q, k, v, [18, 22], 0.25, q), R.attention(q, k.flip(1), v, [17, 23], 0.25, q),
+                  R.attention(q, k, v, [17, 23], 0.26, q)):
+        for name in ("out", "lse", "dq", "dk", "dv"):
+            with pytest.raises(AssertionError):
+                R.check(name, other[name][0], *good[name])
