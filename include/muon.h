@@ -364,8 +364,8 @@ typedef struct muon_attention_desc {
 } muon_attention_desc;
 
 /* One (tokens, heads, head_dim) operand: strides in elements, head_dim
- * contiguous.  data and both strides must be multiples of 16 bytes.  Inputs
- * may overlap or repeat (slices of one projection, stride 0); the rows of an
+ * contiguous.  data and both strides must be multiples of 16 bytes, and
+ * token_stride at most 2^24 elements, head_stride 2^31.  Inputs may overlap or repeat (slices of one projection, stride 0); the rows of an
  * output must not overlap. */
 typedef struct muon_heads {
   void* data;

@@ -119,23 +119,39 @@ struct Tiles {
   }
 };
 
-// Moves ROWS rows of one head from global memory to an LDS tile through
-// registers: load() requests them, store() writes them (rows at or past
-// `end` and elements at or past the head dimension as zeros).
+// Moves tiles of ROWS rows of one head from global memory to LDS through
+// registers: load() requests a tile, store() writes it.  Buffer loads return
+// zeros past the end of their resource, which covers the tile's rows inside
+// the sequence; a chunk past the head dimension gets an offset beyond every
+// resource.
+constexpr uint32_t kOob = 0x80000000u;
 template <class T, int DP, int ROWS>
 struct Stager {
   static constexpr int kN = ROWS * DP * (int)sizeof(T) / 16 / kThreads;
   static_assert(kN * kThreads * 16 == ROWS * DP * (int)sizeof(T), "whole chunks per thread");
+  const char* base;   // the sequence's first row of this head
+  int64_t step;       // bytes from row to row
+  int len, row_bytes;
+  uint32_t off[kN];
   u32x4 buf[kN];
-  __device__ __forceinline__ void load(const T* head, int64_t token_stride, int row0, int end, int dim, int tid) {
+  __device__ __forceinline__ void init(const HeadView& v, int head, const AttnArgs& a, int start, int seq_len,
+                                       int tid) {
     constexpr int cpr = Tiles<T, DP>::kCpr;
-    constexpr int epc = 16 / (int)sizeof(T);
+    base = (const char*)((const T*)v.data + start * v.token + head * v.head);
+    step = v.token * (int64_t)sizeof(T);
+    len = seq_len;
+    row_bytes = a.dim * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int idx = i * kThreads + tid, row = row0 + idx / cpr, c = idx % cpr;
-      buf[i] = u32x4{0, 0, 0, 0};
-      if (row < end && c * epc < dim) buf[i] = *gv<u32x4>(head + row * token_stride + c * epc);
+      const int idx = i * kThreads + tid, row = idx / cpr, c = idx % cpr;
+      off[i] = c * 16 < row_bytes ? (uint32_t)(row * step) + 16u * c : kOob;
     }
+  }
+  __device__ __forceinline__ void load(int row0) {
+    const int rows = min(len - row0, ROWS);
+    const rsrc_t rs = make_rsrc(base + row0 * step, rows > 0 ? (uint32_t)((rows - 1) * step) + row_bytes : 0u);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) buf[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off[i], 0, 0);
   }
   __device__ __forceinline__ void store(char* tile, int tid) const {
     constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
@@ -229,6 +245,77 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int slot, int bm
 }
 inline int64_t slots_of(int64_t tokens, int seqs, int bm) { return tokens / bm + seqs + 1; }
 
+// The tile of a block in order of decreasing work, for up to kRankSeqs
+// sequences: tile `t` of a sequence looks at t + 1 tiles of keys, so the tiles
+// of equal work w are one of each sequence of at least w tiles, and
+// N(w) = sum over sequences of max(0, tiles - w + 1) tiles have work w or
+// more.  Every wave keeps the sequences' tile counts in its lanes, finds the
+// largest w with N(w) > rank, and in that level the sequence.  (Backward, the
+// keys of tile t are looked at by tiles - t tiles of queries.)
+constexpr int kRankSeqs = 256;
+__device__ __forceinline__ int wave_sum(int x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return __builtin_amdgcn_readfirstlane(x);
+}
+__device__ __forceinline__ SeqTile ranked_tile(const AttnArgs& a, int rank, int bm, int lane, bool keys) {
+  constexpr int kC = kRankSeqs / 64;
+  int nt[kC], most = 0, all = 0;
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    const int i = 64 * c + lane;
+    nt[c] = i < a.seqs ? (max(token_at(a, i + 1) - token_at(a, i), 0) + bm - 1) / bm : 0;
+    most = max(most, nt[c]);
+    all += nt[c];
+  }
+  SeqTile t;
+  all = wave_sum(all);
+  if (rank >= all) {
+    t.tail = true;
+    t.start = token_at(a, a.seqs);
+    t.len = (int)a.tokens - t.start;
+    t.row0 = rank - all < (t.len + bm - 1) / bm ? (rank - all) * bm : t.len;
+    return t;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o));
+  int lo = 1, hi = __builtin_amdgcn_readfirstlane(most) + 1, above = 0;  // N(lo) > rank >= N(hi) = above
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) n += max(nt[c] - mid + 1, 0);
+    n = wave_sum(n);
+    if (n > rank) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = n;
+    }
+  }
+  int j = rank - above, seq = 0;  // the j-th sequence of at least lo tiles
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    const uint64_t m = __ballot(nt[c] >= lo);
+    const uint64_t before = m & ((1ull << lane) - 1);
+    const uint64_t hit = __ballot(((m >> lane) & 1) && __popcll(before) == j);
+    if (j >= 0 && hit) seq = 64 * c + __ffsll((unsigned long long)hit) - 1;
+    j -= __popcll(m);
+    if (j < 0) j = -0x40000000;
+  }
+  t.tail = false;
+  t.start = token_at(a, seq);
+  t.len = max(token_at(a, seq + 1) - t.start, 0);
+  t.row0 = (keys ? (t.len + bm - 1) / bm - lo : lo - 1) * bm;
+  return t;
+}
+// Block `i` of `n` along the tiles: heaviest first.  With more sequences than
+// that, each is short beside the whole, and the slots are taken backwards
+// (forwards for keys), heaviest first within a sequence.
+__device__ __forceinline__ SeqTile block_tile(const AttnArgs& a, int i, int n, int bm, int lane, bool keys) {
+  return a.seqs <= kRankSeqs ? ranked_tile(a, i, bm, lane, keys) : find_tile(a, keys ? i : n - 1 - i, bm, lane);
+}
+
 template <class T>
 __device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0, int rows, int dim, int tid) {
   const int dw = dim * (int)sizeof(T) / 16;
@@ -251,10 +338,11 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
   constexpr int BM = 128, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[2][2][kTile];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, col = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
-  const int slot = (int)(gridDim.x / a.q_heads) - 1 - (int)(blockIdx.x / a.q_heads);
-  const SeqTile st = find_tile(a, slot, BM, lane);
+  const SeqTile st =
+      block_tile(a, (int)(blockIdx.x / a.q_heads), (int)(gridDim.x / a.q_heads), BM, lane, false);
   if (st.row0 >= st.len) return;
   if (st.tail) {
     const int rows = min(BM, st.len - st.row0), r0 = st.start + st.row0;
@@ -262,8 +350,6 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
     if ((a.zero_tail & kZeroLse) && tid < rows) a.lse[(int64_t)head * a.tokens + r0 + tid] = 0.f;
     return;
   }
-  const T* kp = (const T*)a.k.data + (int64_t)st.start * a.k.token + kvh * a.k.head;
-  const T* vp = (const T*)a.v.data + (int64_t)st.start * a.v.token + kvh * a.v.head;
   const int qw = st.row0 + 32 * w, qi = qw + col;
   const int wend = qw < st.len ? min(st.len, qw + 32) : 0;  // keys this wave looks at
   const int ntile = (min(st.len, st.row0 + BM) + KT - 1) / KT;
@@ -278,8 +364,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
   float m = -__builtin_inff(), l = 0.f;
 
   Stager<T, DP, KT> sk, sv;
-  sk.load(kp, a.k.token, 0, st.len, a.dim, tid);
-  sv.load(vp, a.v.token, 0, st.len, a.dim, tid);
+  sk.init(a.k, kvh, a, st.start, st.len, tid);
+  sv.init(a.v, kvh, a, st.start, st.len, tid);
+  sk.load(0);
+  sv.load(0);
   sk.store(lds[0][0], tid);
   sv.store(lds[0][1], tid);
   __syncthreads();
@@ -287,8 +375,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
     const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
     const bool more = kt + 1 < ntile;
     if (more) {
-      sk.load(kp, a.k.token, (kt + 1) * KT, st.len, a.dim, tid);
-      sv.load(vp, a.v.token, (kt + 1) * KT, st.len, a.dim, tid);
+      sk.load((kt + 1) * KT);
+      sv.load((kt + 1) * KT);
     }
     if (kt * KT < wend) {
       f32x16 s[MT];
@@ -362,18 +450,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   constexpr int BM = 128, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[2][2][kTile];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, col = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
-  const int slot = (int)(gridDim.x / a.q_heads) - 1 - (int)(blockIdx.x / a.q_heads);
-  const SeqTile st = find_tile(a, slot, BM, lane);
+  const SeqTile st =
+      block_tile(a, (int)(blockIdx.x / a.q_heads), (int)(gridDim.x / a.q_heads), BM, lane, false);
   if (st.row0 >= st.len) return;
   if (st.tail) {
     if (a.zero_tail & kZeroDq)
       zero_rows<T>(a.dq, head, st.start + st.row0, min(BM, st.len - st.row0), a.dim, tid);
     return;
   }
-  const T* kp = (const T*)a.k.data + (int64_t)st.start * a.k.token + kvh * a.k.head;
-  const T* vp = (const T*)a.v.data + (int64_t)st.start * a.v.token + kvh * a.v.head;
   const int qw = st.row0 + 32 * w, qi = qw + col;
   const int wend = qw < st.len ? min(st.len, qw + 32) : 0;
   const int ntile = (min(st.len, st.row0 + BM) + KT - 1) / KT;
@@ -407,8 +494,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
 
   Stager<T, DP, KT> sk, sv;
-  sk.load(kp, a.k.token, 0, st.len, a.dim, tid);
-  sv.load(vp, a.v.token, 0, st.len, a.dim, tid);
+  sk.init(a.k, kvh, a, st.start, st.len, tid);
+  sv.init(a.v, kvh, a, st.start, st.len, tid);
+  sk.load(0);
+  sv.load(0);
   sk.store(lds[0][0], tid);
   sv.store(lds[0][1], tid);
   __syncthreads();
@@ -416,8 +505,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
     const bool more = kt + 1 < ntile;
     if (more) {
-      sk.load(kp, a.k.token, (kt + 1) * KT, st.len, a.dim, tid);
-      sv.load(vp, a.v.token, (kt + 1) * KT, st.len, a.dim, tid);
+      sk.load((kt + 1) * KT);
+      sv.load((kt + 1) * KT);
     }
     if (kt * KT < wend) {
 #pragma unroll
@@ -463,10 +552,11 @@ __global__ __launch_bounds__(kThreads, DP * sizeof(T) <= 128 ? 2 : 1) void atten
   constexpr int kTile = QR * Tl::kRow;
   __shared__ __align__(256) char lds[2][2][kTile];
   __shared__ __align__(16) float stat[2][2][QR];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, h = lane >> 5, col = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int per = a.kv_heads * a.splits;
   const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
-  const SeqTile st = find_tile(a, (int)(blockIdx.x / per), BN, lane);
+  const SeqTile st = block_tile(a, (int)(blockIdx.x / per), (int)(gridDim.x / per), BN, lane, true);
   if (st.row0 >= st.len) return;
   if (st.tail) {
     const int rows = min(BN, st.len - st.row0), r0 = st.start + st.row0;
@@ -492,9 +582,12 @@ __global__ __launch_bounds__(kThreads, DP * sizeof(T) <= 128 ? 2 : 1) void atten
   float sl = 0.f, sdl = 0.f;
   auto load = [&](int it) {
     const int head = head0 + it / nq, row0 = (qt0 + it % nq) * QR;
-    sq.load((const T*)a.q.data + (int64_t)st.start * a.q.token + head * a.q.head, a.q.token, row0, st.len, a.dim, tid);
-    sd.load((const T*)a.dout.data + (int64_t)st.start * a.dout.token + head * a.dout.head, a.dout.token, row0, st.len,
-            a.dim, tid);
+    if (it % nq == 0) {
+      sq.init(a.q, head, a, st.start, st.len, tid);
+      sd.init(a.dout, head, a, st.start, st.len, tid);
+    }
+    sq.load(row0);
+    sd.load(row0);
     if (tid < QR) {
       const bool in = row0 + tid < st.len;
       const int64_t at = (int64_t)head * a.tokens + st.start + row0 + tid;

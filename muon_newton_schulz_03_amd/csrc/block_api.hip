@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kMaxCols = 1 << 20;
 constexpr int64_t kMaxRows = (int64_t)1 << 40;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
+constexpr int64_t kMaxTokenStride = 1 << 24;  // a 64-row tile stays within 32-bit byte offsets
 constexpr int64_t kMaxTokens = 0x7FFFFF00;
 constexpr int kMaxSeqs = 1 << 24;
 constexpr int kMaxHeads = 1 << 16;
@@ -85,9 +86,9 @@ int check_heads(const muon_attention_desc* d, const muon_heads* v, const char* n
   const int es = elem_size(d->dtype);
   // a stride that no address uses does not matter
   const int64_t token = d->tokens > 1 ? v->token_stride : 0, head = heads > 1 ? v->head_stride : 0;
-  if (token < 0 || head < 0 || token > kMaxStride || head > kMaxStride)
-    return fail(MUON_E_INVAL, "attention: %s: strides %lld, %lld outside [0, 2^31]", name, (long long)token,
-                (long long)head);
+  if (token < 0 || head < 0 || token > kMaxTokenStride || head > kMaxStride)
+    return fail(MUON_E_INVAL, "attention: %s: strides %lld, %lld outside [0, 2^24] and [0, 2^31]", name,
+                (long long)token, (long long)head);
   if (misaligned(v->data, 16) || token * es % 16 || head * es % 16)
     return fail(MUON_E_UNSUPPORTED, "attention: %s must start, and step from token to token and head to head, at "
                 "multiples of 16 bytes", name);

@@ -133,7 +133,7 @@ def test_attention_refuses_operands(lib, back):
         for bad, code in ((None, INVAL), (heads(w, data=None), INVAL), (heads(w, data=P + 8), UNSUP),
                           (heads(w, token=w * 64 + 4), UNSUP), (heads(w, head=68), UNSUP),
                           (heads(w, token=-64), INVAL), (heads(w, head=-64), INVAL),
-                          (heads(w, token=(1 << 31) + 8), INVAL)):
+                          (heads(w, token=(1 << 24) + 8), INVAL), (heads(w, head=(1 << 31) + 8), INVAL)):
             assert attn_call(lib, d, back, **{n: bad}) == code, (n, bad)
     for n in (("dq", "dk", "dv") if back else ("out",)):  # rows of an output must not overlap
         w = 2 if n in ("dk", "dv") else 4
