@@ -119,47 +119,118 @@ struct Tiles {
   }
 };
 
-// Moves tiles of ROWS rows of one head from global memory to LDS through
-// registers: load() requests a tile, store() writes it.  Buffer loads return
-// zeros past the end of their resource, which covers the tile's rows inside
-// the sequence; a chunk past the head dimension gets an offset beyond every
-// resource.
+// Copies tiles of ROWS rows of one head from global memory straight to LDS.
+// Each wave instruction writes 64 x 16 contiguous bytes of the tile, and the
+// swizzle is applied by choosing which chunk each lane fetches.  The buffer
+// resource covers the tile's rows inside the sequence, past which loads return
+// zeros; a chunk past the head dimension gets an offset beyond every resource.
+//
+// The instruction is written in assembly because the compiler, which sees a
+// builtin's LDS write, waits for it before every later LDS read of either
+// buffer.  It has no register outputs; wait_tiles() waits for it.  (m0, which
+// holds the LDS address, is reserved: the compiler keeps nothing in it.)
 constexpr uint32_t kOob = 0x80000000u;
+__device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {  // uniform arguments
+  const uint64_t p = (uint64_t)base;
+  auto word = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); };
+  return u32x4{word((uint32_t)p), word((uint32_t)(p >> 32) & 0xFFFFu), word(bytes), 0x00020000u};
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)p);
+}
+__device__ __forceinline__ void dma_b128(u32x4 rs, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(rs) : "memory");
+}
+__device__ __forceinline__ void dma_b32(u32x4 rs, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(rs) : "memory");
+}
+// Waits for this wave's copies, then for the block's other waves: the tiles
+// copied since the last call can be read, and those read before it written.
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The same with the wave's last N copies still in flight, and its LDS reads.
+template <int N>
+__device__ __forceinline__ void wait_but() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 template <class T, int DP, int ROWS>
-struct Stager {
-  static constexpr int kN = ROWS * DP * (int)sizeof(T) / 16 / kThreads;
-  static_assert(kN * kThreads * 16 == ROWS * DP * (int)sizeof(T), "whole chunks per thread");
+struct Copier {
+  static constexpr int kN = ROWS * DP * (int)sizeof(T) / 1024 / (kThreads / 64);
+  static_assert(kN * kThreads * 16 == ROWS * DP * (int)sizeof(T), "whole instructions per wave");
   const char* base;   // the sequence's first row of this head
   int64_t step;       // bytes from row to row
   int len, row_bytes;
   uint32_t off[kN];
-  u32x4 buf[kN];
-  __device__ __forceinline__ void init(const HeadView& v, int head, const AttnArgs& a, int start, int seq_len,
-                                       int tid) {
-    constexpr int cpr = Tiles<T, DP>::kCpr;
-    base = (const char*)((const T*)v.data + start * v.token + head * v.head);
+  __device__ __forceinline__ void init(const HeadView& v, int head, const AttnArgs& a, int start, int seq_len, int w,
+                                       int lane) {
+    constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
+    seek(v, head, start);
     step = v.token * (int64_t)sizeof(T);
     len = seq_len;
     row_bytes = a.dim * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int idx = i * kThreads + tid, row = idx / cpr, c = idx % cpr;
+      const int idx = (w * kN + i) * 64 + lane, row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
       off[i] = c * 16 < row_bytes ? (uint32_t)(row * step) + 16u * c : kOob;
     }
   }
-  __device__ __forceinline__ void load(int row0) {
-    const int rows = min(len - row0, ROWS);
-    const rsrc_t rs = make_rsrc(base + row0 * step, rows > 0 ? (uint32_t)((rows - 1) * step) + row_bytes : 0u);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) buf[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off[i], 0, 0);
+  __device__ __forceinline__ void seek(const HeadView& v, int head, int start) {
+    base = (const char*)((const T*)v.data + start * v.token + head * v.head);
   }
-  __device__ __forceinline__ void store(char* tile, int tid) const {
+  __device__ __forceinline__ void copy(char* tile, int row0, int w, int lane) const {
+    const int rows = min(len - row0, ROWS);
+    const u32x4 rs = buffer_of(base + row0 * step, rows > 0 ? (uint32_t)((rows - 1) * step) + row_bytes : 0u);
+    if (rows == ROWS) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) dma_b128(rs, lds_offset(tile + (w * kN + i) * 1024), off[i]);
+    } else {  // rows may overlap (a step of 0 repeats one), so the resource's end alone does not tell them apart
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        dma_b128(rs, lds_offset(tile + (w * kN + i) * 1024),
+                 ((w * kN + i) * 64 + lane) / Tiles<T, DP>::kCpr < rows ? off[i] : kOob);
+    }
+  }
+};
+
+// One slot of a ring: ROWS rows of two operands (at 0 and kHalf), and two fp32
+// words a row (at 2 kHalf, 64 floats each).  The wave instructions are dealt
+// out evenly, kN of them to every wave, so that waits can count them.
+template <class T, int DP, int ROWS>
+struct PairCopier {
+  static constexpr int kHalf = ROWS * DP * (int)sizeof(T), kSlot = 2 * kHalf + 512;
+  static constexpr int kTileN = 2 * kHalf / 1024 / (kThreads / 64), kN = kTileN + 1;
+  static_assert(kTileN * kThreads * 16 == 2 * kHalf && ROWS <= 64, "whole instructions per wave");
+  uint32_t off[kTileN];
+  __device__ __forceinline__ void init(int64_t step0, int64_t step1, int row_bytes, int w, int lane) {
     constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int idx = i * kThreads + tid, row = idx / cpr, c = idx % cpr;
-      *(u32x4*)(tile + row * kRow + ((c ^ swz<kRow>(row)) << 4)) = buf[i];
+    for (int i = 0; i < kTileN; ++i) {
+      const int n = w * kTileN + i, idx = n * 64 + lane - (n * 1024 >= kHalf ? kHalf / 16 : 0);
+      const int row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
+      off[i] = c * 16 < row_bytes ? (uint32_t)(row * (n * 1024 >= kHalf ? step1 : step0)) + 16u * c : kOob;
     }
+  }
+  // `rows` rows from p0 and p1 (0: a slot of zeros), and their words from s0 and s1.
+  __device__ __forceinline__ void copy(char* slot, const char* p0, int64_t step0, const char* p1, int64_t step1,
+                                       const float* s0, const float* s1, int rows, int row_bytes, int w,
+                                       int lane) const {
+    rows = rows < 0 ? 0 : min(rows, ROWS);
+    const uint32_t n0 = rows > 0 ? (uint32_t)((rows - 1) * step0) + row_bytes : 0u;
+    const uint32_t n1 = rows > 0 ? (uint32_t)((rows - 1) * step1) + row_bytes : 0u;
+#pragma unroll
+    for (int i = 0; i < kTileN; ++i) {
+      const int n = w * kTileN + i;
+      const bool second = n * 1024 >= kHalf;
+      uint32_t o = off[i];
+      if (rows < ROWS && (n * 64 + lane - (second ? kHalf / 16 : 0)) / Tiles<T, DP>::kCpr >= rows) o = kOob;
+      dma_b128(second ? buffer_of(p1, n1) : buffer_of(p0, n0), lds_offset(slot + n * 1024), o);
+    }
+    dma_b32(buffer_of(w & 1 ? s1 : s0, 4 * rows), lds_offset(slot + 2 * kHalf + 256 * (w & 1)), 4 * lane);
   }
 };
 
@@ -326,16 +397,16 @@ __device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0,
 }
 
 // ----------------------------------------------------------------- forward --
-template <class T>
+template <class T, int DP>
 struct Cfg {
-  static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
+  static constexpr int kKeys = sizeof(T) == 2 ? (DP > 96 ? 64 : 64) : 32;  // rows of a streamed tile
 };
 
 template <class T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BM = 128, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BM = 128, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[2][2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
@@ -363,20 +434,17 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
   for (int t = 0; t < DT; ++t) o[t] = f32x16{};
   float m = -__builtin_inff(), l = 0.f;
 
-  Stager<T, DP, KT> sk, sv;
-  sk.init(a.k, kvh, a, st.start, st.len, tid);
-  sv.init(a.v, kvh, a, st.start, st.len, tid);
-  sk.load(0);
-  sv.load(0);
-  sk.store(lds[0][0], tid);
-  sv.store(lds[0][1], tid);
-  __syncthreads();
+  Copier<T, DP, KT> ck, cv;
+  ck.init(a.k, kvh, a, st.start, st.len, w, lane);
+  cv.init(a.v, kvh, a, st.start, st.len, w, lane);
+  ck.copy(lds[0][0], 0, w, lane);
+  cv.copy(lds[0][1], 0, w, lane);
+  wait_tiles();
   for (int kt = 0; kt < ntile; ++kt) {
     const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
-    const bool more = kt + 1 < ntile;
-    if (more) {
-      sk.load((kt + 1) * KT);
-      sv.load((kt + 1) * KT);
+    if (kt + 1 < ntile) {
+      ck.copy(lds[(kt + 1) & 1][0], (kt + 1) * KT, w, lane);
+      cv.copy(lds[(kt + 1) & 1][1], (kt + 1) * KT, w, lane);
     }
     if (kt * KT < wend) {
       f32x16 s[MT];
@@ -427,11 +495,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
         }
       }
     }
-    if (more) {
-      sk.store(lds[(kt + 1) & 1][0], tid);
-      sv.store(lds[(kt + 1) & 1][1], tid);
-    }
-    __syncthreads();
+    wait_tiles();
   }
   l = halves_sum(l);
   if (qi < st.len) {
@@ -442,12 +506,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
 }
 
 // ---------------------------------------------------------------- backward --
-// dQ, and delta for the next kernel.
+// dQ; and for the next kernel delta and lse: in fp32, delta and lse / log 2;
+// in bf16, -delta and -lse / scale, from which it starts its products' sums.
 template <class T, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BM = 128, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BM = 128, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[2][2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
@@ -486,27 +551,28 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     delta = halves_sum(delta);
     if (valid) {
       lse2 = a.lse[(int64_t)head * a.tokens + tok] * kLog2e;
-      if (h == 0) a.delta[(int64_t)head * a.tokens + tok] = delta;
+      if (h == 0) {
+        const int64_t at = (int64_t)head * a.tokens + tok;
+        a.delta[at] = sizeof(T) == 2 ? -delta : delta;
+        a.lse2[at] = sizeof(T) == 2 ? -a.lse[at] / a.scale : lse2;
+      }
     }
   }
   f32x16 dq[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
 
-  Stager<T, DP, KT> sk, sv;
-  sk.init(a.k, kvh, a, st.start, st.len, tid);
-  sv.init(a.v, kvh, a, st.start, st.len, tid);
-  sk.load(0);
-  sv.load(0);
-  sk.store(lds[0][0], tid);
-  sv.store(lds[0][1], tid);
-  __syncthreads();
+  Copier<T, DP, KT> ck, cv;
+  ck.init(a.k, kvh, a, st.start, st.len, w, lane);
+  cv.init(a.v, kvh, a, st.start, st.len, w, lane);
+  ck.copy(lds[0][0], 0, w, lane);
+  cv.copy(lds[0][1], 0, w, lane);
+  wait_tiles();
   for (int kt = 0; kt < ntile; ++kt) {
     const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
-    const bool more = kt + 1 < ntile;
-    if (more) {
-      sk.load((kt + 1) * KT);
-      sv.load((kt + 1) * KT);
+    if (kt + 1 < ntile) {
+      ck.copy(lds[(kt + 1) & 1][0], (kt + 1) * KT, w, lane);
+      cv.copy(lds[(kt + 1) & 1][1], (kt + 1) * KT, w, lane);
     }
     if (kt * KT < wend) {
 #pragma unroll
@@ -533,25 +599,22 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
         }
       }
     }
-    if (more) {
-      sk.store(lds[(kt + 1) & 1][0], tid);
-      sv.store(lds[(kt + 1) & 1][1], tid);
-    }
-    __syncthreads();
+    wait_tiles();
   }
   if (valid) store_row<T, DP>((T*)a.dq.data + tok * a.dq.token + head * a.dq.head, dq, a.scale, a.dim, h);
 }
 
 // dK and dV of 128 keys of one key/value head, over the query heads of its
-// group (or of one part of it) and the query rows from the keys on.
-template <class T, int DP>
-__global__ __launch_bounds__(kThreads, DP * sizeof(T) <= 128 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
+// group (or of one part of it) and the query rows from the keys on, in fp32.
+template <int DP>
+__global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
+  typedef float T;
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BN = 128, QR = Cfg<T>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BN = 128, QR = Cfg<T, DP>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = QR * Tl::kRow;
   __shared__ __align__(256) char lds[2][2][kTile];
-  __shared__ __align__(16) float stat[2][2][QR];
+  __shared__ __align__(256) float stat[2][2][64];  // lse2 and delta of the tile's rows
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int per = a.kv_heads * a.splits;
@@ -578,36 +641,27 @@ __global__ __launch_bounds__(kThreads, DP * sizeof(T) <= 128 ? 2 : 1) void atten
   for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
 
   const int qt0 = st.row0 / QR, nq = (st.len + QR - 1) / QR - qt0, total = nq * hpp;
-  Stager<T, DP, QR> sq, sd;
-  float sl = 0.f, sdl = 0.f;
-  auto load = [&](int it) {
-    const int head = head0 + it / nq, row0 = (qt0 + it % nq) * QR;
-    if (it % nq == 0) {
-      sq.init(a.q, head, a, st.start, st.len, tid);
-      sd.init(a.dout, head, a, st.start, st.len, tid);
-    }
-    sq.load(row0);
-    sd.load(row0);
-    if (tid < QR) {
-      const bool in = row0 + tid < st.len;
-      const int64_t at = (int64_t)head * a.tokens + st.start + row0 + tid;
-      sl = in ? a.lse[at] * kLog2e : __builtin_inff();  // p = 0 in rows past the end
-      sdl = in ? a.delta[at] : 0.f;
-    }
+  Copier<T, DP, QR> cq, cd;
+  cq.init(a.q, head0, a, st.start, st.len, w, lane);
+  cd.init(a.dout, head0, a, st.start, st.len, w, lane);
+  auto copy = [&](int it) {
+    const int head = head0 + it / nq, row0 = (qt0 + it % nq) * QR, b = it & 1;
+    cq.seek(a.q, head, st.start);
+    cd.seek(a.dout, head, st.start);
+    cq.copy(lds[b][0], row0, w, lane);
+    cd.copy(lds[b][1], row0, w, lane);
+    // rows past the end get zeros, which q and dout have there too: p = 1, ds = 0, and neither adds anything
+    if (w < 2)
+      dma_b32(buffer_of((w ? a.delta : a.lse2) + (int64_t)head * a.tokens + st.start + row0,
+                        4 * min(st.len - row0, QR)), lds_offset(stat[b][w]), 4 * lane);
   };
-  auto store = [&](int b) {
-    sq.store(lds[b][0], tid);
-    sd.store(lds[b][1], tid);
-    if (tid < QR) stat[b][0][tid] = sl, stat[b][1][tid] = sdl;
-  };
-  load(0);
-  store(0);
-  __syncthreads();
+  copy(0);
+  wait_tiles();
   for (int it = 0; it < total; ++it) {
     const char *ql = lds[it & 1][0], *dl = lds[it & 1][1];
     const float *ll = stat[it & 1][0], *el = stat[it & 1][1];
     const int q0 = (qt0 + it % nq) * QR;
-    if (it + 1 < total) load(it + 1);
+    if (it + 1 < total) copy(it + 1);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       if (q0 + 32 * j + 31 < kw) continue;  // rows before every key of this wave
@@ -643,8 +697,140 @@ __global__ __launch_bounds__(kThreads, DP * sizeof(T) <= 128 ? 2 : 1) void atten
         }
       }
     }
-    if (it + 1 < total) store((it + 1) & 1);
-    __syncthreads();
+    wait_tiles();
+  }
+  if (!valid) return;
+  if (a.splits == 1) {
+    store_row<T, DP>((T*)a.dk.data + tok * a.dk.token + kvh * a.dk.head, dk, a.scale, a.dim, h);
+    store_row<T, DP>((T*)a.dv.data + tok * a.dv.token + kvh * a.dv.head, dv, 1.f, a.dim, h);
+  } else {
+    float* p = a.part + (((int64_t)part * a.tokens + tok) * a.kv_heads + kvh) * 2 * a.dim;
+    store_row<float, DP>(p, dk, a.scale, a.dim, h);
+    store_row<float, DP>(p + a.dim, dv, 1.f, a.dim, h);
+  }
+}
+
+// The same in bf16.  32 query rows at a time stream through a ring of slots;
+// their scores' sums start from -lse / scale and -delta, so p = exp2(c s) and
+// ds = p dp.  Two blocks share a CU (two waves a SIMD): with head sizes above
+// 64, V's fragments are read from LDS again and again to fit the registers.
+template <int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArgs a) {
+  typedef __bf16 T;
+  typedef Elem<T>::Frag Frag;
+  typedef Tiles<T, DP> Tl;
+  typedef PairCopier<T, DP, 32> Ring;
+  constexpr bool kHoldV = DP <= 64;
+  constexpr int BN = 128, ST = DP / 16, DT = DP / 32, kSlots = DP > 96 ? 2 : 4;
+  __shared__ __align__(256) char ring[kSlots * Ring::kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int per = a.kv_heads * a.splits;
+  const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
+  const SeqTile st = block_tile(a, (int)(blockIdx.x / per), (int)(gridDim.x / per), BN, lane, true);
+  if (st.row0 >= st.len) return;
+  if (st.tail) {
+    const int rows = min(BN, st.len - st.row0), r0 = st.start + st.row0;
+    if (part == 0 && (a.zero_tail & kZeroDk)) zero_rows<T>(a.dk, kvh, r0, rows, a.dim, tid);
+    if (part == 0 && (a.zero_tail & kZeroDv)) zero_rows<T>(a.dv, kvh, r0, rows, a.dim, tid);
+    return;
+  }
+  const int kw = st.row0 + 32 * w, ki = kw + col;
+  const bool valid = ki < st.len;
+  const int64_t tok = st.start + (int64_t)ki;
+  const float c = a.scale * kLog2e;
+  const int hpp = a.group / a.splits, head0 = kvh * a.group + part * hpp;  // this block's query heads
+
+  char* const vt = ring + kSlots * Ring::kSlot;
+  Frag kf[ST], vf[kHoldV ? ST : 1];
+  load_frags<T, DP>(kf, (const T*)a.k.data + tok * a.k.token + kvh * a.k.head, valid, a.dim, h);
+  if constexpr (kHoldV) {
+    load_frags<T, DP>(vf, (const T*)a.v.data + tok * a.v.token + kvh * a.v.head, valid, a.dim, h);
+  } else {
+    Copier<T, DP, BN> cv;
+    cv.init(a.v, kvh, a, st.start, st.len, w, lane);
+    cv.copy(vt, st.row0, w, lane);
+  }
+  f32x16 dk[DT], dv[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
+
+  // The next rows to copy: their slot, head and row, and where they lie.
+  Ring rg;
+  const int64_t qs = a.q.token * (int64_t)sizeof(T), os = a.dout.token * (int64_t)sizeof(T);
+  rg.init(qs, os, a.dim * (int)sizeof(T), w, lane);
+  int cslot = 0, chead = head0, left;
+  const char *qp, *op;
+  const float *lp, *ep;
+  auto seek = [&]() {
+    const int64_t t0 = st.start + (int64_t)st.row0, at = (int64_t)chead * a.tokens + t0;
+    qp = (const char*)((const T*)a.q.data + t0 * a.q.token + chead * a.q.head);
+    op = (const char*)((const T*)a.dout.data + t0 * a.dout.token + chead * a.dout.head);
+    lp = a.lse2 + at;
+    ep = a.delta + at;
+    left = chead < head0 + hpp ? st.len - st.row0 : 0;
+  };
+  auto copy = [&]() {
+    rg.copy(ring + cslot * Ring::kSlot, qp, qs, op, os, lp, ep, left, a.dim * (int)sizeof(T), w, lane);
+    cslot = (cslot + 1) & (kSlots - 1);
+    left -= 32;
+    if (left > 0) {
+      qp += 32 * qs;
+      op += 32 * os;
+      lp += 32;
+      ep += 32;
+    } else {
+      ++chead;
+      seek();
+    }
+  };
+  seek();
+#pragma unroll
+  for (int i = 0; i < kSlots - 1; ++i) copy();
+  const int total = (st.len - st.row0 + 31) / 32 * hpp;
+  int row = st.row0;
+  for (int i = 0; i < total; ++i) {
+    wait_but<(kSlots - 2) * Ring::kN>();
+    copy();
+    const char* sl = ring + (i & (kSlots - 1)) * Ring::kSlot;
+    f32x16 s, dp;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 x = *(const f32x4*)(sl + 2 * Ring::kHalf + 32 * g + 16 * h);
+      const f32x4 y = *(const f32x4*)(sl + 2 * Ring::kHalf + 256 + 32 * g + 16 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * g + e] = x[e], dp[4 * g + e] = y[e];
+    }
+#pragma unroll
+    for (int q = 0; q < ST; ++q) {
+      s = Elem<T>::mma(Tl::row_frag(sl, col, q, h), kf[q], s);
+      if constexpr (kHoldV)
+        dp = Elem<T>::mma(Tl::row_frag(sl + Ring::kHalf, col, q, h), vf[q], dp);
+      else
+        dp = Elem<T>::mma(Tl::row_frag(sl + Ring::kHalf, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
+    }
+    if (row < kw + 31) {  // a row before some key
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (row + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
+    }
+    float p[16], ds[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(s[e] * c);
+      ds[e] = p[e] * dp[e];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
+#pragma unroll
+      for (int t = 0; t < DT; ++t) {
+        dv[t] = Elem<T>::mma(Tl::col_frag(sl + Ring::kHalf, 16 * u, t, lane), pf, dv[t]);
+        dk[t] = Elem<T>::mma(Tl::col_frag(sl, 16 * u, t, lane), sf, dk[t]);
+      }
+    }
+    row += 32;
+    if (row >= st.len) row = st.row0;
   }
   if (!valid) return;
   if (a.splits == 1) {
@@ -690,8 +876,11 @@ template <class T, int DP>
 hipError_t backward_dp(const AttnArgs& a, hipStream_t stream) {
   const int64_t slots = slots_of(a.tokens, a.seqs, 128);
   hipError_t e = launch_kernel(attention_dq_kernel<T, DP>, slots * a.q_heads, kThreads, a, stream);
-  if (e == hipSuccess)
-    e = launch_kernel(attention_dkv_kernel<T, DP>, slots * a.kv_heads * a.splits, kThreads, a, stream);
+  if (e != hipSuccess) return e;
+  if constexpr (sizeof(T) == 2)
+    e = launch_kernel(attention_dkv_bf16_kernel<DP>, slots * a.kv_heads * a.splits, kThreads, a, stream);
+  else
+    e = launch_kernel(attention_dkv_kernel<DP>, slots * a.kv_heads * a.splits, kThreads, a, stream);
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t blocks = (a.tokens * a.kv_heads * 2 * a.dim / 4 + kThreads - 1) / kThreads;
   return launch_kernel(attention_sum_kernel<T>, blocks < 4096 ? blocks : 4096, kThreads, a, stream);

@@ -110,8 +110,11 @@ size_t attention_part_bytes(const muon_attention_desc* d, int splits) {
 int splits_of(const muon_attention_desc* d) {
   return attention_splits(d->tokens, d->seqs, d->q_heads, d->kv_heads, d->head_dim, d->dtype == MUON_DTYPE_BF16);
 }
+size_t attention_row_bytes(const muon_attention_desc* d) {  // one fp32 per query row
+  return align_up((size_t)d->q_heads * d->tokens * sizeof(float));
+}
 size_t attention_workspace(const muon_attention_desc* d) {
-  return align_up((size_t)d->q_heads * d->tokens * sizeof(float)) + align_up(attention_part_bytes(d, splits_of(d))) +
+  return 2 * attention_row_bytes(d) + align_up(attention_part_bytes(d, splits_of(d))) +
          kAlign;  // never 0, which means an error
 }
 
@@ -267,9 +270,8 @@ int muon_attention_backward(const muon_attention_desc* d, const int32_t* cu_seql
   a.lse = const_cast<float*>(lse);
   a.splits = splits_of(d);
   a.delta = (float*)workspace;
-  a.part = a.splits > 1
-               ? (float*)((char*)workspace + align_up((size_t)d->q_heads * d->tokens * sizeof(float)))
-               : nullptr;
+  a.lse2 = (float*)((char*)workspace + attention_row_bytes(d));
+  a.part = a.splits > 1 ? (float*)((char*)workspace + 2 * attention_row_bytes(d)) : nullptr;
   const hipError_t e = launch_attention_backward(a, d->dtype == MUON_DTYPE_BF16, (hipStream_t)hip_stream);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "attention backward launch");
 }

@@ -63,7 +63,8 @@ struct AttnArgs {
   HeadView q, k, v, o;
   HeadView dout, dq, dk, dv;  // backward only
   float* lse;                 // (q_heads, tokens)
-  float* delta;               // backward: (q_heads, tokens) workspace
+  float* delta;               // backward workspace: (q_heads, tokens)
+  float* lse2;                // and again, lse / log 2
   float* part;                // backward: partial dK, dV (see AttnSumArgs); null when one block owns a whole group
   const int32_t* cu;          // (seqs + 1) token offsets of the packed sequences
   int64_t tokens;

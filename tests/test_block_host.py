@@ -161,8 +161,8 @@ def test_attention_workspace_holds_delta(lib):
     for tokens in (1, 1000, 1 << 20):
         for q, kv in ((12, 12), (16, 4), (32, 1)):
             need = lib.muon_attention_workspace_size(ctypes.byref(attn_desc(tokens=tokens, q_heads=q, kv_heads=kv)))
-            assert need >= q * tokens * 4
-            assert need <= q * tokens * 4 + q * tokens * 2 * 64 * 4 + 1024  # and at most one partial per query head
+            assert need >= 2 * q * tokens * 4  # delta and lse of every query row
+            assert need <= 2 * q * tokens * 4 + q * tokens * 2 * 64 * 4 + 1024  # and at most one partial per query head
 
 
 def test_binding_refuses_tensors_before_any_call():

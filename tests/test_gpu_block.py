@@ -304,7 +304,7 @@ def test_attention_nan_stays_in_its_sequence():
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_attention_broadcast_inputs(dtype):
-    """Inputs that repeat one head's memory (stride 0) are read as they stand."""
+    """Inputs that repeat one head's or one token's memory (stride 0), or whose rows overlap, are read as they stand."""
     n, D = 90, 64
     k1, v1 = randn((n, 1, D), 730, dtype), randn((n, 1, D), 731, dtype)
     q, do = randn((n, 4, D), 732, dtype), randn((n, 4, D), 733, dtype)
@@ -313,6 +313,21 @@ def test_attention_broadcast_inputs(dtype):
     out, lse = lib.packed_attention_forward(q.to(DEV), kd, vd, cu)
     g = lib.packed_attention_backward(do.to(DEV), q.to(DEV), kd, vd, out, lse, cu)
     ref = R.attention(q, k1.expand(n, 4, D), v1.expand(n, 4, D), [n], D ** -0.5, do)
+    for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *g)):
+        R.check(name, got, *ref[name])
+    one = randn((1, 1, D), 734, dtype)  # the gradient of a sum: one value everywhere
+    line = randn((n * 8 + D,), 735, dtype)
+    roll = torch.as_strided(line, (n, 1, D), (8, D, 1))
+    rolld = torch.as_strided(line.to(DEV), (n, 1, D), (8, D, 1))
+    oned = one.to(DEV).expand(n, 4, D)
+    out, lse = lib.packed_attention_forward(q.to(DEV), rolld, vd[:, :1], cu)
+    g = lib.packed_attention_backward(oned, q.to(DEV), rolld, vd[:, :1], out, lse, cu)
+    ref = R.attention(q, roll, v1, [n], D ** -0.5, one.expand(n, 4, D))
+    for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *g)):
+        R.check(name, got, *ref[name])
+    out, lse = lib.packed_attention_forward(rolld.expand(n, 4, D), kd[:, :1], oned[:, :1], cu)
+    g = lib.packed_attention_backward(do.to(DEV), rolld.expand(n, 4, D), kd[:, :1], oned[:, :1], out, lse, cu)
+    ref = R.attention(roll.expand(n, 4, D), k1, one.expand(n, 1, D), [n], D ** -0.5, do)
     for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *g)):
         R.check(name, got, *ref[name])
 
