@@ -158,79 +158,51 @@ __device__ __forceinline__ void wait_but() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <class T, int DP, int ROWS>
-struct Copier {
-  static constexpr int kN = ROWS * DP * (int)sizeof(T) / 1024 / (kThreads / 64);
-  static_assert(kN * kThreads * 16 == ROWS * DP * (int)sizeof(T), "whole instructions per wave");
-  const char* base;   // the sequence's first row of this head
-  int64_t step;       // bytes from row to row
-  int len, row_bytes;
-  uint32_t off[kN];
-  __device__ __forceinline__ void init(const HeadView& v, int head, const AttnArgs& a, int start, int seq_len, int w,
-                                       int lane) {
-    constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
-    seek(v, head, start);
-    step = v.token * (int64_t)sizeof(T);
-    len = seq_len;
-    row_bytes = a.dim * (int)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int idx = (w * kN + i) * 64 + lane, row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
-      off[i] = c * 16 < row_bytes ? (uint32_t)(row * step) + 16u * c : kOob;
-    }
-  }
-  __device__ __forceinline__ void seek(const HeadView& v, int head, int start) {
-    base = (const char*)((const T*)v.data + start * v.token + head * v.head);
-  }
-  __device__ __forceinline__ void copy(char* tile, int row0, int w, int lane) const {
-    const int rows = min(len - row0, ROWS);
-    const u32x4 rs = buffer_of(base + row0 * step, rows > 0 ? (uint32_t)((rows - 1) * step) + row_bytes : 0u);
-    if (rows == ROWS) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) dma_b128(rs, lds_offset(tile + (w * kN + i) * 1024), off[i]);
-    } else {  // rows may overlap (a step of 0 repeats one), so the resource's end alone does not tell them apart
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        dma_b128(rs, lds_offset(tile + (w * kN + i) * 1024),
-                 ((w * kN + i) * 64 + lane) / Tiles<T, DP>::kCpr < rows ? off[i] : kOob);
-    }
-  }
-};
-
-// One slot of a ring: ROWS rows of two operands (at 0 and kHalf), and two fp32
-// words a row (at 2 kHalf, 64 floats each).  The wave instructions are dealt
-// out evenly, kN of them to every wave, so that waits can count them.
+// Copies ROWS rows at a time of two operands (K and V, or Q and dO) into a
+// pair of adjacent tiles.  Waves 0 and 1 copy the first operand, waves 2 and 3
+// the second, kN instructions each, so a wave keeps one pointer and one
+// resource, and waits can count instructions.
 template <class T, int DP, int ROWS>
 struct PairCopier {
-  static constexpr int kHalf = ROWS * DP * (int)sizeof(T), kSlot = 2 * kHalf + 512;
-  static constexpr int kTileN = 2 * kHalf / 1024 / (kThreads / 64), kN = kTileN + 1;
-  static_assert(kTileN * kThreads * 16 == 2 * kHalf && ROWS <= 64, "whole instructions per wave");
-  uint32_t off[kTileN];
-  __device__ __forceinline__ void init(int64_t step0, int64_t step1, int row_bytes, int w, int lane) {
+  static constexpr int kTile = ROWS * DP * (int)sizeof(T), kN = 2 * kTile / 1024 / (kThreads / 64);
+  static_assert(kN * kThreads * 16 == 2 * kTile, "whole instructions per wave");
+  const char* at;           // the next row of this wave's operand
+  int64_t step;             // bytes from row to row
+  int left;                 // rows from there to the sequence's end
+  uint32_t row_bytes;
+  uint32_t off[kN];
+  __device__ __forceinline__ void init(const HeadView& x, const HeadView& y, int dim, int w, int lane) {
     constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
+    step = (w < 2 ? x.token : y.token) * (int64_t)sizeof(T);
+    row_bytes = dim * (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kTileN; ++i) {
-      const int n = w * kTileN + i, idx = n * 64 + lane - (n * 1024 >= kHalf ? kHalf / 16 : 0);
-      const int row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
-      off[i] = c * 16 < row_bytes ? (uint32_t)(row * (n * 1024 >= kHalf ? step1 : step0)) + 16u * c : kOob;
+    for (int i = 0; i < kN; ++i) {
+      const int idx = ((w & 1) * kN + i) * 64 + lane, row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
+      off[i] = (uint32_t)c * 16 < row_bytes ? (uint32_t)(row * step) + 16u * c : kOob;
     }
   }
-  // `rows` rows from p0 and p1 (0: a slot of zeros), and their words from s0 and s1.
-  __device__ __forceinline__ void copy(char* slot, const char* p0, int64_t step0, const char* p1, int64_t step1,
-                                       const float* s0, const float* s1, int rows, int row_bytes, int w,
-                                       int lane) const {
-    rows = rows < 0 ? 0 : min(rows, ROWS);
-    const uint32_t n0 = rows > 0 ? (uint32_t)((rows - 1) * step0) + row_bytes : 0u;
-    const uint32_t n1 = rows > 0 ? (uint32_t)((rows - 1) * step1) + row_bytes : 0u;
+  __device__ __forceinline__ void seek(const HeadView& x, int xhead, const HeadView& y, int yhead, int64_t token,
+                                       int rows, int w) {
+    const HeadView& v = w < 2 ? x : y;
+    at = (const char*)((const T*)v.data + token * v.token + (w < 2 ? xhead : yhead) * v.head);
+    left = rows;
+  }
+  // `pair`: the two tiles.  Moves on to the next rows; past the last, tiles of zeros.
+  __device__ __forceinline__ void copy(char* pair, int w, int lane) {
+    const uint32_t lds = lds_offset(pair + w * kN * 1024);
+    if (left >= ROWS) {
+      const u32x4 rs = buffer_of(at, (uint32_t)((ROWS - 1) * step) + row_bytes);
 #pragma unroll
-    for (int i = 0; i < kTileN; ++i) {
-      const int n = w * kTileN + i;
-      const bool second = n * 1024 >= kHalf;
-      uint32_t o = off[i];
-      if (rows < ROWS && (n * 64 + lane - (second ? kHalf / 16 : 0)) / Tiles<T, DP>::kCpr >= rows) o = kOob;
-      dma_b128(second ? buffer_of(p1, n1) : buffer_of(p0, n0), lds_offset(slot + n * 1024), o);
+      for (int i = 0; i < kN; ++i) dma_b128(rs, lds + 1024 * i, off[i]);
+    } else {  // rows may overlap (a step of 0 repeats one), so the resource's end alone does not tell them apart
+      const u32x4 rs = buffer_of(at, left > 0 ? (uint32_t)((left - 1) * step) + row_bytes : 0u);
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        dma_b128(rs, lds + 1024 * i,
+                 (((w & 1) * kN + i) * 64 + lane) / Tiles<T, DP>::kCpr < left ? off[i] : kOob);
     }
-    dma_b32(buffer_of(w & 1 ? s1 : s0, 4 * rows), lds_offset(slot + 2 * kHalf + 256 * (w & 1)), 4 * lane);
+    at += ROWS * step;
+    left -= ROWS;
   }
 };
 
@@ -324,33 +296,57 @@ inline int64_t slots_of(int64_t tokens, int seqs, int bm) { return tokens / bm +
 // largest w with N(w) > rank, and in that level the sequence.  (Backward, the
 // keys of tile t are looked at by tiles - t tiles of queries.)
 constexpr int kRankSeqs = 256;
+// Sum and maximum (of values that are not negative) over the wave in six
+// data-parallel steps: within rows of 16 lanes, then across them; lane 63
+// ends with the result.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
 __device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  return __builtin_amdgcn_readfirstlane(x);
+  x += dpp<0x111, 0xf>(x);
+  x += dpp<0x112, 0xf>(x);
+  x += dpp<0x114, 0xf>(x);
+  x += dpp<0x118, 0xf>(x);
+  x += dpp<0x142, 0xa>(x);
+  x += dpp<0x143, 0xc>(x);
+  return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ int wave_max(int x) {
+  x = max(x, dpp<0x111, 0xf>(x));
+  x = max(x, dpp<0x112, 0xf>(x));
+  x = max(x, dpp<0x114, 0xf>(x));
+  x = max(x, dpp<0x118, 0xf>(x));
+  x = max(x, dpp<0x142, 0xa>(x));
+  x = max(x, dpp<0x143, 0xc>(x));
+  return __builtin_amdgcn_readlane(x, 63);
 }
 __device__ __forceinline__ SeqTile ranked_tile(const AttnArgs& a, int rank, int bm, int lane, bool keys) {
   constexpr int kC = kRankSeqs / 64;
-  int nt[kC], most = 0, all = 0;
+  int from[kC], to[kC], nt[kC], most = 0, all = 0, end = 0;
 #pragma unroll
   for (int c = 0; c < kC; ++c) {
-    const int i = 64 * c + lane;
-    nt[c] = i < a.seqs ? (max(token_at(a, i + 1) - token_at(a, i), 0) + bm - 1) / bm : 0;
-    most = max(most, nt[c]);
-    all += nt[c];
+    from[c] = to[c] = nt[c] = 0;
+    if (c == 0 || a.seqs > 64 * c) {
+      const int i = min(64 * c + lane, a.seqs);
+      from[c] = token_at(a, i);
+      to[c] = token_at(a, min(i + 1, a.seqs));
+      end = __builtin_amdgcn_readlane(to[c], 63);  // the last sequence's, in the last chunk
+      nt[c] = (max(to[c] - from[c], 0) + bm - 1) / bm;
+      most = max(most, nt[c]);
+      all += nt[c];
+    }
   }
   SeqTile t;
   all = wave_sum(all);
   if (rank >= all) {
     t.tail = true;
-    t.start = token_at(a, a.seqs);
+    t.start = end;
     t.len = (int)a.tokens - t.start;
     t.row0 = rank - all < (t.len + bm - 1) / bm ? (rank - all) * bm : t.len;
     return t;
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o));
-  int lo = 1, hi = __builtin_amdgcn_readfirstlane(most) + 1, above = 0;  // N(lo) > rank >= N(hi) = above
+  int lo = 1, hi = wave_max(most) + 1, above = 0;  // N(lo) > rank >= N(hi) = above
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     int n = 0;
@@ -364,19 +360,21 @@ __device__ __forceinline__ SeqTile ranked_tile(const AttnArgs& a, int rank, int 
       above = n;
     }
   }
-  int j = rank - above, seq = 0;  // the j-th sequence of at least lo tiles
+  int j = rank - above;  // the j-th sequence of at least lo tiles
+  t.tail = false;
+  t.start = t.len = 0;
 #pragma unroll
   for (int c = 0; c < kC; ++c) {
     const uint64_t m = __ballot(nt[c] >= lo);
-    const uint64_t before = m & ((1ull << lane) - 1);
-    const uint64_t hit = __ballot(((m >> lane) & 1) && __popcll(before) == j);
-    if (j >= 0 && hit) seq = 64 * c + __ffsll((unsigned long long)hit) - 1;
-    j -= __popcll(m);
-    if (j < 0) j = -0x40000000;
+    const int n = __popcll(m);
+    if (j >= 0 && j < n) {
+      const uint64_t hit = __ballot(((m >> lane) & 1) && __popcll(m & ((1ull << lane) - 1)) == j);
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      t.start = __builtin_amdgcn_readlane(from[c], l);
+      t.len = max(__builtin_amdgcn_readlane(to[c], l) - t.start, 0);
+    }
+    j -= n;
   }
-  t.tail = false;
-  t.start = token_at(a, seq);
-  t.len = max(token_at(a, seq + 1) - t.start, 0);
   t.row0 = (keys ? (t.len + bm - 1) / bm - lo : lo - 1) * bm;
   return t;
 }
@@ -434,18 +432,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
   for (int t = 0; t < DT; ++t) o[t] = f32x16{};
   float m = -__builtin_inff(), l = 0.f;
 
-  Copier<T, DP, KT> ck, cv;
-  ck.init(a.k, kvh, a, st.start, st.len, w, lane);
-  cv.init(a.v, kvh, a, st.start, st.len, w, lane);
-  ck.copy(lds[0][0], 0, w, lane);
-  cv.copy(lds[0][1], 0, w, lane);
+  PairCopier<T, DP, KT> cp;
+  cp.init(a.k, a.v, a.dim, w, lane);
+  cp.seek(a.k, kvh, a.v, kvh, st.start, st.len, w);
+  cp.copy(lds[0][0], w, lane);
   wait_tiles();
   for (int kt = 0; kt < ntile; ++kt) {
     const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
-    if (kt + 1 < ntile) {
-      ck.copy(lds[(kt + 1) & 1][0], (kt + 1) * KT, w, lane);
-      cv.copy(lds[(kt + 1) & 1][1], (kt + 1) * KT, w, lane);
-    }
+    if (kt + 1 < ntile) cp.copy(lds[(kt + 1) & 1][0], w, lane);
     if (kt * KT < wend) {
       f32x16 s[MT];
 #pragma unroll
@@ -562,18 +556,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
   for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
 
-  Copier<T, DP, KT> ck, cv;
-  ck.init(a.k, kvh, a, st.start, st.len, w, lane);
-  cv.init(a.v, kvh, a, st.start, st.len, w, lane);
-  ck.copy(lds[0][0], 0, w, lane);
-  cv.copy(lds[0][1], 0, w, lane);
+  PairCopier<T, DP, KT> cp;
+  cp.init(a.k, a.v, a.dim, w, lane);
+  cp.seek(a.k, kvh, a.v, kvh, st.start, st.len, w);
+  cp.copy(lds[0][0], w, lane);
   wait_tiles();
   for (int kt = 0; kt < ntile; ++kt) {
     const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
-    if (kt + 1 < ntile) {
-      ck.copy(lds[(kt + 1) & 1][0], (kt + 1) * KT, w, lane);
-      cv.copy(lds[(kt + 1) & 1][1], (kt + 1) * KT, w, lane);
-    }
+    if (kt + 1 < ntile) cp.copy(lds[(kt + 1) & 1][0], w, lane);
     if (kt * KT < wend) {
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
@@ -641,15 +631,12 @@ __global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kern
   for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
 
   const int qt0 = st.row0 / QR, nq = (st.len + QR - 1) / QR - qt0, total = nq * hpp;
-  Copier<T, DP, QR> cq, cd;
-  cq.init(a.q, head0, a, st.start, st.len, w, lane);
-  cd.init(a.dout, head0, a, st.start, st.len, w, lane);
+  PairCopier<T, DP, QR> cp;
+  cp.init(a.q, a.dout, a.dim, w, lane);
   auto copy = [&](int it) {
     const int head = head0 + it / nq, row0 = (qt0 + it % nq) * QR, b = it & 1;
-    cq.seek(a.q, head, st.start);
-    cd.seek(a.dout, head, st.start);
-    cq.copy(lds[b][0], row0, w, lane);
-    cd.copy(lds[b][1], row0, w, lane);
+    cp.seek(a.q, head, a.dout, head, st.start + (int64_t)row0, st.len - row0, w);
+    cp.copy(lds[b][0], w, lane);
     // rows past the end get zeros, which q and dout have there too: p = 1, ds = 0, and neither adds anything
     if (w < 2)
       dma_b32(buffer_of((w ? a.delta : a.lse2) + (int64_t)head * a.tokens + st.start + row0,
@@ -710,19 +697,21 @@ __global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kern
   }
 }
 
-// The same in bf16.  32 query rows at a time stream through a ring of slots;
-// their scores' sums start from -lse / scale and -delta, so p = exp2(c s) and
-// ds = p dp.  Two blocks share a CU (two waves a SIMD): with head sizes above
-// 64, V's fragments are read from LDS again and again to fit the registers.
+// The same in bf16.  Query rows stream through a ring of slots, 32 at a time
+// into the products; their scores' sums start from -lse / scale and -delta, so
+// p = exp2(c s) and ds = p dp.  Two blocks or three share a CU, as many waves a
+// SIMD: with head sizes above 64, V's fragments are read from LDS again and
+// again to fit the registers.
 template <int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArgs a) {
   typedef __bf16 T;
   typedef Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  typedef PairCopier<T, DP, 32> Ring;
   constexpr bool kHoldV = DP <= 64;
-  constexpr int BN = 128, ST = DP / 16, DT = DP / 32, kSlots = DP > 96 ? 2 : 4;
-  __shared__ __align__(256) char ring[kSlots * Ring::kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
+  constexpr int BN = 128, ST = DP / 16, DT = DP / 32, QR = DP <= 64 ? 64 : 32, kSlots = DP == 96 ? 4 : 2;
+  typedef PairCopier<T, DP, QR> Pair;
+  constexpr int kSlot = 2 * Pair::kTile + 512;  // Q rows, dO rows, and two words a row
+  __shared__ __align__(256) char ring[kSlots * kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int per = a.kv_heads * a.splits;
@@ -741,45 +730,40 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
   const float c = a.scale * kLog2e;
   const int hpp = a.group / a.splits, head0 = kvh * a.group + part * hpp;  // this block's query heads
 
-  char* const vt = ring + kSlots * Ring::kSlot;
+  char* const vt = ring + kSlots * kSlot;
   Frag kf[ST], vf[kHoldV ? ST : 1];
   load_frags<T, DP>(kf, (const T*)a.k.data + tok * a.k.token + kvh * a.k.head, valid, a.dim, h);
   if constexpr (kHoldV) {
     load_frags<T, DP>(vf, (const T*)a.v.data + tok * a.v.token + kvh * a.v.head, valid, a.dim, h);
-  } else {
-    Copier<T, DP, BN> cv;
-    cv.init(a.v, kvh, a, st.start, st.len, w, lane);
-    cv.copy(vt, st.row0, w, lane);
+  } else {  // two tiles of V's rows, by a copier of its own
+    PairCopier<T, DP, BN / 2> cv;
+    cv.init(a.v, a.v, a.dim, w, lane);
+    cv.seek(a.v, kvh, a.v, kvh, st.start + (int64_t)st.row0 + (w < 2 ? 0 : BN / 2),
+            st.len - st.row0 - (w < 2 ? 0 : BN / 2), w);
+    cv.copy(vt, w, lane);
   }
   f32x16 dk[DT], dv[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
 
-  // The next rows to copy: their slot, head and row, and where they lie.
-  Ring rg;
-  const int64_t qs = a.q.token * (int64_t)sizeof(T), os = a.dout.token * (int64_t)sizeof(T);
-  rg.init(qs, os, a.dim * (int)sizeof(T), w, lane);
-  int cslot = 0, chead = head0, left;
-  const char *qp, *op;
-  const float *lp, *ep;
+  // The rows to copy next: their slot, head and words (even waves copy the first, odd ones the second).
+  Pair cp;
+  cp.init(a.q, a.dout, a.dim, w, lane);
+  int cslot = 0, chead = head0;
+  const float* words;
   auto seek = [&]() {
-    const int64_t t0 = st.start + (int64_t)st.row0, at = (int64_t)chead * a.tokens + t0;
-    qp = (const char*)((const T*)a.q.data + t0 * a.q.token + chead * a.q.head);
-    op = (const char*)((const T*)a.dout.data + t0 * a.dout.token + chead * a.dout.head);
-    lp = a.lse2 + at;
-    ep = a.delta + at;
-    left = chead < head0 + hpp ? st.len - st.row0 : 0;
+    const int64_t t0 = st.start + (int64_t)st.row0;
+    cp.seek(a.q, chead, a.dout, chead, t0, chead < head0 + hpp ? st.len - st.row0 : 0, w);
+    words = (w & 1 ? a.delta : a.lse2) + (int64_t)chead * a.tokens + t0;
   };
   auto copy = [&]() {
-    rg.copy(ring + cslot * Ring::kSlot, qp, qs, op, os, lp, ep, left, a.dim * (int)sizeof(T), w, lane);
+    char* sl = ring + cslot * kSlot;
+    dma_b32(buffer_of(words, 4 * max(min(cp.left, QR), 0)), lds_offset(sl + 2 * Pair::kTile + 256 * (w & 1)),
+            4 * lane);
+    words += QR;
+    cp.copy(sl, w, lane);
     cslot = (cslot + 1) & (kSlots - 1);
-    left -= 32;
-    if (left > 0) {
-      qp += 32 * qs;
-      op += 32 * os;
-      lp += 32;
-      ep += 32;
-    } else {
+    if (cp.left <= 0) {
       ++chead;
       seek();
     }
@@ -787,49 +771,53 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
   seek();
 #pragma unroll
   for (int i = 0; i < kSlots - 1; ++i) copy();
-  const int total = (st.len - st.row0 + 31) / 32 * hpp;
+  const int total = (st.len - st.row0 + QR - 1) / QR * hpp;
   int row = st.row0;
   for (int i = 0; i < total; ++i) {
-    wait_but<(kSlots - 2) * Ring::kN>();
+    wait_but<(kSlots - 2) * (Pair::kN + 1)>();
     copy();
-    const char* sl = ring + (i & (kSlots - 1)) * Ring::kSlot;
-    f32x16 s, dp;
+    const char* sl = ring + (i & (kSlots - 1)) * kSlot;
+#pragma unroll 1
+    for (int j = 0; j < QR; j += 32) {
+      const char *ql = sl + j * Tl::kRow, *ol = ql + Pair::kTile;
+      f32x16 s, dp;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 x = *(const f32x4*)(sl + 2 * Ring::kHalf + 32 * g + 16 * h);
-      const f32x4 y = *(const f32x4*)(sl + 2 * Ring::kHalf + 256 + 32 * g + 16 * h);
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 x = *(const f32x4*)(sl + 2 * Pair::kTile + 4 * j + 32 * g + 16 * h);
+        const f32x4 y = *(const f32x4*)(sl + 2 * Pair::kTile + 256 + 4 * j + 32 * g + 16 * h);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * g + e] = x[e], dp[4 * g + e] = y[e];
-    }
-#pragma unroll
-    for (int q = 0; q < ST; ++q) {
-      s = Elem<T>::mma(Tl::row_frag(sl, col, q, h), kf[q], s);
-      if constexpr (kHoldV)
-        dp = Elem<T>::mma(Tl::row_frag(sl + Ring::kHalf, col, q, h), vf[q], dp);
-      else
-        dp = Elem<T>::mma(Tl::row_frag(sl + Ring::kHalf, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
-    }
-    if (row < kw + 31) {  // a row before some key
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (row + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
-    }
-    float p[16], ds[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(s[e] * c);
-      ds[e] = p[e] * dp[e];
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
-#pragma unroll
-      for (int t = 0; t < DT; ++t) {
-        dv[t] = Elem<T>::mma(Tl::col_frag(sl + Ring::kHalf, 16 * u, t, lane), pf, dv[t]);
-        dk[t] = Elem<T>::mma(Tl::col_frag(sl, 16 * u, t, lane), sf, dk[t]);
+        for (int e = 0; e < 4; ++e) s[4 * g + e] = x[e], dp[4 * g + e] = y[e];
       }
+#pragma unroll
+      for (int q = 0; q < ST; ++q) {
+        s = Elem<T>::mma(Tl::row_frag(ql, col, q, h), kf[q], s);
+        if constexpr (kHoldV)
+          dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), vf[q], dp);
+        else
+          dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
+      }
+      if (row < kw + 31) {  // a row before some key
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (row + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
+      }
+      float p[16], ds[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(s[e] * c);
+        ds[e] = p[e] * dp[e];
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          dv[t] = Elem<T>::mma(Tl::col_frag(ol, 16 * u, t, lane), pf, dv[t]);
+          dk[t] = Elem<T>::mma(Tl::col_frag(ql, 16 * u, t, lane), sf, dk[t]);
+        }
+      }
+      row += 32;
     }
-    row += 32;
     if (row >= st.len) row = st.row0;
   }
   if (!valid) return;
