@@ -51,8 +51,7 @@ int check_norm(const muon_layernorm_desc* d) {
 }
 
 size_t norm_workspace(const muon_layernorm_desc* d) {
-  // one block holds at least one row, whichever kernel the pointers' alignment selects
-  return align_up((size_t)norm_backward_blocks(d->rows, kMaxCols, true) * 2 * (size_t)d->cols * sizeof(float));
+  return align_up((size_t)norm_backward_blocks(d->rows, d->cols) * 2 * (size_t)d->cols * sizeof(float));
 }
 
 int64_t ld_of(int64_t ld, int64_t cols) { return ld ? ld : cols; }
@@ -144,7 +143,7 @@ int muon_layernorm_forward(const muon_layernorm_desc* d, const void* x, const vo
   if (d->rows == 0) return MUON_OK;
   if (!x || !y || !mean || !rstd) return fail(MUON_E_INVAL, "layer norm: x, y, mean or rstd is NULL");
   if (y == x) return fail(MUON_E_INVAL, "layer norm: y must not be x");
-  const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype), ve = 16 / es;
+  const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
   if (misaligned(x, es) || misaligned(y, es) || misaligned(weight, ps) || misaligned(bias, ps) ||
       misaligned(mean, 4) || misaligned(rstd, 4))
     return fail(MUON_E_INVAL, "layer norm: pointer not aligned to its element size");
@@ -152,9 +151,7 @@ int muon_layernorm_forward(const muon_layernorm_desc* d, const void* x, const vo
   a.x = x, a.weight = weight, a.bias = bias, a.out = y, a.mean = mean, a.rstd = rstd;
   a.rows = d->rows, a.cols = (int32_t)d->cols, a.eps = d->eps;
   a.ld_x = ld_of(d->ld_x, d->cols), a.ld_out = ld_of(d->ld_y, d->cols);
-  const bool vec = !misaligned(x, 16) && !misaligned(y, 16) && !misaligned(weight, 16) && !misaligned(bias, 16) &&
-                   d->cols % ve == 0 && a.ld_x % ve == 0 && a.ld_out % ve == 0;
-  const hipError_t e = launch_norm_forward(a, d->x_dtype == MUON_DTYPE_BF16, d->p_dtype == MUON_DTYPE_BF16, vec,
+  const hipError_t e = launch_norm_forward(a, d->x_dtype == MUON_DTYPE_BF16, d->p_dtype == MUON_DTYPE_BF16,
                                            (hipStream_t)hip_stream);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "layer norm forward launch");
 }
@@ -171,7 +168,7 @@ int muon_layernorm_backward(const muon_layernorm_desc* d, const void* dy, const 
   clear_error();
   if (int rc = check_norm(d)) return rc;
   if (!dx && !dweight && !dbias) return fail(MUON_E_INVAL, "layer norm: dx, dweight and dbias are all NULL");
-  const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype), ve = 16 / es;
+  const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
   if (d->rows > 0) {
     if (!dy || !x || !mean || !rstd) return fail(MUON_E_INVAL, "layer norm: dy, x, mean or rstd is NULL");
     if (dx == dy || dx == x) return fail(MUON_E_INVAL, "layer norm: dx must be neither dy nor x");
@@ -193,12 +190,10 @@ int muon_layernorm_backward(const muon_layernorm_desc* d, const void* dy, const 
   a.part = sums ? (float*)workspace : nullptr;
   a.rows = d->rows, a.cols = (int32_t)d->cols, a.eps = d->eps;
   a.ld_x = ld_of(d->ld_x, d->cols), a.ld_dy = ld_of(d->ld_dy, d->cols), a.ld_out = ld_of(d->ld_dx, d->cols);
-  const bool vec = !misaligned(x, 16) && !misaligned(dy, 16) && !misaligned(dx, 16) && !misaligned(weight, 16) &&
-                   d->cols % ve == 0 && a.ld_x % ve == 0 && a.ld_dy % ve == 0 && a.ld_out % ve == 0;
-  a.blocks = norm_backward_blocks(d->rows, d->cols, vec);
+  a.blocks = norm_backward_blocks(d->rows, d->cols);
   hipError_t e = hipSuccess;
   if (d->rows > 0)
-    e = launch_norm_backward(a, d->x_dtype == MUON_DTYPE_BF16, d->p_dtype == MUON_DTYPE_BF16, vec,
+    e = launch_norm_backward(a, d->x_dtype == MUON_DTYPE_BF16, d->p_dtype == MUON_DTYPE_BF16,
                              (hipStream_t)hip_stream);
   if (e == hipSuccess && sums)
     e = launch_norm_sum(NormSumArgs{a.part, dweight, dbias, a.cols, d->rows > 0 ? a.blocks : 0},

@@ -45,9 +45,9 @@ struct NormSumArgs {
   int32_t blocks;
 };
 
-int norm_backward_blocks(int64_t rows, int64_t cols, bool vec);
-hipError_t launch_norm_forward(const NormArgs& a, bool x_bf16, bool p_bf16, bool vec, hipStream_t stream);
-hipError_t launch_norm_backward(const NormArgs& a, bool x_bf16, bool p_bf16, bool vec, hipStream_t stream);
+int norm_backward_blocks(int64_t rows, int64_t cols);
+hipError_t launch_norm_forward(const NormArgs& a, bool x_bf16, bool p_bf16, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& a, bool x_bf16, bool p_bf16, hipStream_t stream);
 hipError_t launch_norm_sum(const NormSumArgs& a, hipStream_t stream);
 
 // -------------------------------------------------------------- attention --

@@ -12,54 +12,64 @@ namespace muon {
 namespace {
 
 // --------------------------------------------------------------- elements --
-template <class T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float* v) {
-  if constexpr (VEC == 1) {
-    v[0] = (float)*gv<T>(p);
+// A row is read and written in vectors of 16 bytes, wherever it starts: global
+// accesses of gfx950 need no alignment, and on rows of 1001 fp32 elements
+// 16-byte accesses off their boundaries take half the time of 4-byte ones.
+// The types below only promise an element's alignment.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+template <class T, int N>
+__device__ __forceinline__ void load_n(const T* p, float* v) {
+  if constexpr (sizeof(T) == 2 && N == 8) {
+    unpack8_bf16(*gv<u32x4_any>(p), v);
   } else if constexpr (sizeof(T) == 2) {
-    unpack8_bf16(*gv<u32x4>(p), v);
+    unpack4_bf16(*gv<u32x2_any>(p), v);
   } else {
 #pragma unroll
-    for (int q = 0; q < VEC / 4; ++q) {
-      const f32x4 r = *gv<f32x4>(p + 4 * q);
+    for (int q = 0; q < N / 4; ++q) {
+      const f32x4 r = *gv<f32x4_any>(p + 4 * q);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * q + e] = r[e];
     }
   }
 }
-template <class T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float* v) {
-  if constexpr (VEC == 1) {
-    *gv<T>(p) = (T)v[0];
-  } else if constexpr (sizeof(T) == 2) {
-    *gv<u32x4>(p) = pack8_bf16(v);
+template <class T, int N>
+__device__ __forceinline__ void store_n(T* p, const float* v) {
+  if constexpr (sizeof(T) == 2) {
+    *gv<u32x4_any>(p) = pack8_bf16(v);
   } else {
 #pragma unroll
-    for (int q = 0; q < VEC / 4; ++q) *gv<f32x4>(p + 4 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    for (int q = 0; q < N / 4; ++q)
+      *gv<f32x4_any>(p + 4 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
   }
 }
-// A row in vectors of VEC elements: 16 bytes, or one element where a row may
-// start off a 16-byte boundary.
-template <class T>
-constexpr int vec_of(bool vec) {
-  return vec ? 16 / (int)sizeof(T) : 1;
-}
-
-// Parameters are bf16 or fp32 independently of the activations; the vector
-// path reads VEC of them at a time in either type.
-template <class P, int VEC>
-__device__ __forceinline__ void load_param(const void* p, int64_t at, float* v, float none) {
-  if (!p) {
+// N elements at p of which `n` are inside the row: the others read as 0 and
+// are not written.  PART: rows are no whole number of vectors (without it n is
+// N, and the loads of a row stay in one block of code: with the branch, a
+// backward pass over 65536 x 768 took 77 us instead of 57).
+template <class T, int N, bool PART>
+__device__ __forceinline__ void load_part(const T* p, int n, float* v) {
+  if (!PART || n >= N) return load_n<T, N>(p, v);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = none;
-    return;
-  }
-  const P* q = (const P*)p + at;
-  if constexpr (VEC == 4 && sizeof(P) == 2) {
-    unpack4_bf16(*gv<u32x2>(q), v);
-  } else {
-    load_vec<P, VEC>(q, v);
-  }
+  for (int e = 0; e < N; ++e) v[e] = e < n ? (float)*gv<T>(p + e) : 0.f;
+}
+template <class T, int N, bool PART>
+__device__ __forceinline__ void store_part(T* p, int n, const float* v) {
+  if (!PART || n >= N) return store_n<T, N>(p, v);
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (e < n) *gv<T>(p + e) = (T)v[e];
+}
+// Parameters are bf16 or fp32 independently of the activations.
+template <class P, int N, bool PART>
+__device__ __forceinline__ void load_param(const void* p, int64_t at, int n, float* v, float none) {
+  if (p) return load_part<P, N, PART>((const P*)p + at, n, v);
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = none;
 }
 
 // Sum over the TPR threads of a row, the same in all of them.
@@ -88,19 +98,20 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*lds)[N], int tid)
 // ---------------------------------------------------------------- forward --
 // TPR threads hold a row of at most TPR * VEC * NV elements in registers and
 // stride over the rows, so the parameters are loaded once.
-template <class T, class P, int VEC, int TPR, int NV>
+template <class T, class P, int TPR, int NV, bool PART>
 __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
+  constexpr int VEC = kVec<T>;
   __shared__ float red[kThreads / 64][1];
   const int tid = threadIdx.x, t = tid % TPR;
   float w[NV][VEC], b[NV][VEC];
-  bool on[NV];
+  int on[NV];  // elements of each vector inside the row
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * TPR + t) * VEC;
-    on[i] = c < a.cols;
+    on[i] = min(max(a.cols - c, 0), VEC);
     if (on[i]) {
-      load_param<P, VEC>(a.weight, c, w[i], 1.f);
-      load_param<P, VEC>(a.bias, c, b[i], 0.f);
+      load_param<P, VEC, PART>(a.weight, c, on[i], w[i], 1.f);
+      load_param<P, VEC, PART>(a.bias, c, on[i], b[i], 0.f);
     }
   }
   const float inv = 1.f / (float)a.cols;
@@ -113,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-      if (on[i]) load_vec<T, VEC>(x + (i * TPR + t) * VEC, v[i]);
+      if (on[i]) load_part<T, VEC, PART>(x + (i * TPR + t) * VEC, on[i], v[i]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += v[i][e];
     }
@@ -124,7 +135,7 @@ __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        v[i][e] = on[i] ? v[i][e] - mean : 0.f;
+        v[i][e] = (PART ? e < on[i] : on[i] > 0) ? v[i][e] - mean : 0.f;
         s[0] = __builtin_fmaf(v[i][e], v[i][e], s[0]);
       }
     row_sum<TPR, 1>(s, red, tid);
@@ -135,15 +146,16 @@ __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
       if (!on[i]) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = __builtin_fmaf(v[i][e] * rstd, w[i][e], b[i][e]);
-      store_vec<T, VEC>(y + (i * TPR + t) * VEC, v[i]);
+      store_part<T, VEC, PART>(y + (i * TPR + t) * VEC, on[i], v[i]);
     }
     if (t == 0) a.mean[row] = mean, a.rstd[row] = rstd;
   }
 }
 
 // Rows of any length: a block a row, which is read three times (from L2 after the first).
-template <class T, class P, int VEC>
+template <class T, class P, bool PART>
 __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a) {
+  constexpr int VEC = kVec<T>;
   __shared__ float red[kThreads / 64][1];
   const int tid = threadIdx.x;
   const float inv = 1.f / (float)a.cols;
@@ -152,7 +164,8 @@ __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a)
     T* y = (T*)a.out + row * a.ld_out;
     float s[1] = {0.f}, v[VEC], w[VEC], b[VEC];
     for (int c = tid * VEC; c < a.cols; c += kThreads * VEC) {
-      load_vec<T, VEC>(x + c, v);
+      const int n = min(a.cols - c, VEC);
+      load_part<T, VEC, PART>(x + c, n, v);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += v[e];
     }
@@ -160,19 +173,21 @@ __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a)
     const float mean = s[0] * inv;
     s[0] = 0.f;
     for (int c = tid * VEC; c < a.cols; c += kThreads * VEC) {
-      load_vec<T, VEC>(x + c, v);
+      const int n = min(a.cols - c, VEC);
+      load_part<T, VEC, PART>(x + c, n, v);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s[0] = __builtin_fmaf(v[e] - mean, v[e] - mean, s[0]);
+      for (int e = 0; e < VEC; ++e) s[0] = !PART || e < n ? __builtin_fmaf(v[e] - mean, v[e] - mean, s[0]) : s[0];
     }
     row_sum<kThreads, 1>(s, red, tid);
     const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
     for (int c = tid * VEC; c < a.cols; c += kThreads * VEC) {
-      load_vec<T, VEC>(x + c, v);
-      load_param<P, VEC>(a.weight, c, w, 1.f);
-      load_param<P, VEC>(a.bias, c, b, 0.f);
+      const int n = min(a.cols - c, VEC);
+      load_part<T, VEC, PART>(x + c, n, v);
+      load_param<P, VEC, PART>(a.weight, c, n, w, 1.f);
+      load_param<P, VEC, PART>(a.bias, c, n, b, 0.f);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = __builtin_fmaf((v[e] - mean) * rstd, w[e], b[e]);
-      store_vec<T, VEC>(y + c, v);
+      store_part<T, VEC, PART>(y + c, n, v);
     }
     if (tid == 0) a.mean[row] = mean, a.rstd[row] = rstd;
   }
@@ -182,21 +197,22 @@ __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a)
 // As the forward pass; every thread also sums its columns of dw and db over
 // its rows, the rows of a block are added through LDS, and the block's sums
 // go to part[block] (fixed order: the result does not depend on timing).
-template <class T, class P, int VEC, int TPR, int NV>
+template <class T, class P, int TPR, int NV, bool PART>
 __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
+  constexpr int VEC = kVec<T>;
   constexpr int RPB = kThreads / TPR;
   __shared__ float red[kThreads / 64][2];
   __shared__ __align__(16) float cross[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * VEC : 1];
   const int tid = threadIdx.x, t = tid % TPR;
   float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
-  bool on[NV];
+  int on[NV];  // elements of each vector inside the row
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * TPR + t) * VEC;
-    on[i] = c < a.cols;
+    on[i] = min(max(a.cols - c, 0), VEC);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.f;
-    if (on[i]) load_param<P, VEC>(a.weight, c, w[i], 1.f);
+    if (on[i]) load_param<P, VEC, PART>(a.weight, c, on[i], w[i], 1.f);
   }
   const float inv = 1.f / (float)a.cols;
   const int64_t stride = (int64_t)gridDim.x * RPB;
@@ -211,8 +227,8 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) xh[i][e] = g[i][e] = 0.f;
       if (on[i]) {
-        load_vec<T, VEC>(x + (i * TPR + t) * VEC, xh[i]);
-        load_vec<T, VEC>(dy + (i * TPR + t) * VEC, g[i]);
+        load_part<T, VEC, PART>(x + (i * TPR + t) * VEC, on[i], xh[i]);
+        load_part<T, VEC, PART>(dy + (i * TPR + t) * VEC, on[i], g[i]);  // 0 past the row: nothing there counts
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           xh[i][e] = (xh[i][e] - mean) * rstd;
@@ -233,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
       if (!on[i]) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) g[i][e] = rstd * (g[i][e] - __builtin_fmaf(xh[i][e], c2, c1));
-      store_vec<T, VEC>(dx + (i * TPR + t) * VEC, g[i]);
+      store_part<T, VEC, PART>(dx + (i * TPR + t) * VEC, on[i], g[i]);
     }
   }
   if (!a.part) return;
@@ -257,15 +273,16 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) v[e] += cross[q][t * VEC + e];
       }
-      if (on[i]) store_vec<float, VEC>(part + (int64_t)k * a.cols + (i * TPR + t) * VEC, v);
+      if (on[i]) store_part<float, VEC, PART>(part + (int64_t)k * a.cols + (i * TPR + t) * VEC, on[i], v);
     }
 }
 
 // Rows of any length: a block takes rows in turn and adds their terms to its
 // own sums in memory (only this block and, for each column, only one thread
 // touches them).
-template <class T, class P, int VEC>
+template <class T, class P, bool PART>
 __global__ __launch_bounds__(kThreads) void norm_backward_long_kernel(NormArgs a) {
+  constexpr int VEC = kVec<T>;
   __shared__ float red[kThreads / 64][2];
   const int tid = threadIdx.x;
   const float inv = 1.f / (float)a.cols;
@@ -277,15 +294,16 @@ __global__ __launch_bounds__(kThreads) void norm_backward_long_kernel(NormArgs a
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s[2] = {0.f, 0.f}, v[VEC], g[VEC], w[VEC];
     for (int c = tid * VEC; c < a.cols; c += kThreads * VEC) {
-      load_vec<T, VEC>(x + c, v);
-      load_vec<T, VEC>(dy + c, g);
-      load_param<P, VEC>(a.weight, c, w, 1.f);
+      const int n = min(a.cols - c, VEC);
+      load_part<T, VEC, PART>(x + c, n, v);
+      load_part<T, VEC, PART>(dy + c, n, g);
+      load_param<P, VEC, PART>(a.weight, c, n, w, 1.f);
       float sw[VEC], sb[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sw[e] = sb[e] = 0.f;
       if (pw && !first) {
-        load_vec<float, VEC>(pw + c, sw);
-        load_vec<float, VEC>(pw + a.cols + c, sb);
+        load_part<float, VEC, PART>(pw + c, n, sw);
+        load_part<float, VEC, PART>(pw + a.cols + c, n, sb);
       }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -296,8 +314,8 @@ __global__ __launch_bounds__(kThreads) void norm_backward_long_kernel(NormArgs a
         s[1] = __builtin_fmaf(g[e] * w[e], xh, s[1]);
       }
       if (pw) {
-        store_vec<float, VEC>(pw + c, sw);
-        store_vec<float, VEC>(pw + a.cols + c, sb);
+        store_part<float, VEC, PART>(pw + c, n, sw);
+        store_part<float, VEC, PART>(pw + a.cols + c, n, sb);
       }
     }
     first = false;
@@ -306,15 +324,16 @@ __global__ __launch_bounds__(kThreads) void norm_backward_long_kernel(NormArgs a
     const float c1 = s[0] * inv, c2 = s[1] * inv;
     T* dx = (T*)a.out + row * a.ld_out;
     for (int c = tid * VEC; c < a.cols; c += kThreads * VEC) {
-      load_vec<T, VEC>(x + c, v);
-      load_vec<T, VEC>(dy + c, g);
-      load_param<P, VEC>(a.weight, c, w, 1.f);
+      const int n = min(a.cols - c, VEC);
+      load_part<T, VEC, PART>(x + c, n, v);
+      load_part<T, VEC, PART>(dy + c, n, g);
+      load_param<P, VEC, PART>(a.weight, c, n, w, 1.f);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float xh = (v[e] - mean) * rstd;
         v[e] = rstd * (g[e] * w[e] - __builtin_fmaf(xh, c2, c1));
       }
-      store_vec<T, VEC>(dx + c, v);
+      store_part<T, VEC, PART>(dx + c, n, v);
     }
   }
 }
@@ -342,71 +361,69 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormSumArgs a) {
 
 // ----------------------------------------------------------------- launch --
 // Rows a block holds at a time, by the row's length: a wave holds a row of up
-// to 2048 elements, a block one of up to 8192 (4096 where rows are not
-// aligned), and longer rows are read again instead of held.
-constexpr int kWaveCols = 2048, kBlockCols = 8192, kScalarWaveCols = 512, kScalarBlockCols = 4096;
+// to 2048 elements, a block one of up to 8192, and longer rows are read again
+// instead of held.
+constexpr int kWaveCols = 2048, kBlockCols = 8192;
 constexpr int kForwardBlocks = 2048;   // 8 a CU
 constexpr int kBackwardBlocks = 1024;  // 4 a CU
 
-template <class T, class P, int VEC, int TPR, int NV>
+template <class T, class P, bool PART, int TPR, int NV>
 hipError_t run_norm(const NormArgs& a, bool backward, hipStream_t s) {
-  if (backward) return launch_kernel(norm_backward_kernel<T, P, VEC, TPR, NV>, a.blocks, kThreads, a, s);
+  if (backward) return launch_kernel(norm_backward_kernel<T, P, TPR, NV, PART>, a.blocks, kThreads, a, s);
   const int64_t need = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
-  return launch_kernel(norm_forward_kernel<T, P, VEC, TPR, NV>, need < kForwardBlocks ? need : kForwardBlocks, kThreads,
-                       a, s);
+  return launch_kernel(norm_forward_kernel<T, P, TPR, NV, PART>, need < kForwardBlocks ? need : kForwardBlocks,
+                       kThreads, a, s);
 }
 
-template <class T, class P, int VEC, int TPR, int NV, int MAX>
+// The smallest power of two of vectors a thread, from NV to MAX, that holds a row.
+template <class T, class P, bool PART, int TPR, int NV, int MAX>
 hipError_t pick_nv(const NormArgs& a, bool backward, hipStream_t s) {
   if constexpr (NV >= MAX) {
-    return run_norm<T, P, VEC, TPR, MAX>(a, backward, s);
+    return run_norm<T, P, PART, TPR, MAX>(a, backward, s);
   } else {
-    if (a.cols <= TPR * VEC * NV) return run_norm<T, P, VEC, TPR, NV>(a, backward, s);
-    return pick_nv<T, P, VEC, TPR, NV * 2, MAX>(a, backward, s);
+    if (a.cols <= TPR * kVec<T> * NV) return run_norm<T, P, PART, TPR, NV>(a, backward, s);
+    return pick_nv<T, P, PART, TPR, NV * 2, MAX>(a, backward, s);
   }
 }
 
-template <class T, class P, bool V>
+template <class T, class P, bool PART>
 hipError_t launch_norm_as(const NormArgs& a, bool backward, hipStream_t s) {
-  constexpr int VEC = vec_of<T>(V);
-  constexpr int wave_cols = V ? kWaveCols : kScalarWaveCols, block_cols = V ? kBlockCols : kScalarBlockCols;
-  constexpr int wave_nv = wave_cols / 64 / VEC, block_first = 2 * wave_cols / kThreads / VEC,
-                block_nv = block_cols / kThreads / VEC;
-  if (a.cols <= wave_cols) return pick_nv<T, P, VEC, 64, 1, wave_nv>(a, backward, s);
-  if (a.cols <= block_cols) return pick_nv<T, P, VEC, kThreads, block_first, block_nv>(a, backward, s);
-  if (backward) return launch_kernel(norm_backward_long_kernel<T, P, VEC>, a.blocks, kThreads, a, s);
-  return launch_kernel(norm_forward_long_kernel<T, P, VEC>, a.rows < kForwardBlocks ? a.rows : kForwardBlocks, kThreads,
-                       a, s);
+  constexpr int V = kVec<T>, wave_nv = kWaveCols / 64 / V, block_first = 2 * kWaveCols / kThreads / V,
+                block_nv = kBlockCols / kThreads / V;
+  if (a.cols <= kWaveCols) return pick_nv<T, P, PART, 64, 1, wave_nv>(a, backward, s);
+  if (a.cols <= kBlockCols) return pick_nv<T, P, PART, kThreads, block_first, block_nv>(a, backward, s);
+  if (backward) return launch_kernel(norm_backward_long_kernel<T, P, PART>, a.blocks, kThreads, a, s);
+  return launch_kernel(norm_forward_long_kernel<T, P, PART>, a.rows < kForwardBlocks ? a.rows : kForwardBlocks,
+                       kThreads, a, s);
 }
 
-hipError_t launch_norm(const NormArgs& a, bool x_bf16, bool p_bf16, bool vec, bool backward, hipStream_t s) {
-  if (x_bf16) {
-    if (p_bf16) return vec ? launch_norm_as<__bf16, __bf16, true>(a, backward, s)
-                           : launch_norm_as<__bf16, __bf16, false>(a, backward, s);
-    return vec ? launch_norm_as<__bf16, float, true>(a, backward, s)
-               : launch_norm_as<__bf16, float, false>(a, backward, s);
-  }
-  if (p_bf16) return vec ? launch_norm_as<float, __bf16, true>(a, backward, s)
-                         : launch_norm_as<float, __bf16, false>(a, backward, s);
-  return vec ? launch_norm_as<float, float, true>(a, backward, s)
-             : launch_norm_as<float, float, false>(a, backward, s);
+template <class T, class P>
+hipError_t launch_norm_types(const NormArgs& a, bool backward, hipStream_t s) {
+  return a.cols % kVec<T> ? launch_norm_as<T, P, true>(a, backward, s) : launch_norm_as<T, P, false>(a, backward, s);
+}
+
+hipError_t launch_norm(const NormArgs& a, bool x_bf16, bool p_bf16, bool backward, hipStream_t s) {
+  if (x_bf16)
+    return p_bf16 ? launch_norm_types<__bf16, __bf16>(a, backward, s)
+                  : launch_norm_types<__bf16, float>(a, backward, s);
+  return p_bf16 ? launch_norm_types<float, __bf16>(a, backward, s) : launch_norm_types<float, float>(a, backward, s);
 }
 
 }  // namespace
 
 // Blocks of the backward pass, each writing one row of partial sums: as many
 // as hold a row each, at most 4 a CU.
-int norm_backward_blocks(int64_t rows, int64_t cols, bool vec) {
-  const int64_t rpb = cols <= (vec ? kWaveCols : kScalarWaveCols) ? kThreads / 64 : 1;
+int norm_backward_blocks(int64_t rows, int64_t cols) {
+  const int64_t rpb = cols <= kWaveCols ? kThreads / 64 : 1;
   const int64_t need = (rows + rpb - 1) / rpb;
   return (int)(need < kBackwardBlocks ? need : kBackwardBlocks);
 }
 
-hipError_t launch_norm_forward(const NormArgs& a, bool x_bf16, bool p_bf16, bool vec, hipStream_t stream) {
-  return launch_norm(a, x_bf16, p_bf16, vec, false, stream);
+hipError_t launch_norm_forward(const NormArgs& a, bool x_bf16, bool p_bf16, hipStream_t stream) {
+  return launch_norm(a, x_bf16, p_bf16, false, stream);
 }
-hipError_t launch_norm_backward(const NormArgs& a, bool x_bf16, bool p_bf16, bool vec, hipStream_t stream) {
-  return launch_norm(a, x_bf16, p_bf16, vec, true, stream);
+hipError_t launch_norm_backward(const NormArgs& a, bool x_bf16, bool p_bf16, hipStream_t stream) {
+  return launch_norm(a, x_bf16, p_bf16, true, stream);
 }
 hipError_t launch_norm_sum(const NormSumArgs& a, hipStream_t stream) {
   return launch_kernel(norm_sum_kernel, (2 * a.cols + 63) / 64, kSumThreads, a, stream);

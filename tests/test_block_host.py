@@ -72,12 +72,13 @@ def test_layer_norm_refuses_pointers(lib):
 
 
 def test_layer_norm_workspace_covers_every_kernel(lib):
-    """One row of 2 cols sums for each block; a block holds at least a row, and at most 1024 run."""
+    """One row of 2 cols sums for each block: a wave holds a row of up to 2048 elements, and at most 1024 blocks of
+    four waves run."""
     for rows in (0, 1, 5, 1023, 1024, 5000, 1 << 33):
         for cols in (1, 64, 1001, 1 << 20):
             need = lib.muon_layernorm_workspace_size(ctypes.byref(norm_desc(rows=rows, cols=cols)))
-            assert need >= max(min(rows, 1024) * 2 * cols * 4, 1)
-            assert need <= min(rows, 1024) * 2 * cols * 4 + 1024
+            blocks = min((rows + 3) // 4 if cols <= 2048 else rows, 1024)
+            assert max(blocks * 2 * cols * 4, 1) <= need <= blocks * 2 * cols * 4 + 1024
 
 
 def attn_desc(**kw):
