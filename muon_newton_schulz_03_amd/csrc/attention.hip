@@ -187,7 +187,8 @@ struct PairCopier {
     at = (const char*)((const T*)v.data + token * v.token + (w < 2 ? xhead : yhead) * v.head);
     left = rows;
   }
-  // `pair`: the two tiles.  Moves on to the next rows; past the last, tiles of zeros.
+  // `pair`: the two tiles.  Moves on by NG tiles; past the last row, tiles of zeros.
+  template <int NG>
   __device__ __forceinline__ void copy(char* pair, int w, int lane) {
     const uint32_t lds = lds_offset(pair + w * kN * 1024);
     if (left >= ROWS) {
@@ -201,8 +202,8 @@ struct PairCopier {
         dma_b128(rs, lds + 1024 * i,
                  (((w & 1) * kN + i) * 64 + lane) / Tiles<T, DP>::kCpr < left ? off[i] : kOob);
     }
-    at += ROWS * step;
-    left -= ROWS;
+    at += NG * ROWS * step;
+    left -= NG * ROWS;
   }
 };
 
@@ -242,6 +243,26 @@ __device__ __forceinline__ void store_row(T* row, const f32x16 (&acc)[DP / 32], 
       else
         *gv<f32x4>(row + d) = f32x4{a, b, c, e};
     }
+}
+
+// Adds the second group of waves' accumulators to the first's through LDS;
+// true in the second group, whose work is done.
+template <int DT>
+__device__ __forceinline__ bool join_groups(f32x16 (&acc)[DT], float* lds, int grp, int w, int lane) {
+  float* sum = lds + w * 16 * DT * 64 + lane;
+  wait_tiles();  // nothing is copied to or read from the tiles any more
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (grp) sum[(16 * t + i) * 64] = acc[t][i];
+  __syncthreads();
+  if (grp) return true;
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[t][i] += sum[(16 * t + i) * 64];
+  return false;
 }
 
 // Largest of / sum over the two lanes l, l ^ 32 that share a column.
@@ -388,7 +409,7 @@ __device__ __forceinline__ SeqTile block_tile(const AttnArgs& a, int i, int n, i
 template <class T>
 __device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0, int rows, int dim, int tid) {
   const int dw = dim * (int)sizeof(T) / 16;
-  for (int i = tid; i < rows * dw; i += kThreads) {
+  for (int i = tid; i < rows * dw; i += (int)blockDim.x) {
     T* p = (T*)v.data + (int64_t)(row0 + i / dw) * v.token + head * v.head;
     gv<u32x4>(p)[i % dw] = u32x4{0, 0, 0, 0};
   }
@@ -400,15 +421,15 @@ struct Cfg {
   static constexpr int kKeys = sizeof(T) == 2 ? (DP > 96 ? 64 : 64) : 32;  // rows of a streamed tile
 };
 
-template <class T, int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs a) {
+template <class T, int DP, int NG>
+__global__ __launch_bounds__(NG * kThreads, 2) void attention_forward_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
   constexpr int BM = 128, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
-  __shared__ __align__(256) char lds[2][2][kTile];
+  __shared__ __align__(256) char lds[NG][2][2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
   const SeqTile st =
       block_tile(a, (int)(blockIdx.x / a.q_heads), (int)(gridDim.x / a.q_heads), BM, lane, false);
@@ -421,7 +442,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
   }
   const int qw = st.row0 + 32 * w, qi = qw + col;
   const int wend = qw < st.len ? min(st.len, qw + 32) : 0;  // keys this wave looks at
-  const int ntile = (min(st.len, st.row0 + BM) + KT - 1) / KT;
+  const int ntile = (min(st.len, st.row0 + BM) + NG * KT - 1) / (NG * KT);  // of each group
   const float c = a.scale * kLog2e;
 
   Frag qf[ST];
@@ -434,13 +455,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
 
   PairCopier<T, DP, KT> cp;
   cp.init(a.k, a.v, a.dim, w, lane);
-  cp.seek(a.k, kvh, a.v, kvh, st.start, st.len, w);
-  cp.copy(lds[0][0], w, lane);
+  cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
+  cp.template copy<NG>(lds[grp][0][0], w, lane);
   wait_tiles();
   for (int kt = 0; kt < ntile; ++kt) {
-    const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
-    if (kt + 1 < ntile) cp.copy(lds[(kt + 1) & 1][0], w, lane);
-    if (kt * KT < wend) {
+    const char *kl = lds[grp][kt & 1][0], *vl = lds[grp][kt & 1][1];
+    const int k0 = (kt * NG + grp) * KT;  // first key of this group's tile
+    if (kt + 1 < ntile) cp.template copy<NG>(lds[grp][(kt + 1) & 1][0], w, lane);
+    if (k0 < wend) {
       f32x16 s[MT];
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
@@ -448,12 +470,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
 #pragma unroll
         for (int q = 0; q < ST; ++q) s[j] = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s[j]);
       }
-      if (kt * KT + KT - 1 > qw) {
+      if (k0 + KT - 1 > qw) {
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (kt * KT + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) s[j][i] = -__builtin_inff();
+            if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) s[j][i] = -__builtin_inff();
       }
       float top = s[0][0];
 #pragma unroll
@@ -492,6 +514,28 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
     wait_tiles();
   }
   l = halves_sum(l);
+  if constexpr (NG == 2) {  // the second group hands its sums to the first
+    float* sum = (float*)lds + w * (16 * DT + 2) * 64 + lane;
+    static_assert(4 * (16 * DT + 2) * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+    if (grp) {
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[(16 * t + i) * 64] = o[t][i];
+      sum[16 * DT * 64] = m;
+      sum[(16 * DT + 1) * 64] = l;
+    }
+    __syncthreads();
+    if (grp) return;
+    const float m2 = sum[16 * DT * 64], mn = fmaxf(m, m2);
+    const float f1 = __builtin_amdgcn_exp2f(m - mn), f2 = __builtin_amdgcn_exp2f(m2 - mn);
+    m = mn;
+    l = l * f1 + sum[(16 * DT + 1) * 64] * f2;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[t][i] = o[t][i] * f1 + sum[(16 * t + i) * 64] * f2;
+  }
   if (qi < st.len) {
     const int64_t tok = st.start + (int64_t)qi;
     store_row<T, DP>((T*)a.o.data + tok * a.o.token + head * a.o.head, o, 1.f / l, a.dim, h);
@@ -502,15 +546,15 @@ __global__ __launch_bounds__(kThreads, 2) void attention_forward_kernel(AttnArgs
 // ---------------------------------------------------------------- backward --
 // dQ; and for the next kernel delta and lse: in fp32, delta and lse / log 2;
 // in bf16, -delta and -lse / scale, from which it starts its products' sums.
-template <class T, int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
+template <class T, int DP, int NG>
+__global__ __launch_bounds__(NG * kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
   constexpr int BM = 128, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
-  __shared__ __align__(256) char lds[2][2][kTile];
+  __shared__ __align__(256) char lds[NG][2][2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
   const SeqTile st =
       block_tile(a, (int)(blockIdx.x / a.q_heads), (int)(gridDim.x / a.q_heads), BM, lane, false);
@@ -522,7 +566,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   }
   const int qw = st.row0 + 32 * w, qi = qw + col;
   const int wend = qw < st.len ? min(st.len, qw + 32) : 0;
-  const int ntile = (min(st.len, st.row0 + BM) + KT - 1) / KT;
+  const int ntile = (min(st.len, st.row0 + BM) + NG * KT - 1) / (NG * KT);
   const float c = a.scale * kLog2e;
   const bool valid = qi < st.len;
   const int64_t tok = st.start + (int64_t)qi;
@@ -545,7 +589,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     delta = halves_sum(delta);
     if (valid) {
       lse2 = a.lse[(int64_t)head * a.tokens + tok] * kLog2e;
-      if (h == 0) {
+      if (h == 0 && grp == 0) {
         const int64_t at = (int64_t)head * a.tokens + tok;
         a.delta[at] = sizeof(T) == 2 ? -delta : delta;
         a.lse2[at] = sizeof(T) == 2 ? -a.lse[at] / a.scale : lse2;
@@ -558,13 +602,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 
   PairCopier<T, DP, KT> cp;
   cp.init(a.k, a.v, a.dim, w, lane);
-  cp.seek(a.k, kvh, a.v, kvh, st.start, st.len, w);
-  cp.copy(lds[0][0], w, lane);
+  cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
+  cp.template copy<NG>(lds[grp][0][0], w, lane);
   wait_tiles();
   for (int kt = 0; kt < ntile; ++kt) {
-    const char *kl = lds[kt & 1][0], *vl = lds[kt & 1][1];
-    if (kt + 1 < ntile) cp.copy(lds[(kt + 1) & 1][0], w, lane);
-    if (kt * KT < wend) {
+    const char *kl = lds[grp][kt & 1][0], *vl = lds[grp][kt & 1][1];
+    const int k0 = (kt * NG + grp) * KT;
+    if (kt + 1 < ntile) cp.template copy<NG>(lds[grp][(kt + 1) & 1][0], w, lane);
+    if (k0 < wend) {
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         f32x16 s = f32x16{}, dp = f32x16{};
@@ -576,10 +621,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
-        if (kt * KT + 32 * j + 31 > qw) {
+        if (k0 + 32 * j + 31 > qw) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (kt * KT + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) ds[i] = 0.f;
+            if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) ds[i] = 0.f;
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -591,22 +636,26 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     }
     wait_tiles();
   }
+  if constexpr (NG == 2) {
+    if (join_groups<DT>(dq, (float*)lds, grp, w, lane)) return;
+    static_assert(4 * 16 * DT * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+  }
   if (valid) store_row<T, DP>((T*)a.dq.data + tok * a.dq.token + head * a.dq.head, dq, a.scale, a.dim, h);
 }
 
 // dK and dV of 128 keys of one key/value head, over the query heads of its
 // group (or of one part of it) and the query rows from the keys on, in fp32.
-template <int DP>
-__global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
+template <int DP, int NG>
+__global__ __launch_bounds__(NG * kThreads, NG == 2 || DP <= 32 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
   typedef float T;
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
   constexpr int BN = 128, QR = Cfg<T, DP>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = QR * Tl::kRow;
-  __shared__ __align__(256) char lds[2][2][kTile];
-  __shared__ __align__(256) float stat[2][2][64];  // lse2 and delta of the tile's rows
+  __shared__ __align__(256) char lds[NG][2][2][kTile];
+  __shared__ __align__(256) float stat[NG][2][2][64];  // lse2 and delta of the tile's rows
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
   const int per = a.kv_heads * a.splits;
   const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
   const SeqTile st = block_tile(a, (int)(blockIdx.x / per), (int)(gridDim.x / per), BN, lane, true);
@@ -634,21 +683,22 @@ __global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kern
   PairCopier<T, DP, QR> cp;
   cp.init(a.q, a.dout, a.dim, w, lane);
   auto copy = [&](int it) {
-    const int head = head0 + it / nq, row0 = (qt0 + it % nq) * QR, b = it & 1;
+    const int n = it * NG + grp, b = it & 1;
+    const int head = head0 + min(n / nq, hpp - 1), row0 = n < total ? (qt0 + n % nq) * QR : st.len;
     cp.seek(a.q, head, a.dout, head, st.start + (int64_t)row0, st.len - row0, w);
-    cp.copy(lds[b][0], w, lane);
+    cp.template copy<1>(lds[grp][b][0], w, lane);
     // rows past the end get zeros, which q and dout have there too: p = 1, ds = 0, and neither adds anything
     if (w < 2)
       dma_b32(buffer_of((w ? a.delta : a.lse2) + (int64_t)head * a.tokens + st.start + row0,
-                        4 * min(st.len - row0, QR)), lds_offset(stat[b][w]), 4 * lane);
+                        4 * min(st.len - row0, QR)), lds_offset(stat[grp][b][w]), 4 * lane);
   };
   copy(0);
   wait_tiles();
-  for (int it = 0; it < total; ++it) {
-    const char *ql = lds[it & 1][0], *dl = lds[it & 1][1];
-    const float *ll = stat[it & 1][0], *el = stat[it & 1][1];
-    const int q0 = (qt0 + it % nq) * QR;
-    if (it + 1 < total) copy(it + 1);
+  for (int it = 0; it * NG < total; ++it) {  // past the last tile: zeros, which add nothing
+    const char *ql = lds[grp][it & 1][0], *dl = lds[grp][it & 1][1];
+    const float *ll = stat[grp][it & 1][0], *el = stat[grp][it & 1][1];
+    const int q0 = (qt0 + (it * NG + grp) % nq) * QR;
+    if ((it + 1) * NG < total) copy(it + 1);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       if (q0 + 32 * j + 31 < kw) continue;  // rows before every key of this wave
@@ -686,6 +736,11 @@ __global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kern
     }
     wait_tiles();
   }
+  if constexpr (NG == 2) {
+    join_groups<DT>(dk, (float*)lds, grp, w, lane);
+    if (join_groups<DT>(dv, (float*)lds, grp, w, lane)) return;
+    static_assert(4 * 16 * DT * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+  }
   if (!valid) return;
   if (a.splits == 1) {
     store_row<T, DP>((T*)a.dk.data + tok * a.dk.token + kvh * a.dk.head, dk, a.scale, a.dim, h);
@@ -702,8 +757,8 @@ __global__ __launch_bounds__(kThreads, DP <= 32 ? 2 : 1) void attention_dkv_kern
 // p = exp2(c s) and ds = p dp.  Two blocks or three share a CU, as many waves a
 // SIMD: with head sizes above 64, V's fragments are read from LDS again and
 // again to fit the registers.
-template <int DP>
-__global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArgs a) {
+template <int DP, int NG>
+__global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(AttnArgs a) {
   typedef __bf16 T;
   typedef Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
@@ -711,9 +766,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
   constexpr int BN = 128, ST = DP / 16, DT = DP / 32, QR = DP <= 64 ? 64 : 32, kSlots = DP == 96 ? 4 : 2;
   typedef PairCopier<T, DP, QR> Pair;
   constexpr int kSlot = 2 * Pair::kTile + 512;  // Q rows, dO rows, and two words a row
-  __shared__ __align__(256) char ring[kSlots * kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
+  __shared__ __align__(256) char lds[NG * kSlots * kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
+  char* const ring = lds + grp * kSlots * kSlot;
   const int per = a.kv_heads * a.splits;
   const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
   const SeqTile st = block_tile(a, (int)(blockIdx.x / per), (int)(gridDim.x / per), BN, lane, true);
@@ -730,7 +786,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
   const float c = a.scale * kLog2e;
   const int hpp = a.group / a.splits, head0 = kvh * a.group + part * hpp;  // this block's query heads
 
-  char* const vt = ring + kSlots * kSlot;
+  char* const vt = lds + NG * kSlots * kSlot;
   Frag kf[ST], vf[kHoldV ? ST : 1];
   load_frags<T, DP>(kf, (const T*)a.k.data + tok * a.k.token + kvh * a.k.head, valid, a.dim, h);
   if constexpr (kHoldV) {
@@ -740,7 +796,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
     cv.init(a.v, a.v, a.dim, w, lane);
     cv.seek(a.v, kvh, a.v, kvh, st.start + (int64_t)st.row0 + (w < 2 ? 0 : BN / 2),
             st.len - st.row0 - (w < 2 ? 0 : BN / 2), w);
-    cv.copy(vt, w, lane);
+    if (grp == 0) cv.template copy<1>(vt, w, lane);
   }
   f32x16 dk[DT], dv[DT];
 #pragma unroll
@@ -749,31 +805,36 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
   // The rows to copy next: their slot, head and words (even waves copy the first, odd ones the second).
   Pair cp;
   cp.init(a.q, a.dout, a.dim, w, lane);
-  int cslot = 0, chead = head0;
+  int cslot = 0, chead = head0, crow = st.row0;
   const float* words;
+  auto next = [&](int& head, int& row) {
+    row += QR;
+    if (row >= st.len) row = st.row0, ++head;
+  };
   auto seek = [&]() {
-    const int64_t t0 = st.start + (int64_t)st.row0;
-    cp.seek(a.q, chead, a.dout, chead, t0, chead < head0 + hpp ? st.len - st.row0 : 0, w);
+    const int64_t t0 = st.start + (int64_t)crow;
+    cp.seek(a.q, chead, a.dout, chead, t0, chead < head0 + hpp ? st.len - crow : 0, w);
     words = (w & 1 ? a.delta : a.lse2) + (int64_t)chead * a.tokens + t0;
   };
   auto copy = [&]() {
     char* sl = ring + cslot * kSlot;
     dma_b32(buffer_of(words, 4 * max(min(cp.left, QR), 0)), lds_offset(sl + 2 * Pair::kTile + 256 * (w & 1)),
             4 * lane);
-    words += QR;
-    cp.copy(sl, w, lane);
+    words += NG * QR;
+    cp.template copy<NG>(sl, w, lane);
     cslot = (cslot + 1) & (kSlots - 1);
-    if (cp.left <= 0) {
-      ++chead;
-      seek();
-    }
+    const int head = chead;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) next(chead, crow);
+    if (chead != head) seek();
   };
+  int row = st.row0, rhead = head0;  // the rows in hand
+  if (grp) next(chead, crow), next(rhead, row);
   seek();
 #pragma unroll
   for (int i = 0; i < kSlots - 1; ++i) copy();
-  const int total = (st.len - st.row0 + QR - 1) / QR * hpp;
-  int row = st.row0;
-  for (int i = 0; i < total; ++i) {
+  const int total = ((st.len - st.row0 + QR - 1) / QR * hpp + NG - 1) / NG;
+  for (int i = 0; i < total; ++i) {  // a group's rows past the last: zeros, which add nothing
     wait_but<(kSlots - 2) * (Pair::kN + 1)>();
     copy();
     const char* sl = ring + (i & (kSlots - 1)) * kSlot;
@@ -796,10 +857,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
         else
           dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
       }
-      if (row < kw + 31) {  // a row before some key
+      if (row + j < kw + 31) {  // a row before some key
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (row + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
+          if (row + j + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
       }
       float p[16], ds[16];
 #pragma unroll
@@ -816,9 +877,14 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_bf16_kernel(AttnArg
           dk[t] = Elem<T>::mma(Tl::col_frag(ql, 16 * u, t, lane), sf, dk[t]);
         }
       }
-      row += 32;
     }
-    if (row >= st.len) row = st.row0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) next(rhead, row);
+  }
+  if constexpr (NG == 2) {
+    join_groups<DT>(dk, (float*)lds, grp, w, lane);
+    if (join_groups<DT>(dv, (float*)lds, grp, w, lane)) return;
+    static_assert(4 * 16 * DT * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
   }
   if (!valid) return;
   if (a.splits == 1) {
@@ -854,21 +920,36 @@ __global__ __launch_bounds__(kThreads) void attention_sum_kernel(AttnArgs a) {
   }
 }
 
+// Blocks of two groups of waves, which share a tile's streamed side and join
+// their sums, halve a block's run: worth it while the grid is about what the
+// 256 CUs hold at once and the longest block decides.  Forward and backward, 12
+// heads of 64 (one group / two): 4096 tokens 76 / 54 and 171 / 127 us; 8192
+// tokens (792 blocks) 157 / 135 and 419 / 414; 16 heads of 128, 8192 tokens
+// (1056 blocks) 281 / 295 and 927 / 948.  Short sequences only pay for the
+// join: 32 of 512 tokens 35 / 42 and 100 / 142.
+inline bool two_groups(const AttnArgs& a, int64_t blocks) {
+  return blocks <= 800 && a.tokens >= 256 * (int64_t)a.seqs;
+}
 template <class T, int DP>
 hipError_t forward_dp(const AttnArgs& a, hipStream_t stream) {
-  return launch_kernel(attention_forward_kernel<T, DP>, slots_of(a.tokens, a.seqs, 128) * a.q_heads, kThreads, a,
-                       stream);
+  const int64_t grid = slots_of(a.tokens, a.seqs, 128) * a.q_heads;
+  return two_groups(a, grid) ? launch_kernel(attention_forward_kernel<T, DP, 2>, grid, 2 * kThreads, a, stream)
+                    : launch_kernel(attention_forward_kernel<T, DP, 1>, grid, kThreads, a, stream);
 }
 
 template <class T, int DP>
 hipError_t backward_dp(const AttnArgs& a, hipStream_t stream) {
-  const int64_t slots = slots_of(a.tokens, a.seqs, 128);
-  hipError_t e = launch_kernel(attention_dq_kernel<T, DP>, slots * a.q_heads, kThreads, a, stream);
+  const int64_t slots = slots_of(a.tokens, a.seqs, 128), gq = slots * a.q_heads, gk = slots * a.kv_heads * a.splits;
+  hipError_t e = two_groups(a, gq) ? launch_kernel(attention_dq_kernel<T, DP, 2>, gq, 2 * kThreads, a, stream)
+                          : launch_kernel(attention_dq_kernel<T, DP, 1>, gq, kThreads, a, stream);
   if (e != hipSuccess) return e;
   if constexpr (sizeof(T) == 2)
-    e = launch_kernel(attention_dkv_bf16_kernel<DP>, slots * a.kv_heads * a.splits, kThreads, a, stream);
+    e = two_groups(a, gk) ? launch_kernel(attention_dkv_bf16_kernel<DP, 2>, gk, 2 * kThreads, a, stream)
+                 : launch_kernel(attention_dkv_bf16_kernel<DP, 1>, gk, kThreads, a, stream);
+  else if (DP <= 64 && two_groups(a, gk))  // more does not fit the registers of two waves a SIMD
+    e = launch_kernel(attention_dkv_kernel<DP <= 64 ? DP : 64, 2>, gk, 2 * kThreads, a, stream);
   else
-    e = launch_kernel(attention_dkv_kernel<DP>, slots * a.kv_heads * a.splits, kThreads, a, stream);
+    e = launch_kernel(attention_dkv_kernel<DP, 1>, gk, kThreads, a, stream);
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t blocks = (a.tokens * a.kv_heads * 2 * a.dim / 4 + kThreads - 1) / kThreads;
   return launch_kernel(attention_sum_kernel<T>, blocks < 4096 ? blocks : 4096, kThreads, a, stream);

@@ -169,8 +169,10 @@ def attention_case(lengths, heads, kv, dim, dtype, seed, scale=None, std=1.0, ta
     return worst
 
 
+# Sets of a mean of 256 tokens and more, in grids this small, take two groups of waves a block; the others take one.
 LENGTHS = [[1], [1, 1, 1], [2, 31, 32, 33], [63, 64, 65], [127, 128, 129], [0, 5, 0, 0, 300, 0], [257, 1, 190, 64],
-           [511], [640]]
+           [511], [640], [700, 20, 400],
+           [256, 3, 509]]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -217,6 +219,24 @@ def test_attention_rising_scores(dtype):
         grads = lib.packed_attention_backward(dd, qd, kd, vd, out, lse, cu)
         ref = R.attention(q, kk, v, [n], d ** -0.5, do)
         for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+            R.check(name, got, *ref[name])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+def test_attention_groups_of_waves(dim, dtype):
+    """The same tokens under both block shapes: alone (two groups), and with so many empty sequences behind them that
+    the grid takes one group.  Rounding differs, the bounds hold for both."""
+    lengths = [300, 470]
+    T = sum(lengths)
+    q, k, v, do = (randn((T, h, dim), 505 + i, dtype) for i, h in enumerate((4, 2, 2, 4)))
+    ref = R.attention(q, k, v, lengths, dim ** -0.5, do)
+    dev = [t.to(DEV) for t in (q, k, v, do)]
+    for extra in (0, 40):
+        cu = cu_of(lengths + [0] * extra)
+        out, lse = lib.packed_attention_forward(*dev[:3], cu)
+        g = lib.packed_attention_backward(dev[3], *dev[:3], out, lse, cu)
+        for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *g)):
             R.check(name, got, *ref[name])
 
 
