@@ -159,13 +159,13 @@ __device__ __forceinline__ void wait_but() {
 }
 
 // Copies ROWS rows at a time of two operands (K and V, or Q and dO) into a
-// pair of adjacent tiles.  Waves 0 and 1 copy the first operand, waves 2 and 3
-// the second, kN instructions each, so a wave keeps one pointer and one
-// resource, and waits can count instructions.
-template <class T, int DP, int ROWS>
+// pair of adjacent tiles.  The first half of a group's WR waves copies the
+// first operand, the other half the second, kN instructions each, so a wave
+// keeps one pointer and one resource, and waits can count instructions.
+template <class T, int DP, int ROWS, int WR>
 struct PairCopier {
-  static constexpr int kTile = ROWS * DP * (int)sizeof(T), kN = 2 * kTile / 1024 / (kThreads / 64);
-  static_assert(kN * kThreads * 16 == 2 * kTile, "whole instructions per wave");
+  static constexpr int kTile = ROWS * DP * (int)sizeof(T), kN = 2 * kTile / 1024 / WR, kHalf = WR / 2;
+  static_assert(kN * WR * 1024 == 2 * kTile, "whole instructions per wave");
   const char* at;           // the next row of this wave's operand
   int64_t step;             // bytes from row to row
   int left;                 // rows from there to the sequence's end
@@ -173,18 +173,18 @@ struct PairCopier {
   uint32_t off[kN];
   __device__ __forceinline__ void init(const HeadView& x, const HeadView& y, int dim, int w, int lane) {
     constexpr int cpr = Tiles<T, DP>::kCpr, kRow = Tiles<T, DP>::kRow;
-    step = (w < 2 ? x.token : y.token) * (int64_t)sizeof(T);
+    step = (w < kHalf ? x.token : y.token) * (int64_t)sizeof(T);
     row_bytes = dim * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int idx = ((w & 1) * kN + i) * 64 + lane, row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
+      const int idx = (w % kHalf * kN + i) * 64 + lane, row = idx / cpr, c = (idx % cpr) ^ swz<kRow>(row);
       off[i] = (uint32_t)c * 16 < row_bytes ? (uint32_t)(row * step) + 16u * c : kOob;
     }
   }
   __device__ __forceinline__ void seek(const HeadView& x, int xhead, const HeadView& y, int yhead, int64_t token,
                                        int rows, int w) {
-    const HeadView& v = w < 2 ? x : y;
-    at = (const char*)((const T*)v.data + token * v.token + (w < 2 ? xhead : yhead) * v.head);
+    const HeadView& v = w < kHalf ? x : y;
+    at = (const char*)((const T*)v.data + token * v.token + (w < kHalf ? xhead : yhead) * v.head);
     left = rows;
   }
   // `pair`: the two tiles.  Moves on by NG tiles; past the last row, tiles of zeros.
@@ -200,7 +200,7 @@ struct PairCopier {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
         dma_b128(rs, lds + 1024 * i,
-                 (((w & 1) * kN + i) * 64 + lane) / Tiles<T, DP>::kCpr < left ? off[i] : kOob);
+                 ((w % kHalf * kN + i) * 64 + lane) / Tiles<T, DP>::kCpr < left ? off[i] : kOob);
     }
     at += NG * ROWS * step;
     left -= NG * ROWS;
@@ -245,23 +245,29 @@ __device__ __forceinline__ void store_row(T* row, const f32x16 (&acc)[DP / 32], 
     }
 }
 
-// Adds the second group of waves' accumulators to the first's through LDS;
-// true in the second group, whose work is done.
-template <int DT>
+// Adds the other groups of waves' accumulators to the first's, in order,
+// through LDS (kJoin bytes); true in the others, whose work is done.
+template <int DT, int WR, int NG>
+constexpr int kJoin = (NG - 1) * WR * 16 * DT * 64 * 4;
+template <int WR, int NG, int DT>
 __device__ __forceinline__ bool join_groups(f32x16 (&acc)[DT], float* lds, int grp, int w, int lane) {
   float* sum = lds + w * 16 * DT * 64 + lane;
   wait_tiles();  // nothing is copied to or read from the tiles any more
+  if (grp) {
+    float* to = sum + (grp - 1) * WR * 16 * DT * 64;
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (grp) sum[(16 * t + i) * 64] = acc[t][i];
+      for (int i = 0; i < 16; ++i) to[(16 * t + i) * 64] = acc[t][i];
+  }
   __syncthreads();
   if (grp) return true;
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
+  for (int g = 0; g < NG - 1; ++g)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[t][i] += sum[(16 * t + i) * 64];
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[t][i] += sum[(g * WR * 16 * DT + 16 * t + i) * 64];
   return false;
 }
 
@@ -421,15 +427,15 @@ struct Cfg {
   static constexpr int kKeys = sizeof(T) == 2 ? (DP > 96 ? 64 : 64) : 32;  // rows of a streamed tile
 };
 
-template <class T, int DP, int NG>
-__global__ __launch_bounds__(NG * kThreads, 2) void attention_forward_kernel(AttnArgs a) {
+template <class T, int DP, int WR, int NG>
+__global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BM = 128, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BM = 32 * WR, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
   const SeqTile st =
       block_tile(a, (int)(blockIdx.x / a.q_heads), (int)(gridDim.x / a.q_heads), BM, lane, false);
@@ -453,7 +459,7 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_forward_kernel(Att
   for (int t = 0; t < DT; ++t) o[t] = f32x16{};
   float m = -__builtin_inff(), l = 0.f;
 
-  PairCopier<T, DP, KT> cp;
+  PairCopier<T, DP, KT, WR> cp;
   cp.init(a.k, a.v, a.dim, w, lane);
   cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
   cp.template copy<NG>(lds[grp][0][0], w, lane);
@@ -514,27 +520,32 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_forward_kernel(Att
     wait_tiles();
   }
   l = halves_sum(l);
-  if constexpr (NG == 2) {  // the second group hands its sums to the first
-    float* sum = (float*)lds + w * (16 * DT + 2) * 64 + lane;
-    static_assert(4 * (16 * DT + 2) * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+  if constexpr (NG > 1) {  // the other groups hand their sums to the first
+    constexpr int kOne = (16 * DT + 2) * 64;
+    static_assert((NG - 1) * WR * kOne * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+    float* sum = (float*)lds + w * kOne + lane;
     if (grp) {
+      float* to = sum + (grp - 1) * WR * kOne;
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[(16 * t + i) * 64] = o[t][i];
-      sum[16 * DT * 64] = m;
-      sum[(16 * DT + 1) * 64] = l;
+        for (int i = 0; i < 16; ++i) to[(16 * t + i) * 64] = o[t][i];
+      to[16 * DT * 64] = m;
+      to[(16 * DT + 1) * 64] = l;
     }
     __syncthreads();
     if (grp) return;
-    const float m2 = sum[16 * DT * 64], mn = fmaxf(m, m2);
-    const float f1 = __builtin_amdgcn_exp2f(m - mn), f2 = __builtin_amdgcn_exp2f(m2 - mn);
-    m = mn;
-    l = l * f1 + sum[(16 * DT + 1) * 64] * f2;
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
+    for (int g = 0; g < NG - 1; ++g, sum += WR * kOne) {
+      const float m2 = sum[16 * DT * 64], mn = fmaxf(m, m2);
+      const float f1 = __builtin_amdgcn_exp2f(m - mn), f2 = __builtin_amdgcn_exp2f(m2 - mn);
+      m = mn;
+      l = l * f1 + sum[(16 * DT + 1) * 64] * f2;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[t][i] = o[t][i] * f1 + sum[(16 * t + i) * 64] * f2;
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][i] = o[t][i] * f1 + sum[(16 * t + i) * 64] * f2;
+    }
   }
   if (qi < st.len) {
     const int64_t tok = st.start + (int64_t)qi;
@@ -546,15 +557,17 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_forward_kernel(Att
 // ---------------------------------------------------------------- backward --
 // dQ; and for the next kernel delta and lse: in fp32, delta and lse / log 2;
 // in bf16, -delta and -lse / scale, from which it starts its products' sums.
-template <class T, int DP, int NG>
-__global__ __launch_bounds__(NG * kThreads, 2) void attention_dq_kernel(AttnArgs a) {
+template <class T, int DP, int WR, int NG>
+__global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BM = 128, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BM = 32 * WR, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
+  constexpr bool kFix = sizeof(T) == 2;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
+  __shared__ float offs[NG][WR][kFix ? 64 : 1];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
   const SeqTile st =
       block_tile(a, (int)(blockIdx.x / a.q_heads), (int)(gridDim.x / a.q_heads), BM, lane, false);
@@ -589,73 +602,92 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dq_kernel(AttnArgs
     delta = halves_sum(delta);
     if (valid) {
       lse2 = a.lse[(int64_t)head * a.tokens + tok] * kLog2e;
-      if (h == 0 && grp == 0) {
-        const int64_t at = (int64_t)head * a.tokens + tok;
-        a.delta[at] = sizeof(T) == 2 ? -delta : delta;
-        a.lse2[at] = sizeof(T) == 2 ? -a.lse[at] / a.scale : lse2;
-      }
+      if (h == 0 && grp == 0) a.lse2[(int64_t)head * a.tokens + tok] = kFix ? -lse2 / c : lse2;
     }
   }
   f32x16 dq[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
-
-  PairCopier<T, DP, KT> cp;
+  PairCopier<T, DP, KT, WR> cp;
   cp.init(a.k, a.v, a.dim, w, lane);
-  cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
-  cp.template copy<NG>(lds[grp][0][0], w, lane);
-  wait_tiles();
-  for (int kt = 0; kt < ntile; ++kt) {
-    const char *kl = lds[grp][kt & 1][0], *vl = lds[grp][kt & 1][1];
-    const int k0 = (kt * NG + grp) * KT;
-    if (kt + 1 < ntile) cp.template copy<NG>(lds[grp][(kt + 1) & 1][0], w, lane);
-    if (k0 < wend) {
+  // out is rounded to bf16, and so delta is off; but the ds of a row must sum
+  // to zero, so their sum is the difference, and the exact delta goes to the
+  // next kernel.  In a sequence's first rows, where few terms average such
+  // errors, dq is made again with it.
+  for (int pass = kFix && st.row0 == 0 ? 0 : 1; pass < 2; ++pass) {
+    float off = 0.f;
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        f32x16 s = f32x16{}, dp = f32x16{};
+    for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
+    cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
+    cp.template copy<NG>(lds[grp][0][0], w, lane);
+    wait_tiles();
+    for (int kt = 0; kt < ntile; ++kt) {
+      const char *kl = lds[grp][kt & 1][0], *vl = lds[grp][kt & 1][1];
+      const int k0 = (kt * NG + grp) * KT;
+      if (kt + 1 < ntile) cp.template copy<NG>(lds[grp][(kt + 1) & 1][0], w, lane);
+      if (k0 < wend) {
 #pragma unroll
-        for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s);
+        for (int j = 0; j < MT; ++j) {
+          f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
-        for (int q = 0; q < ST; ++q) dp = Elem<T>::mma(Tl::row_frag(vl, 32 * j + col, q, h), df[q], dp);
-        float ds[16];
+          for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
-        if (k0 + 32 * j + 31 > qw) {
+          for (int q = 0; q < ST; ++q) dp = Elem<T>::mma(Tl::row_frag(vl, 32 * j + col, q, h), df[q], dp);
+          float ds[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) ds[i] = 0.f;
-        }
+            ds[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+          if (k0 + 32 * j + 31 > qw) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const Frag pf = Elem<T>::pack(ds + 8 * u);
+            for (int i = 0; i < 16; ++i)
+              if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) ds[i] = 0.f;
+          }
+          if constexpr (kFix) {
 #pragma unroll
-          for (int t = 0; t < DT; ++t) dq[t] = Elem<T>::mma(Tl::col_frag(kl, 32 * j + 16 * u, t, lane), pf, dq[t]);
+            for (int i = 0; i < 16; ++i) off += ds[i];
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const Frag pf = Elem<T>::pack(ds + 8 * u);
+#pragma unroll
+            for (int t = 0; t < DT; ++t) dq[t] = Elem<T>::mma(Tl::col_frag(kl, 32 * j + 16 * u, t, lane), pf, dq[t]);
+          }
         }
       }
+      wait_tiles();
     }
-    wait_tiles();
+    if constexpr (kFix) {
+      off = halves_sum(off);
+      if constexpr (NG > 1) {
+        offs[grp][w][lane] = off;
+        __syncthreads();
+        off = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) off += offs[g][w][lane];
+        __syncthreads();
+      }
+      delta += off;
+    }
   }
-  if constexpr (NG == 2) {
-    if (join_groups<DT>(dq, (float*)lds, grp, w, lane)) return;
-    static_assert(4 * 16 * DT * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+  if (valid && h == 0 && grp == 0) a.delta[(int64_t)head * a.tokens + tok] = kFix ? -delta : delta;
+  if constexpr (NG > 1) {
+    static_assert(kJoin<DT, WR, NG> <= sizeof(lds), "the sums fit the tiles");
+    if (join_groups<WR, NG>(dq, (float*)lds, grp, w, lane)) return;
   }
   if (valid) store_row<T, DP>((T*)a.dq.data + tok * a.dq.token + head * a.dq.head, dq, a.scale, a.dim, h);
 }
 
 // dK and dV of 128 keys of one key/value head, over the query heads of its
 // group (or of one part of it) and the query rows from the keys on, in fp32.
-template <int DP, int NG>
-__global__ __launch_bounds__(NG * kThreads, NG == 2 || DP <= 32 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
+template <int DP, int WR, int NG>
+__global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
   typedef float T;
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BN = 128, QR = Cfg<T, DP>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BN = 32 * WR, QR = Cfg<T, DP>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = QR * Tl::kRow;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
   __shared__ __align__(256) float stat[NG][2][2][64];  // lse2 and delta of the tile's rows
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   const int per = a.kv_heads * a.splits;
   const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
   const SeqTile st = block_tile(a, (int)(blockIdx.x / per), (int)(gridDim.x / per), BN, lane, true);
@@ -680,7 +712,7 @@ __global__ __launch_bounds__(NG * kThreads, NG == 2 || DP <= 32 ? 2 : 1) void at
   for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
 
   const int qt0 = st.row0 / QR, nq = (st.len + QR - 1) / QR - qt0, total = nq * hpp;
-  PairCopier<T, DP, QR> cp;
+  PairCopier<T, DP, QR, WR> cp;
   cp.init(a.q, a.dout, a.dim, w, lane);
   auto copy = [&](int it) {
     const int n = it * NG + grp, b = it & 1;
@@ -736,10 +768,10 @@ __global__ __launch_bounds__(NG * kThreads, NG == 2 || DP <= 32 ? 2 : 1) void at
     }
     wait_tiles();
   }
-  if constexpr (NG == 2) {
-    join_groups<DT>(dk, (float*)lds, grp, w, lane);
-    if (join_groups<DT>(dv, (float*)lds, grp, w, lane)) return;
-    static_assert(4 * 16 * DT * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+  if constexpr (NG > 1) {
+    static_assert(kJoin<DT, WR, NG> <= sizeof(lds), "the sums fit the tiles");
+    join_groups<WR, NG>(dk, (float*)lds, grp, w, lane);
+    if (join_groups<WR, NG>(dv, (float*)lds, grp, w, lane)) return;
   }
   if (!valid) return;
   if (a.splits == 1) {
@@ -763,12 +795,12 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
   typedef Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
   constexpr bool kHoldV = DP <= 64;
-  constexpr int BN = 128, ST = DP / 16, DT = DP / 32, QR = DP <= 64 ? 64 : 32, kSlots = DP == 96 ? 4 : 2;
-  typedef PairCopier<T, DP, QR> Pair;
+  constexpr int WR = 4, BN = 32 * WR, ST = DP / 16, DT = DP / 32, QR = DP <= 64 ? 64 : 32, kSlots = DP == 96 ? 4 : 2;
+  typedef PairCopier<T, DP, QR, WR> Pair;
   constexpr int kSlot = 2 * Pair::kTile + 512;  // Q rows, dO rows, and two words a row
   __shared__ __align__(256) char lds[NG * kSlots * kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) & 3, grp = __builtin_amdgcn_readfirstlane(tid >> 8);
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   char* const ring = lds + grp * kSlots * kSlot;
   const int per = a.kv_heads * a.splits;
   const int kvh = (int)(blockIdx.x % per) / a.splits, part = (int)(blockIdx.x % per) % a.splits;
@@ -792,7 +824,7 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
   if constexpr (kHoldV) {
     load_frags<T, DP>(vf, (const T*)a.v.data + tok * a.v.token + kvh * a.v.head, valid, a.dim, h);
   } else {  // two tiles of V's rows, by a copier of its own
-    PairCopier<T, DP, BN / 2> cv;
+    PairCopier<T, DP, BN / 2, WR> cv;
     cv.init(a.v, a.v, a.dim, w, lane);
     cv.seek(a.v, kvh, a.v, kvh, st.start + (int64_t)st.row0 + (w < 2 ? 0 : BN / 2),
             st.len - st.row0 - (w < 2 ? 0 : BN / 2), w);
@@ -881,10 +913,10 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
 #pragma unroll
     for (int g = 0; g < NG; ++g) next(rhead, row);
   }
-  if constexpr (NG == 2) {
-    join_groups<DT>(dk, (float*)lds, grp, w, lane);
-    if (join_groups<DT>(dv, (float*)lds, grp, w, lane)) return;
-    static_assert(4 * 16 * DT * 64 * sizeof(float) <= sizeof(lds), "the sums fit the tiles");
+  if constexpr (NG > 1) {
+    static_assert(kJoin<DT, WR, NG> <= sizeof(lds), "the sums fit the tiles");
+    join_groups<WR, NG>(dk, (float*)lds, grp, w, lane);
+    if (join_groups<WR, NG>(dv, (float*)lds, grp, w, lane)) return;
   }
   if (!valid) return;
   if (a.splits == 1) {
@@ -930,26 +962,44 @@ __global__ __launch_bounds__(kThreads) void attention_sum_kernel(AttnArgs a) {
 inline bool two_groups(const AttnArgs& a, int64_t blocks) {
   return blocks <= 800 && a.tokens >= 256 * (int64_t)a.seqs;
 }
+// fp32 products are 16 times slower than bf16 ones, so a block of 128 rows runs
+// long, and K and V need not be shared by as many rows: up to head size 64, a
+// block takes 64 rows and four groups of two waves (2048 tokens in 5
+// sequences, 12 heads of 64: forward and backward 71 and 226 us with 128 rows
+// and two groups, 43 and 138 with this).
+template <class T, int DP>
+constexpr bool kNarrow = sizeof(T) == 4 && DP <= 64;
+constexpr int64_t grid_of(const AttnArgs& a, int heads, int bm) { return slots_of(a.tokens, a.seqs, bm) * heads; }
+
 template <class T, int DP>
 hipError_t forward_dp(const AttnArgs& a, hipStream_t stream) {
-  const int64_t grid = slots_of(a.tokens, a.seqs, 128) * a.q_heads;
-  return two_groups(a, grid) ? launch_kernel(attention_forward_kernel<T, DP, 2>, grid, 2 * kThreads, a, stream)
-                    : launch_kernel(attention_forward_kernel<T, DP, 1>, grid, kThreads, a, stream);
+  if constexpr (kNarrow<T, DP>) {
+    return launch_kernel(attention_forward_kernel<T, DP, 2, 4>, grid_of(a, a.q_heads, 64), 512, a, stream);
+  } else {
+    const int64_t grid = grid_of(a, a.q_heads, 128);
+    return two_groups(a, grid) ? launch_kernel(attention_forward_kernel<T, DP, 4, 2>, grid, 512, a, stream)
+                               : launch_kernel(attention_forward_kernel<T, DP, 4, 1>, grid, 256, a, stream);
+  }
 }
 
 template <class T, int DP>
 hipError_t backward_dp(const AttnArgs& a, hipStream_t stream) {
-  const int64_t slots = slots_of(a.tokens, a.seqs, 128), gq = slots * a.q_heads, gk = slots * a.kv_heads * a.splits;
-  hipError_t e = two_groups(a, gq) ? launch_kernel(attention_dq_kernel<T, DP, 2>, gq, 2 * kThreads, a, stream)
-                          : launch_kernel(attention_dq_kernel<T, DP, 1>, gq, kThreads, a, stream);
-  if (e != hipSuccess) return e;
-  if constexpr (sizeof(T) == 2)
-    e = two_groups(a, gk) ? launch_kernel(attention_dkv_bf16_kernel<DP, 2>, gk, 2 * kThreads, a, stream)
-                 : launch_kernel(attention_dkv_bf16_kernel<DP, 1>, gk, kThreads, a, stream);
-  else if (DP <= 64 && two_groups(a, gk))  // more does not fit the registers of two waves a SIMD
-    e = launch_kernel(attention_dkv_kernel<DP <= 64 ? DP : 64, 2>, gk, 2 * kThreads, a, stream);
-  else
-    e = launch_kernel(attention_dkv_kernel<DP, 1>, gk, kThreads, a, stream);
+  hipError_t e;
+  if constexpr (kNarrow<T, DP>) {
+    e = launch_kernel(attention_dq_kernel<T, DP, 2, 4>, grid_of(a, a.q_heads, 64), 512, a, stream);
+    if (e == hipSuccess)
+      e = launch_kernel(attention_dkv_kernel<DP, 2, 4>, grid_of(a, a.kv_heads * a.splits, 64), 512, a, stream);
+  } else {
+    const int64_t gq = grid_of(a, a.q_heads, 128), gk = grid_of(a, a.kv_heads * a.splits, 128);
+    e = two_groups(a, gq) ? launch_kernel(attention_dq_kernel<T, DP, 4, 2>, gq, 512, a, stream)
+                          : launch_kernel(attention_dq_kernel<T, DP, 4, 1>, gq, 256, a, stream);
+    if (e != hipSuccess) return e;
+    if constexpr (sizeof(T) == 2)
+      e = two_groups(a, gk) ? launch_kernel(attention_dkv_bf16_kernel<DP, 2>, gk, 512, a, stream)
+                            : launch_kernel(attention_dkv_bf16_kernel<DP, 1>, gk, 256, a, stream);
+    else  // two groups do not fit the registers of two waves a SIMD
+      e = launch_kernel(attention_dkv_kernel<DP, 4, 1>, gk, 256, a, stream);
+  }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t blocks = (a.tokens * a.kv_heads * 2 * a.dim / 4 + kThreads - 1) / kThreads;
   return launch_kernel(attention_sum_kernel<T>, blocks < 4096 ? blocks : 4096, kThreads, a, stream);

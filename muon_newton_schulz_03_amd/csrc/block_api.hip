@@ -73,7 +73,7 @@ int check_attention(const muon_attention_desc* d) {
   if (!std::isfinite(d->scale) || !(d->scale > 0.f))
     return fail(MUON_E_INVAL, "attention: scale must be finite and positive");
   if (d->reserved != 0) return fail(MUON_E_INVAL, "attention: reserved field must be 0");
-  if ((d->tokens / 128 + d->seqs + 1) * (int64_t)d->q_heads > 0x7FFFFFFF)
+  if ((d->tokens / 64 + d->seqs + 1) * (int64_t)d->q_heads > 0x7FFFFFFF)
     return fail(MUON_E_UNSUPPORTED, "attention: %lld tokens, %d sequences and %d heads exceed one launch's grid",
                 (long long)d->tokens, d->seqs, d->q_heads);
   return MUON_OK;

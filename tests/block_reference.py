@@ -127,11 +127,16 @@ def attention(q, k, v, lengths, scale, dout=None, dtype=None):
             ds = p * (dp - delta)
             e_delta = (do.abs() * eo).sum(1, keepdim=True) + (D + 8) * U32 * (do.abs() * o.abs()).sum(1, keepdim=True)
             e_dp = ((D + 8) * U32 * (do.abs() @ vh.abs().T)).masked_fill(hidden, 0.0)
-            e_ds = 1.01 * (low * ds.abs() + (e_p + 4 * U32) * p * (dp.abs() + delta.abs()) + p * (e_dp + e_delta))
+            # dK's ds has delta corrected by the ds' own sum (zero by definition), and so has dQ's in the first 128 rows
+            e_base = low * ds.abs() + (e_p + 4 * U32) * p * (dp.abs() + delta.abs()) + p * e_dp
+            e_sum = (acc + e_p) * (p * (dp.abs() + delta.abs())).sum(1, keepdim=True) + (p * e_dp).sum(1, keepdim=True)
+            e_fixed = 1.01 * (e_base + p * (torch.minimum(e_sum, e_delta) if low else e_delta))
+            e_ds = 1.01 * (e_base + p * e_delta)
+            e_ds[:128] = e_fixed[:128]
             dq[r, h] = ds @ kh * scale
             e_dq[r, h] = scale * (1.01 * e_ds @ kh.abs() + acc * (ds.abs() @ kh.abs()))
             dk[r, g] += ds.T @ qh * scale
-            e_dk[r, g] += scale * (1.01 * e_ds.T @ qh.abs() + (H // G) * acc * (ds.abs().T @ qh.abs()))
+            e_dk[r, g] += scale * (1.01 * e_fixed.T @ qh.abs() + (H // G) * acc * (ds.abs().T @ qh.abs()))
             dv[r, g] += p.T @ do
             e_dv[r, g] += 1.01 * (low + e_p.amax() + (H // G) * acc) * (p.T @ do.abs())
     res = dict(out=(out, e_out), lse=(lse, e_lse))
