@@ -163,35 +163,41 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     return dx, dw, db
 
 
-def _heads(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> Heads:
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have shape (tokens, heads, head_dim)")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+def _heads(t: torch.Tensor, name: str, device, dtype, shape) -> Heads:
+    """The descriptor of a (tokens, heads, head_dim) operand after its checks."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} is not a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    token, head, elem = t.stride()
+    if elem != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    return Heads(t.data_ptr(), token, head)
 
 
 def _attention(q, k, v, cu_seqlens, scale):
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q is not a device tensor")
-    if q.dtype not in _DTYPES:
+    for name, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} is not a device tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have shape (tokens, heads, head_dim)")
+    dtype, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
+    if dtype not in _DTYPES:
         raise ValueError("q must be float32 or bfloat16")
-    hq = _heads(q, "q")
-    for name, t in (("k", k), ("v", v)):
-        _check(t, name, q.device, q.dtype)
-    hk, hv = _heads(k, "k"), _heads(v, "v", k)
-    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise ValueError(f"k has shape {tuple(k.shape)}, which does not go with q's {tuple(q.shape)}")
-    _check(cu_seqlens, "cu_seqlens", q.device, torch.int32)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+    if ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError(f"k has shape {tuple(ks)}, which does not go with q's {tuple(qs)}")
+    hq, hk, hv = _heads(q, "q", dev, dtype, qs), _heads(k, "k", dev, dtype, ks), _heads(v, "v", dev, dtype, ks)
+    _check(cu_seqlens, "cu_seqlens", dev, torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous vector of at least one offset")
-    dim = q.shape[2]
+    tokens, heads, dim = qs
     if scale is None:
         scale = 1.0 / math.sqrt(dim) if dim else 1.0
-    d = AttentionDesc(q.shape[0], cu_seqlens.numel() - 1, q.shape[1], k.shape[1], dim, _DTYPES[q.dtype], scale, 0)
-    return d, hq, hk, hv
+    return AttentionDesc(tokens, cu_seqlens.shape[0] - 1, heads, ks[1], dim, _DTYPES[dtype], scale, 0), hq, hk, hv
 
 
 def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
@@ -215,8 +221,7 @@ def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         if lse is None:
             lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
             flags |= _lib.ATTENTION_ZERO_LSE
-        _check(out, "out", dev, q.dtype)
-        ho = _heads(out, "out", q)
+        ho = _heads(out, "out", dev, q.dtype, q.shape)
         _check_lse(lse, q)
         _lib.check(lib.muon_attention_forward(
             ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
@@ -245,20 +250,18 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     lib = _lib.load()
     d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
     dev, flags = q.device, 0
-    _check(dout, "dout", dev, q.dtype)
-    _check(out, "out", dev, q.dtype)
     _check_lse(lse, q)
-    hdo, ho = _heads(dout, "dout", q), _heads(out, "out", q)
+    dtype, qs, ks = q.dtype, q.shape, k.shape
+    hdo, ho = _heads(dout, "dout", dev, dtype, qs), _heads(out, "out", dev, dtype, qs)
     with _On(dev):
         if dq is None:
-            dq, flags = q.new_empty(q.shape), flags | _lib.ATTENTION_ZERO_DQ
+            dq, flags = q.new_empty(qs), flags | _lib.ATTENTION_ZERO_DQ
         if dk is None:
-            dk, flags = k.new_empty(k.shape), flags | _lib.ATTENTION_ZERO_DK
+            dk, flags = q.new_empty(ks), flags | _lib.ATTENTION_ZERO_DK
         if dv is None:
-            dv, flags = k.new_empty(k.shape), flags | _lib.ATTENTION_ZERO_DV
-        for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-            _check(t, name, dev, q.dtype)
-        gq, gk, gv = _heads(dq, "dq", q), _heads(dk, "dk", k), _heads(dv, "dv", k)
+            dv, flags = q.new_empty(ks), flags | _lib.ATTENTION_ZERO_DV
+        gq, gk = _heads(dq, "dq", dev, dtype, qs), _heads(dk, "dk", dev, dtype, ks)
+        gv = _heads(dv, "dv", dev, dtype, ks)
         nbytes = lib.muon_attention_workspace_size(ctypes.byref(d))
         if nbytes == 0:
             raise _lib.MuonError(_lib.MUON_E_INVAL, _lib.last_error())

@@ -107,7 +107,7 @@ size_t attention_part_bytes(const muon_attention_desc* d, int splits) {
   return splits > 1 ? (size_t)splits * d->tokens * d->kv_heads * 2 * d->head_dim * sizeof(float) : 0;
 }
 int splits_of(const muon_attention_desc* d) {
-  return attention_splits(d->tokens, d->seqs, d->q_heads, d->kv_heads, d->head_dim, d->dtype == MUON_DTYPE_BF16);
+  return attention_splits(d->tokens, d->seqs, d->q_heads, d->kv_heads);
 }
 size_t attention_row_bytes(const muon_attention_desc* d) {  // one fp32 per query row
   return align_up((size_t)d->q_heads * d->tokens * sizeof(float));

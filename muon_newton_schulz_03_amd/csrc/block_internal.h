@@ -79,7 +79,7 @@ struct AttnArgs {
 enum { kZeroOut = 1, kZeroLse = 2 };               // AttnArgs::zero_tail, forward
 enum { kZeroDq = 1, kZeroDk = 2, kZeroDv = 4 };    // and backward
 
-int attention_splits(int64_t tokens, int seqs, int q_heads, int kv_heads, int dim, bool bf16);
+int attention_splits(int64_t tokens, int seqs, int q_heads, int kv_heads);
 hipError_t launch_attention_forward(const AttnArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_attention_backward(const AttnArgs& a, bool bf16, hipStream_t stream);
 
