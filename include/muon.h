@@ -333,8 +333,8 @@ int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, con
  * sequences' offsets; a sequence may be empty.  Token i of a sequence attends
  * to its tokens 0 .. i.  Query head h reads key/value head
  * h / (q_heads / kv_heads).  head_dim: a multiple of 8, at most 128.  dtype:
- * MUON_DTYPE_BF16 or MUON_DTYPE_F32, of every operand.  scale > 0 multiplies
- * the scores.
+ * MUON_DTYPE_BF16 or MUON_DTYPE_F32, of every operand.  scale, from 2^-60 to
+ * 2^60, multiplies the scores.
  *
  * cu_seqlens is not checked (it is read on the device); offsets outside
  * [0, tokens] are clamped and decreasing ones make empty sequences, so no
@@ -346,10 +346,12 @@ int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, con
  *
  * bf16: products take bf16 operands (probabilities and score gradients are
  * rounded to bf16 for theirs) and accumulate in fp32, where softmax
- * statistics are held.  fp32: fp32 throughout.  Keys and values are read in
- * tiles of up to 128 tokens, and masked ones get weight zero: a NaN or
- * infinity in a token's k or v can therefore reach the outputs of earlier
- * tokens of the same sequence (0 * Inf), but never another sequence. */
+ * statistics are held.  fp32: fp32 throughout.  A score of -inf has weight 0; a
+ * row of nothing else is NaN.  Rows are taken 128 at a time, and masked
+ * positions get weight zero: a NaN or infinity in a token's k or v can reach
+ * the outputs of up to 127 earlier tokens of the same sequence (0 * Inf), and
+ * one in its q or dout the dk and dv of as many later ones, but never another
+ * sequence. */
 typedef struct muon_attention_desc {
   int64_t tokens;
   int32_t seqs;

@@ -457,7 +457,7 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(Attn
   f32x16 o[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) o[t] = f32x16{};
-  float m = -__builtin_inff(), l = 0.f;
+  float m = -__FLT_MAX__, l = 0.f;  // not -inf: scores of -inf before the first finite one have weight 0, not NaN
 
   PairCopier<T, DP, KT, WR> cp;
   cp.init(a.k, a.v, a.dim, w, lane);

@@ -21,6 +21,7 @@ constexpr int64_t kMaxTokens = 0x7FFFFF00;
 constexpr int kMaxSeqs = 1 << 24;
 constexpr int kMaxHeads = 1 << 16;
 constexpr int kMaxDim = 128;
+constexpr float kMinScale = 0x1p-60f;  // lse / scale stays finite
 constexpr size_t kAlign = 256;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -70,8 +71,8 @@ int check_attention(const muon_attention_desc* d) {
     return fail(MUON_E_UNSUPPORTED, "attention: head_dim=%d must be a multiple of 8, at most %d", d->head_dim, kMaxDim);
   if (d->dtype != MUON_DTYPE_F32 && d->dtype != MUON_DTYPE_BF16)
     return fail(MUON_E_UNSUPPORTED, "attention: dtype %d unsupported", d->dtype);
-  if (!std::isfinite(d->scale) || !(d->scale > 0.f))
-    return fail(MUON_E_INVAL, "attention: scale must be finite and positive");
+  if (!(d->scale >= kMinScale && d->scale <= 1.f / kMinScale))
+    return fail(MUON_E_INVAL, "attention: scale %g outside [2^-60, 2^60]", d->scale);
   if (d->reserved != 0) return fail(MUON_E_INVAL, "attention: reserved field must be 0");
   if ((d->tokens / 64 + d->seqs + 1) * (int64_t)d->q_heads > 0x7FFFFFFF)
     return fail(MUON_E_UNSUPPORTED, "attention: %lld tokens, %d sequences and %d heads exceed one launch's grid",

@@ -96,7 +96,8 @@ BAD_ATTN = [(dict(tokens=-1), INVAL), (dict(tokens=1 << 31), INVAL), (dict(seqs=
             (dict(kv_heads=3), INVAL), (dict(q_heads=2, kv_heads=4), INVAL), (dict(q_heads=1 << 17), INVAL),
             (dict(head_dim=0), UNSUP), (dict(head_dim=-8), UNSUP), (dict(head_dim=68), UNSUP),
             (dict(head_dim=136), UNSUP), (dict(dtype=2), UNSUP), (dict(scale=0.0), INVAL), (dict(scale=-1.0), INVAL),
-            (dict(scale=math.nan), INVAL), (dict(scale=math.inf), INVAL), (dict(reserved=7), INVAL),
+            (dict(scale=math.nan), INVAL), (dict(scale=math.inf), INVAL), (dict(scale=2.0 ** -61), INVAL),
+            (dict(scale=2.0 ** 61), INVAL), (dict(reserved=7), INVAL),
             (dict(tokens=1 << 30, q_heads=1 << 14, kv_heads=1 << 14), UNSUP)]
 
 

@@ -352,6 +352,72 @@ def test_attention_broadcast_inputs(dtype):
         R.check(name, got, *ref[name])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_scores_of_minus_infinity_weigh_nothing(dtype):
+    """Keys whose scores are -inf for every query, from single ones to whole tiles and the sequence's first: the other
+    keys' softmax stands; a row that sees no other key is NaN."""
+    n, D = 300, 64
+    q, k, v = (randn((n, 1, D), 745 + i, dtype) for i in range(3))
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    for dead in ([0], list(range(64)), list(range(64, 128)) + [200], list(range(128))):
+        kk = k.clone()
+        kk[dead, :, 0] = float("-inf")
+        out, lse = lib.packed_attention_forward(q.to(DEV), kk.to(DEV), v.to(DEV), cu_of([n]))
+        live = torch.ones(n, dtype=torch.bool)
+        live[dead] = False
+        s = (q[:, 0].double() @ k[:, 0].double().T) * D ** -0.5
+        s = s.masked_fill(torch.ones(n, n, dtype=torch.bool).triu(1) | ~live[None], float("-inf"))
+        sees = live.cumsum(0) > 0
+        want = torch.softmax(s, 1) @ v[:, 0].double()
+        mass = torch.softmax(s, 1) @ v[:, 0].double().abs()
+        u = R.unit(dtype)
+        # p and the result rounded (bf16), and in fp32 the scores' sums of 64 terms and the sum over at most 300 keys
+        bound = u * want.abs() + ((u if dtype == BF else 0) + (64 + 300 + 64) * 2 * R.U32 * 8) * mass
+        R.check("out", out[sees.to(DEV), 0], want[sees], bound[sees])
+        assert torch.isnan(out[~sees.to(DEV)].float()).all()
+        assert (lse[0, ~sees.to(DEV)] == float("-inf")).all() and torch.isfinite(lse[0, sees.to(DEV)]).all()
+
+
+def test_binding_refuses_what_does_not_go_together():
+    x, w = torch.zeros(4, 64, device=DEV, dtype=BF), torch.ones(64, device=DEV)
+    y, mean, rstd = lib.layer_norm_forward(x, w)
+    bad = [lambda: lib.layer_norm_forward(x.half()), lambda: lib.layer_norm_forward(x, w[:32]),
+           lambda: lib.layer_norm_forward(x, w.cpu()), lambda: lib.layer_norm_forward(x, w, w.to(BF)),
+           lambda: lib.layer_norm_forward(x, w.half()), lambda: lib.layer_norm_forward(x, w, out=x.float()),
+           lambda: lib.layer_norm_forward(x, w, out=x[:2]), lambda: lib.layer_norm_forward(x.t()),
+           lambda: lib.layer_norm_forward(x[:1].expand(4, 64)), lambda: lib.layer_norm_forward(x, out=x[:1].expand(4, 64)),
+           lambda: lib.layer_norm_backward(x.float(), x, mean, rstd), lambda: lib.layer_norm_backward(x, x, mean[:2], rstd),
+           lambda: lib.layer_norm_backward(x, x, mean.to(BF), rstd),
+           lambda: lib.layer_norm_backward(x, x, mean, rstd, dx=x[:2])]
+    q, k = torch.zeros(10, 4, 64, device=DEV, dtype=BF), torch.zeros(10, 2, 64, device=DEV, dtype=BF)
+    cu = cu_of([10])
+    out, lse = lib.packed_attention_forward(q, k, k, cu)
+    f, b = lib.packed_attention_forward, lib.packed_attention_backward
+    bad += [lambda: f(q, k.float(), k, cu), lambda: f(q, k, k[:5], cu), lambda: f(q, k[:5], k[:5], cu),
+            lambda: f(q, k, k, cu.long()), lambda: f(q, k, k, cu.cpu()), lambda: f(q, k, k, cu[:0]),
+            lambda: f(q, k, k, cu.expand(2, 2)), lambda: f(q.half(), k.half(), k.half(), cu),
+            lambda: f(q.transpose(1, 2), k, k, cu), lambda: f(q[0], k[0], k[0], cu), lambda: f(q, k, k, cu, out=q[:5]),
+            lambda: f(q, k, k, cu, lse=lse.t()), lambda: f(q, k[..., :32], k[..., :32], cu),
+            lambda: f(q.cpu(), k, k, cu), lambda: b(q[:5], q, k, k, out, lse, cu),
+            lambda: b(q, q, k, k, out, lse[:2], cu), lambda: b(q, q, k, k, out, lse, cu, dk=q)]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+    x3, k3 = torch.zeros(10, 3, 64, device=DEV, dtype=BF), torch.zeros(10, 1, 64, device=DEV, dtype=BF)
+    errors = [lambda: lib.layer_norm_forward(x, out=x), lambda: lib.layer_norm_backward(x, x.clone(), mean, rstd, dx=x),
+              lambda: lib.layer_norm_forward(x, eps=-1.0), lambda: f(x3, k, k, cu), lambda: f(q, k, k, cu, out=q),
+              lambda: f(q, k, k, cu, scale=0.0), lambda: f(q[..., :60], k[..., :60], k[..., :60], cu),
+              lambda: f(q, k, k, cu, out=k3.expand(10, 4, 64)), lambda: b(q.clone(), q, k, k, out, lse, cu, dq=q),
+              lambda: b(q, q.clone(), k, k, out, lse, cu, dk=torch.zeros_like(k), dv=k)]
+    buf = torch.zeros(10 * 4 * 64 + 8, device=DEV, dtype=BF)
+    errors.append(lambda: f(buf[4:4 + 2560].view(10, 4, 64), k, k, cu))  # not at a multiple of 16 bytes
+    for i, call in enumerate(errors):
+        with pytest.raises(lib._lib.MuonError):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+
+
 def test_attention_offsets_past_32_bits():
     """Tokens 2^25 bytes apart: byte offsets pass 2^32 within one sequence."""
     n, D, step = 200, 64, 1 << 24
