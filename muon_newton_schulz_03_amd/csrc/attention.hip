@@ -7,6 +7,29 @@
 //   delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j
 //   dk_j = scale sum_{h in group, i >= j} ds_ij q_i,  dv_j = sum_{h in group, i >= j} p_ij do_i
+//
+// Design.
+//   * A block owns 128 rows of the side that is kept (queries for the output
+//     and dQ, keys for dK and dV), 32 a wave, as columns of 32x32 MFMA blocks:
+//     scores come out transposed, so a lane holds 16 scores of ONE row, row
+//     statistics are a lane's own (two lanes share a row), and the same
+//     registers, packed to bf16, are the right operand of the next product.
+//   * The other side streams through LDS in tiles, copied there directly;
+//     row-wise fragments are 16-byte reads and column-wise ones transposing
+//     reads, both without bank conflicts (SQ_LDS_BANK_CONFLICT is 0).
+//   * dQ has a kernel of its own and repeats the two score products (7
+//     products instead of 5): adding dQ from the other kernel would need
+//     atomics, whose order changes results.
+//   * Registers decide: one wave alone on a SIMD issues a vector operation
+//     every 3 ns, two or more every 1.2 ns, so every kernel is shaped to have
+//     two to four waves a SIMD.  Hand-pipelined versions with one wave, or a
+//     tile of scores ahead, were slower or no faster (dK/dV at heads of 128:
+//     757 us against 507 now).
+//   * What bounds the long bf16 runs: matrix and vector operations of the
+//     waves on a SIMD overlap in part; the MFMA units are busy 46 to 52% of
+//     the time (a library GEMM: 69%).  Rates on 8192 tokens, 16 query and 4
+//     key/value heads of 128: forward 978, dQ 1030, dK/dV 1085 TFLOP/s of their
+//     own products (library GEMM of 8192^3: 1410).
 #include "block_internal.h"
 #include "device_common.h"
 
@@ -15,7 +38,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;  // see softmax_tile
+constexpr float kLazy = 8.f;  // see the forward kernel's running maximum
 
 // ------------------------------------------------------------ element types --
 // A fragment is one lane's share of 16 contraction steps of a 32x32 product:
@@ -422,6 +445,17 @@ __device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0,
 }
 
 // ----------------------------------------------------------------- forward --
+// NG groups of WR waves: the block's rows are 32 WR, wave w of each group
+// holds rows 32 w .. +31, and the groups take the tiles of keys in turn, with
+// softmax statistics of their own that the first group joins at the end.
+//
+// One pass over the keys, with the running maximum and sum in registers (fp32);
+// p is rounded to bf16 for its product only (l sums the fp32 values).  Bound by
+// vector operations at heads of 64 (per 64 keys and 32 rows: 156 of them, 740
+// clocks, against 512 of MFMA; 64 keys at a time rather than 32: 67 and 82 us
+// on 16384 packed tokens) and by the overlap of both at 128.  Times: 16384
+// tokens in 24 sequences, 12 heads of 64: 61 us (640 TFLOP/s of the visible
+// pairs); 16384 tokens, 16/4 heads of 128: 1061 us (1036 TFLOP/s).
 template <class T, int DP>
 struct Cfg {
   static constexpr int kKeys = sizeof(T) == 2 ? (DP > 96 ? 64 : 64) : 32;  // rows of a streamed tile
@@ -557,6 +591,10 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(Attn
 // ---------------------------------------------------------------- backward --
 // dQ; and for the next kernel delta and lse: in fp32, delta and lse / log 2;
 // in bf16, -delta and -lse / scale, from which it starts its products' sums.
+// The forward kernel's layout, with dO's fragments in registers beside Q's and
+// no running maximum; ds is rounded to bf16 for its product.  Times: 16384
+// tokens in 24 sequences, 12 heads of 64: 87 us (676 TFLOP/s); 8192 tokens,
+// 16/4 heads of 128: 400 us (1030).
 template <class T, int DP, int WR, int NG>
 __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
@@ -675,8 +713,10 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs 
   if (valid) store_row<T, DP>((T*)a.dq.data + tok * a.dq.token + head * a.dq.head, dq, a.scale, a.dim, h);
 }
 
-// dK and dV of 128 keys of one key/value head, over the query heads of its
+// dK and dV of 32 WR keys of one key/value head, over the query heads of its
 // group (or of one part of it) and the query rows from the keys on, in fp32.
+// Bound by the fp32 MFMA (157 TFLOP/s): 2048 tokens in 5 sequences, 12 heads of
+// 64, 77 us with NG = 4 (MFMA busy 43%).
 template <int DP, int WR, int NG>
 __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
   typedef float T;
@@ -788,7 +828,9 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
 // into the products; their scores' sums start from -lse / scale and -delta, so
 // p = exp2(c s) and ds = p dp.  Two blocks or three share a CU, as many waves a
 // SIMD: with head sizes above 64, V's fragments are read from LDS again and
-// again to fit the registers.
+// again to fit the registers (held, they leave one wave a SIMD: 757 us on 8192
+// tokens, 16/4 heads of 128, against 507, 1085 TFLOP/s).  At heads of 64, 64
+// rows a step take 106 us on 16384 packed tokens, 32 rows 116.
 template <int DP, int NG>
 __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(AttnArgs a) {
   typedef __bf16 T;
@@ -930,6 +972,7 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
 }
 
 // Sums the parts of a split group in their order: part[split][token][kv head][dK, dV][dim].
+// Bound by memory: 4 parts of 8192 tokens and 4 heads of 128 (134 MB) in 22 us, 6.1 TB/s (most of it from the Infinity Cache).
 template <class T>
 __global__ __launch_bounds__(kThreads) void attention_sum_kernel(AttnArgs a) {
   const int per = a.kv_heads * 2 * a.dim / 4;  // groups of 4 elements a token

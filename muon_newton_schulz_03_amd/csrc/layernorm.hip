@@ -5,6 +5,12 @@
 //   dx = rstd (g - sum g / n - xh sum(g xh) / n),  dw = sum_rows dy xh,  db = sum_rows dy.
 // All arithmetic is fp32; the variance is the mean square of the centred
 // values, taken from registers, so a large common offset cancels nothing.
+//
+// Bound by memory: each operand moves once.  65536 x 768 in bf16: forward 37 us
+// (201 MB, 5.4 TB/s), backward 57 us (302 MB, 5.3 TB/s) and 4 us for the
+// parameter gradients' second stage, where a plain copy of 100 MB to 100 MB
+// reaches 7.1 TB/s from the Infinity Cache and one of 2 GiB 5.0; with inputs
+// that no cache holds, 51 us forward.
 #include "block_internal.h"
 #include "device_common.h"
 
@@ -97,7 +103,8 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*lds)[N], int tid)
 
 // ---------------------------------------------------------------- forward --
 // TPR threads hold a row of at most TPR * VEC * NV elements in registers and
-// stride over the rows, so the parameters are loaded once.
+// stride over the rows, so the parameters are loaded once.  A wave a row up to
+// 2048 elements: no barrier, and several rows in flight a SIMD.
 template <class T, class P, int TPR, int NV, bool PART>
 __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
   constexpr int VEC = kVec<T>;
