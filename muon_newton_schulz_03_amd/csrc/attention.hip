@@ -175,7 +175,8 @@ __device__ __forceinline__ void wait_tiles() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// The same with the wave's last N copies still in flight, and its LDS reads.
+// The same with the wave's last N copies still in flight.  (It waits for no LDS
+// read: those of the slot that is written next have long fed their products.)
 template <int N>
 __device__ __forceinline__ void wait_but() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -456,16 +457,16 @@ __device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0,
 // on 16384 packed tokens) and by the overlap of both at 128.  Times: 16384
 // tokens in 24 sequences, 12 heads of 64: 61 us (640 TFLOP/s of the visible
 // pairs); 16384 tokens, 16/4 heads of 128: 1061 us (1036 TFLOP/s).
-template <class T, int DP>
+template <class T>
 struct Cfg {
-  static constexpr int kKeys = sizeof(T) == 2 ? (DP > 96 ? 64 : 64) : 32;  // rows of a streamed tile
+  static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
 };
 
 template <class T, int DP, int WR, int NG>
 __global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BM = 32 * WR, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BM = 32 * WR, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
@@ -537,12 +538,13 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(Attn
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        float p[16];
+        float p[16], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -m));
-          l += p[i];
+          sum += p[i];
         }
+        l += sum;  // 16 at a time: the error of a long sum grows with its number of additions
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const Frag pf = Elem<T>::pack(p + 8 * u);
@@ -599,7 +601,7 @@ template <class T, int DP, int WR, int NG>
 __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BM = 32 * WR, KT = Cfg<T, DP>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BM = 32 * WR, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   constexpr bool kFix = sizeof(T) == 2;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
@@ -679,8 +681,10 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs 
               if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) ds[i] = 0.f;
           }
           if constexpr (kFix) {
+            float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) off += ds[i];
+            for (int i = 0; i < 16; ++i) sum += ds[i];
+            off += sum;
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -722,7 +726,7 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
   typedef float T;
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
-  constexpr int BN = 32 * WR, QR = Cfg<T, DP>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
+  constexpr int BN = 32 * WR, QR = Cfg<T>::kKeys, MT = QR / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = QR * Tl::kRow;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
   __shared__ __align__(256) float stat[NG][2][2][64];  // lse2 and delta of the tile's rows
