@@ -70,6 +70,22 @@ __device__ __forceinline__ void store_part(T* p, int n, const float* v) {
   for (int e = 0; e < N; ++e)
     if (e < n) *gv<T>(p + e) = (T)v[e];
 }
+// A vector as it was loaded, converted when it is wanted.
+template <class T, int N, bool PART>
+struct Held {
+  float v[N];
+  __device__ __forceinline__ void load(const T* p, int n) { load_part<T, N, PART>(p, n, v); }
+  __device__ __forceinline__ void get(float* out) const {
+#pragma unroll
+    for (int e = 0; e < N; ++e) out[e] = v[e];
+  }
+};
+template <int N>
+struct Held<__bf16, N, false> {
+  u32x4 r;
+  __device__ __forceinline__ void load(const __bf16* p, int) { r = *gv<u32x4_any>(p); }
+  __device__ __forceinline__ void get(float* out) const { unpack8_bf16(r, out); }
+};
 // Parameters are bf16 or fp32 independently of the activations.
 template <class P, int N, bool PART>
 __device__ __forceinline__ void load_param(const void* p, int64_t at, int n, float* v, float none) {
@@ -123,15 +139,27 @@ __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
   }
   const float inv = 1.f / (float)a.cols;
   const int64_t stride = (int64_t)gridDim.x * (kThreads / TPR);
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + tid / TPR; row < a.rows; row += stride) {
+  const int64_t first = (int64_t)blockIdx.x * (kThreads / TPR) + tid / TPR;
+  Held<T, VEC, PART> next[NV];  // the row after this one is on its way
+  auto fetch = [&](int64_t row) {
     const T* x = (const T*)a.x + row * a.ld_x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (on[i] && row < a.rows) next[i].load(x + (i * TPR + t) * VEC, on[i]);
+  };
+  fetch(first);
+  for (int64_t row = first; row < a.rows; row += stride) {
     float v[NV][VEC];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-      if (on[i]) load_part<T, VEC, PART>(x + (i * TPR + t) * VEC, on[i], v[i]);
+      if (on[i]) next[i].get(v[i]);
+    }
+    fetch(row + stride);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += v[i][e];
     }
@@ -205,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a)
 // its rows, the rows of a block are added through LDS, and the block's sums
 // go to part[block] (fixed order: the result does not depend on timing).
 template <class T, class P, int TPR, int NV, bool PART>
-__global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
+__global__ __launch_bounds__(kThreads, kVec<T> * NV <= 16 && !PART ? 4 : 1) void norm_backward_kernel(NormArgs a) {
   constexpr int VEC = kVec<T>;
   constexpr int RPB = kThreads / TPR;
   __shared__ float red[kThreads / 64][2];
@@ -223,19 +251,36 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(NormArgs a) {
   }
   const float inv = 1.f / (float)a.cols;
   const int64_t stride = (int64_t)gridDim.x * RPB;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + tid / TPR; row < a.rows; row += stride) {
+  const int64_t first = (int64_t)blockIdx.x * RPB + tid / TPR;
+  Held<T, VEC, PART> nx[NV], ny[NV];  // the row after this one is on its way
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](int64_t row) {
     const T* x = (const T*)a.x + row * a.ld_x;
     const T* dy = (const T*)a.dy + row * a.ld_dy;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    if (row >= a.rows) return;
+    nmean = a.mean[row], nrstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (on[i]) {
+        nx[i].load(x + (i * TPR + t) * VEC, on[i]);
+        ny[i].load(dy + (i * TPR + t) * VEC, on[i]);  // 0 past the row: nothing there counts
+      }
+  };
+  fetch(first);
+  for (int64_t row = first; row < a.rows; row += stride) {
+    const float mean = nmean, rstd = nrstd;
     float xh[NV][VEC], g[NV][VEC];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) xh[i][e] = g[i][e] = 0.f;
+      if (on[i]) nx[i].get(xh[i]), ny[i].get(g[i]);
+    }
+    fetch(row + stride);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
       if (on[i]) {
-        load_part<T, VEC, PART>(x + (i * TPR + t) * VEC, on[i], xh[i]);
-        load_part<T, VEC, PART>(dy + (i * TPR + t) * VEC, on[i], g[i]);  // 0 past the row: nothing there counts
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           xh[i][e] = (xh[i][e] - mean) * rstd;
@@ -374,7 +419,7 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormSumArgs a) {
 // to 2048 elements, a block one of up to 8192, and longer rows are read again
 // instead of held.
 constexpr int kWaveCols = 2048, kBlockCols = 8192;
-constexpr int kForwardBlocks = 2048;   // 8 a CU
+constexpr int kForwardBlocks = 1024;   // 4 a CU
 constexpr int kBackwardBlocks = 1024;  // 4 a CU
 
 template <class T, class P, bool PART, int TPR, int NV>
