@@ -6,11 +6,11 @@
 // All arithmetic is fp32; the variance is the mean square of the centred
 // values, taken from registers, so a large common offset cancels nothing.
 //
-// Bound by memory: each operand moves once.  65536 x 768 in bf16: forward 37 us
-// (201 MB, 5.4 TB/s), backward 57 us (302 MB, 5.3 TB/s) and 4 us for the
+// Bound by memory: each operand moves once.  65536 x 768 in bf16: forward 34 us
+// (201 MB, 5.9 TB/s), backward 53 us (302 MB, 5.7 TB/s) and 4 us for the
 // parameter gradients' second stage, where a plain copy of 100 MB to 100 MB
 // reaches 7.1 TB/s from the Infinity Cache and one of 2 GiB 5.0; with inputs
-// that no cache holds, 51 us forward.
+// that no cache holds, 46 us forward.
 #include "block_internal.h"
 #include "device_common.h"
 
@@ -70,22 +70,15 @@ __device__ __forceinline__ void store_part(T* p, int n, const float* v) {
   for (int e = 0; e < N; ++e)
     if (e < n) *gv<T>(p + e) = (T)v[e];
 }
-// A vector as it was loaded, converted when it is wanted.
-template <class T, int N, bool PART>
-struct Held {
-  float v[N];
-  __device__ __forceinline__ void load(const T* p, int n) { load_part<T, N, PART>(p, n, v); }
-  __device__ __forceinline__ void get(float* out) const {
-#pragma unroll
-    for (int e = 0; e < N; ++e) out[e] = v[e];
-  }
-};
-template <int N>
-struct Held<__bf16, N, false> {
-  u32x4 r;
-  __device__ __forceinline__ void load(const __bf16* p, int) { r = *gv<u32x4_any>(p); }
-  __device__ __forceinline__ void get(float* out) const { unpack8_bf16(r, out); }
-};
+// Whether a row's loads are started while the row before is summed.  bf16 rows
+// of whole vectors, forward / backward without it and with it: 65536 x 768
+// 47 / 61 and 40 / 59 us, 8192 x 8192 72 / 119 and 65 / 100, 16384 x 2048
+// 31 / 58 and 28 / 46; 16384 x 1536 19 / 46 and 21 / 37.  With rows of fp32 or
+// of odd lengths the held row takes registers or branches that cost more than
+// the wait: backward 44 and 59 us for 16384 x 1024 in fp32, 94 and 154 for
+// 65536 x 770 in bf16.
+template <class T, bool PART>
+constexpr bool kAhead = sizeof(T) == 2 && !PART;
 // Parameters are bf16 or fp32 independently of the activations.
 template <class P, int N, bool PART>
 __device__ __forceinline__ void load_param(const void* p, int64_t at, int n, float* v, float none) {
@@ -120,10 +113,13 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*lds)[N], int tid)
 // ---------------------------------------------------------------- forward --
 // TPR threads hold a row of at most TPR * VEC * NV elements in registers and
 // stride over the rows, so the parameters are loaded once.  A wave a row up to
-// 2048 elements: no barrier, and several rows in flight a SIMD.
+// 2048 elements: no barrier, and several rows in flight a SIMD.  Blocks: 1024
+// instead of 2048 take the same 40 us for 65536 x 768 and 80 instead of 65 for
+// 8192 x 8192.
 template <class T, class P, int TPR, int NV, bool PART>
 __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
   constexpr int VEC = kVec<T>;
+  constexpr bool AHEAD = kAhead<T, PART>;
   __shared__ float red[kThreads / 64][1];
   const int tid = threadIdx.x, t = tid % TPR;
   float w[NV][VEC], b[NV][VEC];
@@ -140,29 +136,31 @@ __global__ __launch_bounds__(kThreads) void norm_forward_kernel(NormArgs a) {
   const float inv = 1.f / (float)a.cols;
   const int64_t stride = (int64_t)gridDim.x * (kThreads / TPR);
   const int64_t first = (int64_t)blockIdx.x * (kThreads / TPR) + tid / TPR;
-  Held<T, VEC, PART> next[NV];  // the row after this one is on its way
+  u32x4 next[NV];  // AHEAD: the row after this one, as it was loaded
   auto fetch = [&](int64_t row) {
     const T* x = (const T*)a.x + row * a.ld_x;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (on[i] && row < a.rows) next[i].load(x + (i * TPR + t) * VEC, on[i]);
+      if (on[i] && row < a.rows) next[i] = *gv<u32x4_any>(x + (i * TPR + t) * VEC);
   };
-  fetch(first);
+  if constexpr (AHEAD) fetch(first);
   for (int64_t row = first; row < a.rows; row += stride) {
+    const T* x = (const T*)a.x + row * a.ld_x;
     float v[NV][VEC];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-      if (on[i]) next[i].get(v[i]);
+      if (!on[i]) continue;
+      if constexpr (AHEAD) unpack8_bf16(next[i], v[i]);
+      else load_part<T, VEC, PART>(x + (i * TPR + t) * VEC, on[i], v[i]);
     }
-    fetch(row + stride);
+    if constexpr (AHEAD) fetch(row + stride);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s[0] += v[i][e];
-    }
     row_sum<TPR, 1>(s, red, tid);
     const float mean = s[0] * inv;
     s[0] = 0.f;
@@ -233,9 +231,10 @@ __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a)
 // its rows, the rows of a block are added through LDS, and the block's sums
 // go to part[block] (fixed order: the result does not depend on timing).
 template <class T, class P, int TPR, int NV, bool PART>
-__global__ __launch_bounds__(kThreads, kVec<T> * NV <= 16 && !PART ? 4 : 1) void norm_backward_kernel(NormArgs a) {
+__global__ __launch_bounds__(kThreads, (kAhead<T, PART> && NV <= 2 ? 4 : 1)) void norm_backward_kernel(NormArgs a) {
   constexpr int VEC = kVec<T>;
   constexpr int RPB = kThreads / TPR;
+  constexpr bool AHEAD = kAhead<T, PART>;
   __shared__ float red[kThreads / 64][2];
   __shared__ __align__(16) float cross[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * VEC : 1];
   const int tid = threadIdx.x, t = tid % TPR;
@@ -252,44 +251,52 @@ __global__ __launch_bounds__(kThreads, kVec<T> * NV <= 16 && !PART ? 4 : 1) void
   const float inv = 1.f / (float)a.cols;
   const int64_t stride = (int64_t)gridDim.x * RPB;
   const int64_t first = (int64_t)blockIdx.x * RPB + tid / TPR;
-  Held<T, VEC, PART> nx[NV], ny[NV];  // the row after this one is on its way
+  u32x4 nx[NV], ny[NV];  // AHEAD: the row after this one, as it was loaded
   float nmean = 0.f, nrstd = 0.f;
   auto fetch = [&](int64_t row) {
+    if (row >= a.rows) return;
     const T* x = (const T*)a.x + row * a.ld_x;
     const T* dy = (const T*)a.dy + row * a.ld_dy;
-    if (row >= a.rows) return;
     nmean = a.mean[row], nrstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (on[i]) {
-        nx[i].load(x + (i * TPR + t) * VEC, on[i]);
-        ny[i].load(dy + (i * TPR + t) * VEC, on[i]);  // 0 past the row: nothing there counts
+        nx[i] = *gv<u32x4_any>(x + (i * TPR + t) * VEC);
+        ny[i] = *gv<u32x4_any>(dy + (i * TPR + t) * VEC);
       }
   };
-  fetch(first);
+  if constexpr (AHEAD) fetch(first);
   for (int64_t row = first; row < a.rows; row += stride) {
-    const float mean = nmean, rstd = nrstd;
+    const T* x = (const T*)a.x + row * a.ld_x;
+    const T* dy = (const T*)a.dy + row * a.ld_dy;
+    const float mean = AHEAD ? nmean : a.mean[row], rstd = AHEAD ? nrstd : a.rstd[row];
     float xh[NV][VEC], g[NV][VEC];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) xh[i][e] = g[i][e] = 0.f;
-      if (on[i]) nx[i].get(xh[i]), ny[i].get(g[i]);
+      if (!on[i]) continue;
+      if constexpr (AHEAD) {
+        unpack8_bf16(nx[i], xh[i]);
+        unpack8_bf16(ny[i], g[i]);
+      } else {
+        load_part<T, VEC, PART>(x + (i * TPR + t) * VEC, on[i], xh[i]);
+        load_part<T, VEC, PART>(dy + (i * TPR + t) * VEC, on[i], g[i]);  // 0 past the row: nothing there counts
+      }
     }
-    fetch(row + stride);
+    if constexpr (AHEAD) fetch(row + stride);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (on[i]) {
+      if (!on[i]) continue;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          xh[i][e] = (xh[i][e] - mean) * rstd;
-          dw[i][e] = __builtin_fmaf(g[i][e], xh[i][e], dw[i][e]);
-          db[i][e] += g[i][e];
-          g[i][e] *= w[i][e];
-          s[0] += g[i][e];
-          s[1] = __builtin_fmaf(g[i][e], xh[i][e], s[1]);
-        }
+      for (int e = 0; e < VEC; ++e) {
+        xh[i][e] = (xh[i][e] - mean) * rstd;
+        dw[i][e] = __builtin_fmaf(g[i][e], xh[i][e], dw[i][e]);
+        db[i][e] += g[i][e];
+        g[i][e] *= w[i][e];
+        s[0] += g[i][e];
+        s[1] = __builtin_fmaf(g[i][e], xh[i][e], s[1]);
       }
     }
     if (!a.out) continue;
@@ -419,7 +426,7 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(NormSumArgs a) {
 // to 2048 elements, a block one of up to 8192, and longer rows are read again
 // instead of held.
 constexpr int kWaveCols = 2048, kBlockCols = 8192;
-constexpr int kForwardBlocks = 1024;   // 4 a CU
+constexpr int kForwardBlocks = 2048;   // 8 a CU
 constexpr int kBackwardBlocks = 1024;  // 4 a CU
 
 template <class T, class P, bool PART, int TPR, int NV>
