@@ -6,11 +6,11 @@
 // All arithmetic is fp32; the variance is the mean square of the centred
 // values, taken from registers, so a large common offset cancels nothing.
 //
-// Bound by memory: each operand moves once.  65536 x 768 in bf16: forward 34 us
-// (201 MB, 5.9 TB/s), backward 53 us (302 MB, 5.7 TB/s) and 4 us for the
+// Bound by memory: each operand moves once.  65536 x 768 in bf16: forward 35 us
+// (201 MB, 5.7 TB/s), backward 53 us (302 MB, 5.7 TB/s) and 4 us for the
 // parameter gradients' second stage, where a plain copy of 100 MB to 100 MB
 // reaches 7.1 TB/s from the Infinity Cache and one of 2 GiB 5.0; with inputs
-// that no cache holds, 46 us forward.
+// that no cache holds, 44 us forward.
 #include "block_internal.h"
 #include "device_common.h"
 
