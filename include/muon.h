@@ -312,7 +312,8 @@ typedef struct muon_layernorm_desc {
 
 /* y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps), with the
  * row's mean and biased variance; mean[rows] and rstd[rows] (fp32) are written
- * for the backward call.  y must not be x.  rows == 0 does nothing. */
+ * for the backward call.  y and x may be columns of one buffer, but share no
+ * element.  rows == 0 does nothing. */
 int muon_layernorm_forward(const muon_layernorm_desc* desc, const void* x, const void* weight, const void* bias,
                            void* y, float* mean, float* rstd, void* hip_stream);
 
@@ -322,7 +323,7 @@ size_t muon_layernorm_workspace_size(const muon_layernorm_desc* desc);
 
 /* Gradients of the forward call: dx (x_dtype), dweight[cols] and dbias[cols]
  * (fp32, overwritten; zero when rows == 0).  Any of the three may be NULL, but
- * not all.  dx must be neither dy nor x.  workspace (256-byte aligned) may be
+ * not all.  dx shares no element with dy or x.  workspace (256-byte aligned) may be
  * NULL when dweight and dbias are. */
 int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, const void* x, const void* weight,
                             const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
@@ -365,8 +366,9 @@ typedef struct muon_attention_desc {
 
 /* One (tokens, heads, head_dim) operand: strides in elements, head_dim
  * contiguous.  data and both strides must be multiples of 16 bytes, and
- * token_stride at most 2^24 elements, head_stride 2^31.  Inputs may overlap or repeat (slices of one projection, stride 0); the rows of an
- * output must not overlap. */
+ * token_stride at most 2^24 elements, head_stride 2^31.  Inputs may overlap or
+ * repeat (slices of one projection, stride 0); the rows of an output must not
+ * overlap, and no output shares an element with another operand. */
 typedef struct muon_heads {
   void* data;
   int64_t token_stride;

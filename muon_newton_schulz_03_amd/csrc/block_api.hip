@@ -107,6 +107,15 @@ int check_heads(const muon_attention_desc* d, const muon_heads* v, const char* n
 size_t attention_part_bytes(const muon_attention_desc* d, int splits) {
   return splits > 1 ? (size_t)splits * d->tokens * d->kv_heads * 2 * d->head_dim * sizeof(float) : 0;
 }
+// Whether two blocks of rows * cols elements share one.  Decided where their
+// leading dimensions agree (views of one buffer).
+bool rows_meet(const muon_layernorm_desc* d, const void* p, int64_t ld_p, const void* q, int64_t ld_q) {
+  const uint64_t es = elem_size(d->x_dtype), w = d->cols * es, ld = ld_of(ld_p, d->cols) * es;
+  if (!p || !q || ld_of(ld_p, d->cols) != ld_of(ld_q, d->cols)) return p && p == q;
+  const uint64_t a = (uint64_t)(uintptr_t)p, b = (uint64_t)(uintptr_t)q, apart = a < b ? b - a : a - b;
+  const uint64_t k = apart / ld, r = apart % ld, n = d->rows;  // the later block starts k rows and r bytes on
+  return (k < n && r < w) || (k + 1 < n && ld - r < w);
+}
 int splits_of(const muon_attention_desc* d) {
   return attention_splits(d->tokens, d->seqs, d->q_heads, d->kv_heads);
 }
@@ -143,7 +152,7 @@ int muon_layernorm_forward(const muon_layernorm_desc* d, const void* x, const vo
   if (int rc = check_norm(d)) return rc;
   if (d->rows == 0) return MUON_OK;
   if (!x || !y || !mean || !rstd) return fail(MUON_E_INVAL, "layer norm: x, y, mean or rstd is NULL");
-  if (y == x) return fail(MUON_E_INVAL, "layer norm: y must not be x");
+  if (rows_meet(d, x, d->ld_x, y, d->ld_y)) return fail(MUON_E_INVAL, "layer norm: y overlaps x");
   const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
   if (misaligned(x, es) || misaligned(y, es) || misaligned(weight, ps) || misaligned(bias, ps) ||
       misaligned(mean, 4) || misaligned(rstd, 4))
@@ -172,7 +181,8 @@ int muon_layernorm_backward(const muon_layernorm_desc* d, const void* dy, const 
   const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
   if (d->rows > 0) {
     if (!dy || !x || !mean || !rstd) return fail(MUON_E_INVAL, "layer norm: dy, x, mean or rstd is NULL");
-    if (dx == dy || dx == x) return fail(MUON_E_INVAL, "layer norm: dx must be neither dy nor x");
+    if (rows_meet(d, dy, d->ld_dy, dx, d->ld_dx) || rows_meet(d, x, d->ld_x, dx, d->ld_dx))
+      return fail(MUON_E_INVAL, "layer norm: dx overlaps dy or x");
   }
   if (misaligned(x, es) || misaligned(dy, es) || misaligned(dx, es) || misaligned(weight, ps) || misaligned(mean, 4) ||
       misaligned(rstd, 4) || misaligned(dweight, 4) || misaligned(dbias, 4))

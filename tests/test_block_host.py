@@ -71,6 +71,19 @@ def test_layer_norm_refuses_pointers(lib):
     assert fwd(ctypes.byref(norm_desc(rows=0)), None, None, None, None, None, None, None) == 0
 
 
+@pytest.mark.parametrize("ld,apart", [(0, 2), (0, 128), (0, 7 * 128 + 126), (200, 2), (200, 126), (200, 400),
+                                      (200, 400 - 126), (200, 6 * 400 + 274), (200, 7 * 400 + 126)])
+def test_layer_norm_refuses_overlapping_rows(lib, ld, apart):
+    """8 rows of 64 bf16 elements, an output `apart` bytes before or behind an input of the same leading dimension."""
+    d = ctypes.byref(norm_desc(ld_x=ld, ld_y=ld, ld_dy=ld, ld_dx=ld))
+    for off in (apart, -apart):
+        assert lib.muon_layernorm_forward(d, P, P, P, P + off, P, P, None) == INVAL
+        assert "overlap" in _lib.last_error()
+        for dy, x in ((P, 8 * P), (8 * P, P)):
+            assert lib.muon_layernorm_backward(d, dy, x, P, P, P, P + off, P, P, P, 1 << 40, None) == INVAL
+            assert "overlap" in _lib.last_error()
+
+
 def test_layer_norm_workspace_covers_every_kernel(lib):
     """One row of 2 cols sums for each block: a wave holds a row of up to 2048 elements, and at most 1024 blocks of
     four waves run."""

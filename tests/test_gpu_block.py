@@ -60,6 +60,30 @@ def test_layer_norm_rows(rows, cols):
     norm_case(x, None, None, randn((rows, cols), 12, BF))
 
 
+@pytest.mark.parametrize("dtype,rows,cols", [(BF, 9001, 520), (BF, 8203, 1536), (BF, 8195, 770), (F32, 8201, 1024),
+                                             (BF, 2561, 4096), (BF, 2051, 6000), (F32, 2053, 2309)])
+def test_layer_norm_rows_in_turn(dtype, rows, cols):
+    """More rows than the launch holds at once, with parameters: each thread takes several."""
+    say(f"[gpu] layer norm {rows}x{cols} {dtype}")
+    norm_case(randn((rows, cols), 13, dtype), 1 + randn((cols,), 14, std=0.2), randn((cols,), 15),
+              randn((rows, cols), 16, dtype))
+
+
+def test_layer_norm_between_columns_of_one_buffer():
+    """Input and output interleaved row by row: the same bits as in separate buffers, nothing else written."""
+    rows, cols = 9000, 128
+    buf = randn((rows, 3 * cols), 17, BF).to(DEV)
+    x, dy = buf[:, :cols], buf[:, 2 * cols:]
+    y, mean, rstd = lib.layer_norm_forward(x.contiguous())
+    dx, _, _ = lib.layer_norm_backward(dy.contiguous(), x.contiguous(), mean, rstd)
+    keep = buf.clone()
+    lib.layer_norm_forward(x, out=buf[:, cols:2 * cols])
+    assert torch.equal(buf[:, cols:2 * cols], y)
+    lib.layer_norm_backward(dy, x, mean, rstd, dx=buf[:, cols:2 * cols])
+    assert torch.equal(buf[:, cols:2 * cols], dx)
+    assert torch.equal(buf[:, :cols], keep[:, :cols]) and torch.equal(buf[:, 2 * cols:], keep[:, 2 * cols:])
+
+
 def test_layer_norm_offset_and_constant_rows():
     """A large common offset must not cancel the variance; a constant row has rstd 1 / sqrt(eps)."""
     x = randn((16, 768), 21) + 1000.0
