@@ -175,11 +175,10 @@ __device__ __forceinline__ void wait_tiles() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// The same with the wave's last N copies still in flight.  (It waits for no LDS
-// read: those of the slot that is written next have long fed their products.)
+// The same with the wave's last N copies still in flight.
 template <int N>
 __device__ __forceinline__ void wait_but() {
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // Copies ROWS rows at a time of two operands (K and V, or Q and dO) into a

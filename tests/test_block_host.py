@@ -240,3 +240,15 @@ def test_reference_check_sees_a_wrong_value():
         for name in ("out", "lse", "dq", "dk", "dv"):
             with pytest.raises(AssertionError):
                 R.check(name, other[name][0], *good[name])
+
+
+# ------------------------------------------------------------ the sources --
+def test_every_barrier_before_a_tile_is_overwritten_waits_for_lds_reads():
+    """A copy into a tile may only start when every wave's reads of it have returned.  The compiler orders its LDS
+    reads before an assembly barrier, not their return, so each such barrier has to wait for them itself."""
+    path = os.path.join(os.path.dirname(_lib.LIB_PATH), "csrc", "attention.hip")
+    with open(path) as f:
+        barriers = [line for line in f if "asm" in line and "s_barrier" in line]
+    assert len(barriers) >= 2
+    for line in barriers:
+        assert "lgkmcnt(0)" in line.split("s_barrier")[0], line
