@@ -348,11 +348,12 @@ int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, con
  * bf16: products take bf16 operands (probabilities and score gradients are
  * rounded to bf16 for theirs) and accumulate in fp32, where softmax
  * statistics are held.  fp32: fp32 throughout.  A score of -inf has weight 0; a
- * row of nothing else is NaN.  Rows are taken 128 at a time, and masked
- * positions get weight zero: a NaN or infinity in a token's k or v can reach
- * the outputs of up to 127 earlier tokens of the same sequence (0 * Inf), and
- * one in its q or dout the dk and dv of as many later ones, but never another
- * sequence. */
+ * row of nothing else is NaN.  What the mask hides does not count, whatever it
+ * holds: a NaN or infinity in a token's k or v reaches the outputs of that
+ * token and of later ones in its sequence, one in its q or dout the dk and dv
+ * of that token and of earlier ones, as in the formulas.  (Blocks of
+ * rows that meet one are computed twice: a call full of NaN takes three times
+ * as long.) */
 typedef struct muon_attention_desc {
   int64_t tokens;
   int32_t seqs;

@@ -268,6 +268,91 @@ __device__ __forceinline__ void store_row(T* row, const f32x16 (&acc)[DP / 32], 
     }
 }
 
+// ---------------------------------------------- what a mask hides, no one sees --
+// A masked pair has weight 0, but 0 times a NaN or an infinity is NaN, and a
+// matrix instruction multiplies every pair of its block.  A block that is
+// masked as a whole is skipped; for the wave's block on the diagonal, every
+// pass ends with a test of the accumulators (0 x each, summed: a few dozen
+// operations a wave), and where one is not finite the thread block makes its
+// pass again, carefully: in the block on the diagonal, values of the right
+// operand that are not finite are taken as 0, and added afterwards to the rows
+// that see them.  The careful pass is code of its own, behind the first: one
+// loop with both ways in it cost 50 to 130 registers.  Times with the test and
+// without, forward and backward: 8192 tokens of 12 heads of 64 131 / 417 and
+// 133 / 421 us, 16/4 heads of 128 280 / 914 and 276 / 911; nothing but NaN takes
+// three times as long.
+template <class T>
+__device__ __forceinline__ typename Elem<T>::Frag finite_part(typename Elem<T>::Frag f, bool diag) {
+  float v[8];
+  Elem<T>::unpack(f, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (__builtin_isfinite(v[e]) | !diag) ? v[e] : 0.f;
+  return Elem<T>::pack(v);
+}
+template <int DT>
+__device__ __forceinline__ float not_finite(const f32x16 (&acc)[DT]) {  // 0 or NaN
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i % 4] = __builtin_fmaf(acc[t][i], 0.f, x[i % 4]);
+  return (x[0] + x[1]) + (x[2] + x[3]);
+}
+// Whether any wave of the block holds a NaN; `flags`: a word a wave, used once.
+template <int WAVES>
+__device__ __forceinline__ bool any_nan(float x, int* flags, int wave) {
+  flags[wave] = __any(x != x);
+  __syncthreads();
+  int any = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) any |= flags[i];
+  return __builtin_amdgcn_readfirstlane(any) != 0;
+}
+// Adds to the lane's columns of an accumulator tile set (laid out as in
+// store_row) `f` times what finite_part() took from `rows` rows, the lane's
+// being those from `lo` to `hi`.
+template <class T, int DP>
+__device__ __forceinline__ void add_not_finite(f32x16 (&acc)[DP / 32], const T* row, int64_t step, int rows, int lo,
+                                               int hi, float f, int dim, int h) {
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = 32 * t + 8 * g + 4 * h;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r) {
+        if (r < lo || r > hi || d >= dim) continue;
+        float v[4];
+        if constexpr (sizeof(T) == 2) {
+          unpack4_bf16(*gv<u32x2>(row + r * step + d), v);
+        } else {
+          const f32x4 y = *gv<f32x4>(row + r * step + d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = y[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += __builtin_isfinite(v[e]) ? 0.f : f * v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][4 * g + e] += x[e];
+    }
+}
+// Waves a SIMD that the first pass's registers leave room for.  As launch
+// bounds they make the careful pass spill where it would take more.
+template <class T, int DP, int NG>
+constexpr int kForwardWaves = sizeof(T) == 4 ? (DP == 32 ? 4 : 2) : DP == 32 ? 5 : DP == 64 ? 4 : DP == 96 && NG == 1 ? 3 : 2;
+template <class T, int DP, int NG>
+constexpr int kDqWaves = sizeof(T) == 4 ? (DP == 32 ? 3 : 2) : DP == 32 ? 4 : DP == 64 && NG == 1 ? 3 : 2;
+template <int DP>
+constexpr int kDkvWaves = DP == 32 ? 4 : DP == 64 ? 3 : 2;
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
 // Adds the other groups of waves' accumulators to the first's, in order,
 // through LDS (kJoin bytes); true in the others, whose work is done.
 template <int DT, int WR, int NG>
@@ -462,12 +547,13 @@ struct Cfg {
 };
 
 template <class T, int DP, int WR, int NG>
-__global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NG * WR * 64, (kForwardWaves<T, DP, NG>)) void attention_forward_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
   constexpr int BM = 32 * WR, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
   constexpr int kTile = KT * Tl::kRow;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
+  __shared__ int flags[NG * WR];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
@@ -489,70 +575,85 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(Attn
   load_frags<T, DP>(qf, (const T*)a.q.data + (st.start + (int64_t)qi) * a.q.token + head * a.q.head, qi < st.len,
                     a.dim, h);
   f32x16 o[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) o[t] = f32x16{};
-  float m = -__FLT_MAX__, l = 0.f;  // not -inf: scores of -inf before the first finite one have weight 0, not NaN
-
+  float m, l;
   PairCopier<T, DP, KT, WR> cp;
   cp.init(a.k, a.v, a.dim, w, lane);
-  cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
-  cp.template copy<NG>(lds[grp][0][0], w, lane);
-  wait_tiles();
-  for (int kt = 0; kt < ntile; ++kt) {
-    const char *kl = lds[grp][kt & 1][0], *vl = lds[grp][kt & 1][1];
-    const int k0 = (kt * NG + grp) * KT;  // first key of this group's tile
-    if (kt + 1 < ntile) cp.template copy<NG>(lds[grp][(kt + 1) & 1][0], w, lane);
-    if (k0 < wend) {
-      f32x16 s[MT];
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        s[j] = f32x16{};
+    for (int t = 0; t < DT; ++t) o[t] = f32x16{};
+    m = -__FLT_MAX__, l = 0.f;  // not -inf: scores of -inf before the first finite one have weight 0, not NaN
+
+    cp.seek(a.k, kvh, a.v, kvh, st.start + (int64_t)grp * KT, st.len - grp * KT, w);
+    cp.template copy<NG>(lds[grp][0][0], w, lane);
+    wait_tiles();
+    for (int kt = 0; kt < ntile; ++kt) {
+      const char *kl = lds[grp][kt & 1][0], *vl = lds[grp][kt & 1][1];
+      const int k0 = (kt * NG + grp) * KT;  // first key of this group's tile
+      if (kt + 1 < ntile) cp.template copy<NG>(lds[grp][(kt + 1) & 1][0], w, lane);
+      if (k0 < wend) {
+        f32x16 s[MT];
 #pragma unroll
-        for (int q = 0; q < ST; ++q) s[j] = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s[j]);
-      }
-      if (k0 + KT - 1 > qw) {
+        for (int j = 0; j < MT; ++j) {
+          s[j] = f32x16{};
+#pragma unroll
+          for (int q = 0; q < ST; ++q) s[j] = Elem<T>::mma(Tl::row_frag(kl, 32 * j + col, q, h), qf[q], s[j]);
+        }
+        if (k0 + KT - 1 > qw) {
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) s[j][i] = -__builtin_inff();
+        }
+        float top = s[0][0];
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (k0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) > qi) s[j][i] = -__builtin_inff();
-      }
-      float top = s[0][0];
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, s[j][i]);
+        top = halves_max(top) * c;
+        // The running maximum only has to keep exp2's arguments small: it is
+        // raised (and the sums rescaled) when a score passes it by more than
+        // kLazy, so p <= 2^kLazy, and most tiles rescale nothing.
+        if (__any(top > m + kLazy)) {
+          const float mn = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - mn);
+          m = mn;
+          l *= f;
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
+          for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[j][i]);
-      top = halves_max(top) * c;
-      // The running maximum only has to keep exp2's arguments small: it is
-      // raised (and the sums rescaled) when a score passes it by more than
-      // kLazy, so p <= 2^kLazy, and most tiles rescale nothing.
-      if (__any(top > m + kLazy)) {
-        const float mn = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - mn);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[t][i] *= f;
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        float p[16], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -m));
-          sum += p[i];
+            for (int i = 0; i < 16; ++i) o[t][i] *= f;
         }
-        l += sum;  // 16 at a time: the error of a long sum grows with its number of additions
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const Frag pf = Elem<T>::pack(p + 8 * u);
+        for (int j = 0; j < MT; ++j) {
+          float p[16], sum = 0.f;
 #pragma unroll
-          for (int t = 0; t < DT; ++t) o[t] = Elem<T>::mma(Tl::col_frag(vl, 32 * j + 16 * u, t, lane), pf, o[t]);
+          for (int i = 0; i < 16; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], c, -m));
+            sum += p[i];
+          }
+          l += sum;  // 16 at a time: the error of a long sum grows with its number of additions
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const Frag pf = Elem<T>::pack(p + 8 * u);
+#pragma unroll
+            for (int t = 0; t < DT; ++t) {
+              Frag vf = Tl::col_frag(vl, 32 * j + 16 * u, t, lane);
+              if (careful.value) vf = finite_part<T>(vf, k0 + KT - 1 > qw);
+              o[t] = Elem<T>::mma(vf, pf, o[t]);
+            }
+          }
         }
       }
+      wait_tiles();
     }
-    wait_tiles();
+  };
+  pass(No{});
+  if (any_nan<NG * WR>(not_finite(o), flags, grp * WR + w)) {
+    pass(Yes{});
+    const int k0 = qw / KT * KT;
+    if (grp == 0 && qi < st.len)
+      add_not_finite<T, DP>(o, (const T*)a.v.data + (st.start + (int64_t)k0) * a.v.token + kvh * a.v.head, a.v.token,
+                            min(KT, st.len - k0), 0, qi - k0, 1.f, a.dim, h);
   }
   l = halves_sum(l);
   if constexpr (NG > 1) {  // the other groups hand their sums to the first
@@ -597,7 +698,7 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_forward_kernel(Attn
 // tokens in 24 sequences, 12 heads of 64: 87 us (676 TFLOP/s); 8192 tokens,
 // 16/4 heads of 128: 400 us (1030).
 template <class T, int DP, int WR, int NG>
-__global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NG * WR * 64, (kDqWaves<T, DP, NG>)) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
   constexpr int BM = 32 * WR, KT = Cfg<T>::kKeys, MT = KT / 32, ST = DP / 16, DT = DP / 32;
@@ -605,6 +706,7 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs 
   constexpr bool kFix = sizeof(T) == 2;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
   __shared__ float offs[NG][WR][kFix ? 64 : 1];
+  __shared__ int flags[NG * WR];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   const int head = blockIdx.x % a.q_heads, kvh = head / a.group;
@@ -651,7 +753,7 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs 
   // to zero, so their sum is the difference, and the exact delta goes to the
   // next kernel.  In a sequence's first rows, where few terms average such
   // errors, dq is made again with it.
-  for (int pass = kFix && st.row0 == 0 ? 0 : 1; pass < 2; ++pass) {
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
     float off = 0.f;
 #pragma unroll
     for (int t = 0; t < DT; ++t) dq[t] = f32x16{};
@@ -689,7 +791,11 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs 
           for (int u = 0; u < 2; ++u) {
             const Frag pf = Elem<T>::pack(ds + 8 * u);
 #pragma unroll
-            for (int t = 0; t < DT; ++t) dq[t] = Elem<T>::mma(Tl::col_frag(kl, 32 * j + 16 * u, t, lane), pf, dq[t]);
+            for (int t = 0; t < DT; ++t) {
+              Frag kf = Tl::col_frag(kl, 32 * j + 16 * u, t, lane);
+              if (careful.value) kf = finite_part<T>(kf, k0 + KT - 1 > qw);
+              dq[t] = Elem<T>::mma(kf, pf, dq[t]);
+            }
           }
         }
       }
@@ -705,9 +811,19 @@ __global__ __launch_bounds__(NG * WR * 64, 2) void attention_dq_kernel(AttnArgs 
         for (int g = 0; g < NG; ++g) off += offs[g][w][lane];
         __syncthreads();
       }
-      delta += off;
     }
+    return off;
+  };
+  if (kFix && st.row0 == 0) delta += pass(No{});
+  float off = pass(No{});
+  if (any_nan<NG * WR>(not_finite(dq), flags, grp * WR + w)) {
+    off = pass(Yes{});
+    const int k0 = qw / KT * KT;
+    if (grp == 0 && valid)
+      add_not_finite<T, DP>(dq, (const T*)a.k.data + (st.start + (int64_t)k0) * a.k.token + kvh * a.k.head, a.k.token,
+                            min(KT, st.len - k0), 0, qi - k0, 0.f, a.dim, h);
   }
+  delta += off;
   if (valid && h == 0 && grp == 0) a.delta[(int64_t)head * a.tokens + tok] = kFix ? -delta : delta;
   if constexpr (NG > 1) {
     static_assert(kJoin<DT, WR, NG> <= sizeof(lds), "the sums fit the tiles");
@@ -729,6 +845,7 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
   constexpr int kTile = QR * Tl::kRow;
   __shared__ __align__(256) char lds[NG][2][2][kTile];
   __shared__ __align__(256) float stat[NG][2][2][64];  // lse2 and delta of the tile's rows
+  __shared__ int flags[NG * WR];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   const int per = a.kv_heads * a.splits;
@@ -751,9 +868,6 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
   load_frags<T, DP>(kf, (const T*)a.k.data + tok * a.k.token + kvh * a.k.head, valid, a.dim, h);
   load_frags<T, DP>(vf, (const T*)a.v.data + tok * a.v.token + kvh * a.v.head, valid, a.dim, h);
   f32x16 dk[DT], dv[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
-
   const int qt0 = st.row0 / QR, nq = (st.len + QR - 1) / QR - qt0, total = nq * hpp;
   PairCopier<T, DP, QR, WR> cp;
   cp.init(a.q, a.dout, a.dim, w, lane);
@@ -767,49 +881,68 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
       dma_b32(buffer_of((w ? a.delta : a.lse2) + (int64_t)head * a.tokens + st.start + row0,
                         4 * min(st.len - row0, QR)), lds_offset(stat[grp][b][w]), 4 * lane);
   };
-  copy(0);
-  wait_tiles();
-  for (int it = 0; it * NG < total; ++it) {  // past the last tile: zeros, which add nothing
-    const char *ql = lds[grp][it & 1][0], *dl = lds[grp][it & 1][1];
-    const float *ll = stat[grp][it & 1][0], *el = stat[grp][it & 1][1];
-    const int q0 = (qt0 + (it * NG + grp) % nq) * QR;
-    if ((it + 1) * NG < total) copy(it + 1);
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      if (q0 + 32 * j + 31 < kw) continue;  // rows before every key of this wave
-      f32x16 s = f32x16{}, dp = f32x16{};
-#pragma unroll
-      for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(ql, 32 * j + col, q, h), kf[q], s);
-#pragma unroll
-      for (int q = 0; q < ST; ++q) dp = Elem<T>::mma(Tl::row_frag(dl, 32 * j + col, q, h), vf[q], dp);
-      float p[16], ds[16];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 lse2 = *(const f32x4*)(ll + 32 * j + 8 * g + 4 * h);
-        const f32x4 del = *(const f32x4*)(el + 32 * j + 8 * g + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * g + e;
-          p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2[e]));
-          ds[i] = p[i] * (dp[i] - del[e]);
-        }
-      }
-      if (q0 + 32 * j < kw + 31) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (q0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) < ki) p[i] = ds[i] = 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
-#pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          dv[t] = Elem<T>::mma(Tl::col_frag(dl, 32 * j + 16 * u, t, lane), pf, dv[t]);
-          dk[t] = Elem<T>::mma(Tl::col_frag(ql, 32 * j + 16 * u, t, lane), sf, dk[t]);
-        }
-      }
-    }
+    for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
+    copy(0);
     wait_tiles();
+    for (int it = 0; it * NG < total; ++it) {  // past the last tile: zeros, which add nothing
+      const char *ql = lds[grp][it & 1][0], *dl = lds[grp][it & 1][1];
+      const float *ll = stat[grp][it & 1][0], *el = stat[grp][it & 1][1];
+      const int q0 = (qt0 + (it * NG + grp) % nq) * QR;
+      if ((it + 1) * NG < total) copy(it + 1);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if (q0 + 32 * j + 31 < kw) continue;  // rows before every key of this wave
+        f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+        for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(ql, 32 * j + col, q, h), kf[q], s);
+#pragma unroll
+        for (int q = 0; q < ST; ++q) dp = Elem<T>::mma(Tl::row_frag(dl, 32 * j + col, q, h), vf[q], dp);
+        float p[16], ds[16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 lse2 = *(const f32x4*)(ll + 32 * j + 8 * g + 4 * h);
+          const f32x4 del = *(const f32x4*)(el + 32 * j + 8 * g + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * g + e;
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse2[e]));
+            ds[i] = p[i] * (dp[i] - del[e]);
+          }
+        }
+        if (q0 + 32 * j < kw + 31) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (q0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) < ki) p[i] = ds[i] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
+#pragma unroll
+          for (int t = 0; t < DT; ++t) {
+            Frag of = Tl::col_frag(dl, 32 * j + 16 * u, t, lane), qf = Tl::col_frag(ql, 32 * j + 16 * u, t, lane);
+            if (careful.value) of = finite_part<T>(of, q0 + 32 * j < kw + 31), qf = finite_part<T>(qf, q0 + 32 * j < kw + 31);
+            dv[t] = Elem<T>::mma(of, pf, dv[t]);
+            dk[t] = Elem<T>::mma(qf, sf, dk[t]);
+          }
+        }
+      }
+      wait_tiles();
+    }
+  };
+  pass(No{});
+  if (any_nan<NG * WR>(not_finite(dk) + not_finite(dv), flags, grp * WR + w)) {
+    pass(Yes{});
+    if (grp == 0 && valid)
+      for (int head = head0; head < head0 + hpp; ++head) {
+        const int64_t t0 = st.start + (int64_t)kw;
+        const int rows = min(32, st.len - kw);
+        add_not_finite<T, DP>(dk, (const T*)a.q.data + t0 * a.q.token + head * a.q.head, a.q.token, rows, col, 31, 0.f,
+                              a.dim, h);
+        add_not_finite<T, DP>(dv, (const T*)a.dout.data + t0 * a.dout.token + head * a.dout.head, a.dout.token, rows,
+                              col, 31, 1.f, a.dim, h);
+      }
   }
   if constexpr (NG > 1) {
     static_assert(kJoin<DT, WR, NG> <= sizeof(lds), "the sums fit the tiles");
@@ -835,7 +968,7 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
 // tokens, 16/4 heads of 128, against 507, 1085 TFLOP/s).  At heads of 64, 64
 // rows a step take 106 us on 16384 packed tokens, 32 rows 116.
 template <int DP, int NG>
-__global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NG * kThreads, kDkvWaves<DP>) void attention_dkv_bf16_kernel(AttnArgs a) {
   typedef __bf16 T;
   typedef Elem<T>::Frag Frag;
   typedef Tiles<T, DP> Tl;
@@ -844,6 +977,7 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
   typedef PairCopier<T, DP, QR, WR> Pair;
   constexpr int kSlot = 2 * Pair::kTile + 512;  // Q rows, dO rows, and two words a row
   __shared__ __align__(256) char lds[NG * kSlots * kSlot + (kHoldV ? 0 : BN * Tl::kRow)];
+  __shared__ int flags[NG * WR];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, col = lane & 31;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6) % WR, grp = __builtin_amdgcn_readfirstlane(tid >> 6) / WR;
   char* const ring = lds + grp * kSlots * kSlot;
@@ -876,13 +1010,11 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
     if (grp == 0) cv.template copy<1>(vt, w, lane);
   }
   f32x16 dk[DT], dv[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
 
   // The rows to copy next: their slot, head and words (even waves copy the first, odd ones the second).
   Pair cp;
   cp.init(a.q, a.dout, a.dim, w, lane);
-  int cslot = 0, chead = head0, crow = st.row0;
+  int cslot, chead, crow;
   const float* words;
   auto next = [&](int& head, int& row) {
     row += QR;
@@ -905,58 +1037,80 @@ __global__ __launch_bounds__(NG * kThreads, 2) void attention_dkv_bf16_kernel(At
     for (int i = 0; i < NG; ++i) next(chead, crow);
     if (chead != head) seek();
   };
-  int row = st.row0, rhead = head0;  // the rows in hand
-  if (grp) next(chead, crow), next(rhead, row);
-  seek();
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < kSlots - 1; ++i) copy();
-  const int total = ((st.len - st.row0 + QR - 1) / QR * hpp + NG - 1) / NG;
-  for (int i = 0; i < total; ++i) {  // a group's rows past the last: zeros, which add nothing
-    wait_but<(kSlots - 2) * (Pair::kN + 1)>();
-    copy();
-    const char* sl = ring + (i & (kSlots - 1)) * kSlot;
+    for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
+    cslot = 0, chead = head0, crow = st.row0;
+    int row = st.row0, rhead = head0;  // the rows in hand
+    if (grp) next(chead, crow), next(rhead, row);
+    seek();
+#pragma unroll
+    for (int i = 0; i < kSlots - 1; ++i) copy();
+    const int total = ((st.len - st.row0 + QR - 1) / QR * hpp + NG - 1) / NG;
+    for (int i = 0; i < total; ++i) {  // a group's rows past the last: zeros, which add nothing
+      wait_but<(kSlots - 2) * (Pair::kN + 1)>();
+      copy();
+      const char* sl = ring + (i & (kSlots - 1)) * kSlot;
 #pragma unroll 1
-    for (int j = 0; j < QR; j += 32) {
-      const char *ql = sl + j * Tl::kRow, *ol = ql + Pair::kTile;
-      f32x16 s, dp;
+      for (int j = 0; j < QR; j += 32) {
+        if (careful.value && row + j + 31 < kw) continue;  // rows before every key of this wave
+        const char *ql = sl + j * Tl::kRow, *ol = ql + Pair::kTile;
+        f32x16 s, dp;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4 x = *(const f32x4*)(sl + 2 * Pair::kTile + 4 * j + 32 * g + 16 * h);
-        const f32x4 y = *(const f32x4*)(sl + 2 * Pair::kTile + 256 + 4 * j + 32 * g + 16 * h);
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 x = *(const f32x4*)(sl + 2 * Pair::kTile + 4 * j + 32 * g + 16 * h);
+          const f32x4 y = *(const f32x4*)(sl + 2 * Pair::kTile + 256 + 4 * j + 32 * g + 16 * h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * g + e] = x[e], dp[4 * g + e] = y[e];
-      }
+          for (int e = 0; e < 4; ++e) s[4 * g + e] = x[e], dp[4 * g + e] = y[e];
+        }
 #pragma unroll
-      for (int q = 0; q < ST; ++q) {
-        s = Elem<T>::mma(Tl::row_frag(ql, col, q, h), kf[q], s);
-        if constexpr (kHoldV)
-          dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), vf[q], dp);
-        else
-          dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
-      }
-      if (row + j < kw + 31) {  // a row before some key
+        for (int q = 0; q < ST; ++q) {
+          s = Elem<T>::mma(Tl::row_frag(ql, col, q, h), kf[q], s);
+          if constexpr (kHoldV)
+            dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), vf[q], dp);
+          else
+            dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
+        }
+        if (row + j < kw + 31) {  // a row before some key
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (row + j + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
-      }
-      float p[16], ds[16];
+          for (int e = 0; e < 16; ++e)
+            if (row + j + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
+        }
+        float p[16], ds[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(s[e] * c);
-        ds[e] = p[e] * dp[e];
-      }
+        for (int e = 0; e < 16; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(s[e] * c);
+          ds[e] = p[e] * dp[e];
+        }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
+        for (int u = 0; u < 2; ++u) {
+          const Frag pf = Elem<T>::pack(p + 8 * u), sf = Elem<T>::pack(ds + 8 * u);
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          dv[t] = Elem<T>::mma(Tl::col_frag(ol, 16 * u, t, lane), pf, dv[t]);
-          dk[t] = Elem<T>::mma(Tl::col_frag(ql, 16 * u, t, lane), sf, dk[t]);
+          for (int t = 0; t < DT; ++t) {
+            Frag of = Tl::col_frag(ol, 16 * u, t, lane), qf = Tl::col_frag(ql, 16 * u, t, lane);
+            if (careful.value) of = finite_part<T>(of, row + j < kw + 31), qf = finite_part<T>(qf, row + j < kw + 31);
+            dv[t] = Elem<T>::mma(of, pf, dv[t]);
+            dk[t] = Elem<T>::mma(qf, sf, dk[t]);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) next(rhead, row);
+      for (int g = 0; g < NG; ++g) next(rhead, row);
+    }
+  };
+  pass(No{});
+  if (any_nan<NG * WR>(not_finite(dk) + not_finite(dv), flags, grp * WR + w)) {
+    wait_tiles();  // the copies of rows past the last
+    pass(Yes{});
+    if (grp == 0 && valid)
+      for (int head = head0; head < head0 + hpp; ++head) {
+        const int64_t t0 = st.start + (int64_t)kw;
+        const int rows = min(32, st.len - kw);
+        add_not_finite<T, DP>(dk, (const T*)a.q.data + t0 * a.q.token + head * a.q.head, a.q.token, rows, col, 31, 0.f,
+                              a.dim, h);
+        add_not_finite<T, DP>(dv, (const T*)a.dout.data + t0 * a.dout.token + head * a.dout.head, a.dout.token, rows,
+                              col, 31, 1.f, a.dim, h);
+      }
   }
   if constexpr (NG > 1) {
     static_assert(kJoin<DT, WR, NG> <= sizeof(lds), "the sums fit the tiles");

@@ -1,0 +1,93 @@
+"""Calls of the block's operators at the edges of what their contract allows, on the GPU.
+
+Values are held against the fp64 definitions within block_reference's bounds.
+"""
+import pytest
+import torch
+
+import block_reference as R
+import muon_newton_schulz_03_amd as lib
+from muon_harness import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def randn(shape, seed, dtype=F32, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def cu_of(lengths):
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    return torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+
+def run_attention(q, k, v, do, cu):
+    dev = [t.to(DEV) for t in (q, k, v, do)]
+    out, lse = lib.packed_attention_forward(*dev[:3], cu)
+    grads = lib.packed_attention_backward(dev[3], *dev[:3], out, lse, cu)
+    torch.cuda.synchronize()
+    return dict(zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)))
+
+
+# ---------------------------------------------- what a mask hides, no one sees --
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("extra", [0, 40])  # 40 empty sequences behind: one group of waves a block instead of two
+def test_attention_later_tokens_never_reach_earlier_ones(dim, dtype, extra):
+    """NaN and infinities in a token's operands reach what its own scores reach, by the formulas, and nothing else:
+    no earlier token's out and dq (k, v), no later token's dk and dv (q, dout), no other row (q, dout)."""
+    n, H, G = 330, 4, 2
+    q, k, v, do = (randn((n, h, dim), 900 + i, dtype) for i, h in enumerate((H, G, G, H)))
+    ref = R.attention(q, k, v, [n], dim ** -0.5, do)
+    cu = cu_of([n] + [0] * extra)
+
+    def clean(name, got, rows, heads):
+        rows = torch.tensor(list(rows), dtype=torch.long)
+        for h in heads:
+            at = (h, rows) if name == "lse" else (rows, h)
+            R.check(f"{name} head {h}", got[name].cpu()[at], *(t[at] for t in ref[name]))
+
+    everything, mine = range(n), [0, 1]  # query heads 0 and 1 read key/value head 0
+    for t, bad in ((1, float("nan")), (40, float("inf")), (62, float("nan")), (127, float("-inf")),
+                   (130, float("nan")), (255, float("inf")), (n - 1, float("nan"))):
+        say(f"[gpu] poisoned token {t} dim {dim} {dtype} extra {extra}: {bad}")
+        before, after, others = range(t), range(t + 1, n), [i for i in range(n) if i != t]
+        x = v.clone()
+        x[t, 0, dim - 3] = bad
+        got = run_attention(q, k, x, do, cu)
+        clean("lse", got, everything, range(H))
+        clean("dv", got, everything, range(G))
+        for name in ("out", "dq"):
+            clean(name, got, before, mine)
+            clean(name, got, everything, [2, 3])
+        clean("dk", got, everything, [1])
+        assert not torch.isfinite(got["out"][t:, :2, dim - 3].float()).any()
+        x = k.clone()
+        x[t, 0, 5] = bad
+        got = run_attention(q, x, v, do, cu)
+        for name in ("out", "dq", "lse"):
+            clean(name, got, before, mine)
+            clean(name, got, everything, [2, 3])
+        x = q.clone()
+        x[t, 0, 5] = bad
+        got = run_attention(x, k, v, do, cu)
+        for name in ("out", "dq", "lse"):
+            clean(name, got, others, [0])
+            clean(name, got, everything, [1, 2, 3])
+        for name in ("dk", "dv"):
+            clean(name, got, after, [0])
+            clean(name, got, everything, [1])
+        x = do.clone()
+        x[t, 1, 2] = bad
+        got = run_attention(q, k, v, x, cu)
+        clean("dq", got, others, [1])
+        clean("dq", got, everything, [0, 2, 3])
+        for name in ("dk", "dv"):
+            clean(name, got, after, [0])
+            clean(name, got, everything, [1])
+        assert not torch.isfinite(got["dv"][:t + 1, 0, 2].float()).any()
