@@ -292,7 +292,10 @@ int muon_fused_limits(muon_plan* plan, int32_t spin_limit, int32_t dep_bias);
  * device pointer of the current device, which hip_stream belongs to; calls
  * may be captured in a graph; errors are codes with a message in
  * muon_last_error().  A call keeps nothing: calls on different streams or
- * threads are independent as long as their buffers and workspaces are.
+ * threads are independent as long as their buffers and workspaces are.  A call
+ * whose output or workspace shares memory with another of its operands is
+ * refused (MUON_E_INVAL).  Operands may lie between each other's rows in one
+ * buffer if they step through it alike.
  * Results are bitwise reproducible (no atomics).  NaN and infinities are not
  * inspected; they propagate as in the formulas. */
 
@@ -312,8 +315,7 @@ typedef struct muon_layernorm_desc {
 
 /* y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps), with the
  * row's mean and biased variance; mean[rows] and rstd[rows] (fp32) are written
- * for the backward call.  y and x may be columns of one buffer, but share no
- * element.  rows == 0 does nothing. */
+ * for the backward call.  rows == 0 does nothing. */
 int muon_layernorm_forward(const muon_layernorm_desc* desc, const void* x, const void* weight, const void* bias,
                            void* y, float* mean, float* rstd, void* hip_stream);
 
@@ -323,8 +325,7 @@ size_t muon_layernorm_workspace_size(const muon_layernorm_desc* desc);
 
 /* Gradients of the forward call: dx (x_dtype), dweight[cols] and dbias[cols]
  * (fp32, overwritten; zero when rows == 0).  Any of the three may be NULL, but
- * not all.  dx shares no element with dy or x.  workspace (256-byte aligned) may be
- * NULL when dweight and dbias are. */
+ * not all.  workspace (256-byte aligned) may be NULL when dweight and dbias are. */
 int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, const void* x, const void* weight,
                             const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                             void* workspace, size_t ws_bytes, void* hip_stream);
@@ -369,7 +370,7 @@ typedef struct muon_attention_desc {
  * contiguous.  data and both strides must be multiples of 16 bytes, and
  * token_stride at most 2^24 elements, head_stride 2^31.  Inputs may overlap or
  * repeat (slices of one projection, stride 0); the rows of an output must not
- * overlap, and no output shares an element with another operand. */
+ * overlap. */
 typedef struct muon_heads {
   void* data;
   int64_t token_stride;
@@ -393,8 +394,7 @@ int muon_attention_forward(const muon_attention_desc* desc, const int32_t* cu_se
 size_t muon_attention_workspace_size(const muon_attention_desc* desc);
 
 /* Gradients of the forward call, from its inputs, its out and lse, and dout.
- * dq, dk and dv are overwritten (they may be slices of one buffer, but not
- * inputs); dk and dv sum over the query heads of their group. */
+ * dq, dk and dv are overwritten (they may be slices of one buffer); dk and dv sum over the query heads of their group. */
 int muon_attention_backward(const muon_attention_desc* desc, const int32_t* cu_seqlens, const muon_heads* dout,
                             const muon_heads* q, const muon_heads* k, const muon_heads* v, const muon_heads* out,
                             const float* lse, const muon_heads* dq, const muon_heads* dk, const muon_heads* dv,

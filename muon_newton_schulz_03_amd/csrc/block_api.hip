@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kMaxCols = 1 << 20;
 constexpr int64_t kMaxRows = (int64_t)1 << 40;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
+constexpr double kMaxElements = 0x1p56;  // byte offsets fit 64 bits
 constexpr int64_t kMaxTokenStride = 1 << 24;  // a 64-row tile stays within 32-bit byte offsets
 constexpr int64_t kMaxTokens = 0x7FFFFF00;
 constexpr int kMaxSeqs = 1 << 24;
@@ -27,6 +28,66 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool misaligned(const void* p, size_t n) { return (uintptr_t)p % n != 0; }
 int elem_size(int dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
+
+// ---------------------------------------------------------------- overlap --
+// The bytes of an operand: n x m pieces of `width` bytes, `step` and `inner`
+// bytes apart.  A step of 0 repeats a piece.
+struct Area {
+  int64_t at, n, step, m, inner, width;
+};
+Area flat(const void* p, size_t bytes) { return Area{(int64_t)(uintptr_t)p, 1, 0, 1, 0, p ? (int64_t)bytes : 0}; }
+Area area(const void* p, int64_t n, int64_t step, int64_t m, int64_t inner, int64_t width) {
+  if (n == 1 || step == 0) n = 1, step = 0;
+  if (m == 1 || inner == 0) m = 1, inner = 0;
+  return Area{(int64_t)(uintptr_t)p, n, step, m, inner, p && n ? width : 0};
+}
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }  // b > 0
+
+// Whether two operands share a byte.  Exact for operands whose steps agree
+// (slices of one buffer; one piece agrees with everything) or whose pieces of
+// a row are few; others count as sharing where their extents meet.
+bool meet(const Area& a, const Area& b) {
+  if (!a.width || !b.width) return false;
+  const int64_t ea = (a.m - 1) * a.inner + a.width, eb = (b.m - 1) * b.inner + b.width;  // a row's extent
+  const int64_t apart = b.at - a.at;
+  if (apart >= (a.n - 1) * a.step + ea || -apart >= (b.n - 1) * b.step + eb) return false;
+  const int64_t step = a.step ? a.step : b.step, inner = a.inner ? a.inner : b.inner;
+  if (a.step && b.step && a.step != b.step) return true;
+  if (step) {  // columns of one buffer: b's rows start r bytes into a's, or between them
+    const int64_t r = apart - floor_div(apart, step) * step;
+    if (r >= ea && step - r >= eb) return false;
+  }
+  // a piece of b lies x + di step behind one of a, di from -(a.n - 1) to b.n - 1
+  auto hit = [&](int64_t x) {
+    if (!step) return x < a.width && -x < b.width;
+    const int64_t lo = floor_div(-b.width - x, step) + 1, hi = -floor_div(x - a.width, step) - 1;
+    return (lo > -(a.n - 1) ? lo : -(a.n - 1)) <= (hi < b.n - 1 ? hi : b.n - 1);
+  };
+  if (!a.inner || !b.inner || a.inner == b.inner) {
+    for (int64_t j = -(a.m - 1); j < b.m; ++j)
+      if (hit(apart + j * inner)) return true;
+    return false;
+  }
+  if (a.m * b.m > 1 << 14) return true;
+  for (int64_t i = 0; i < a.m; ++i)
+    for (int64_t j = 0; j < b.m; ++j)
+      if (hit(apart + j * b.inner - i * a.inner)) return true;
+  return false;
+}
+
+struct Operand {
+  const char* name;
+  Area area;
+};
+// The first `written` operands share no byte with any other.
+int check_apart(const char* what, const Operand* ops, int written, int n) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (meet(ops[i].area, ops[j].area))
+        return fail(MUON_E_INVAL, "%s: %s overlaps %s (or lies between its rows with other strides)", what, ops[i].name,
+                    ops[j].name);
+  return MUON_OK;
+}
 
 // ------------------------------------------------------------- layer norm --
 int check_norm(const muon_layernorm_desc* d) {
@@ -48,6 +109,9 @@ int check_norm(const muon_layernorm_desc* d) {
   if (!(d->eps >= 0.f) || !std::isfinite(d->eps))
     return fail(MUON_E_INVAL, "layer norm: eps must be finite and not negative");
   if (d->reserved != 0) return fail(MUON_E_INVAL, "layer norm: reserved field must be 0");
+  for (int i = 0; i < 4; ++i)
+    if ((double)d->rows * (double)(lds[i] ? lds[i] : d->cols) > kMaxElements)
+      return fail(MUON_E_INVAL, "layer norm: rows=%lld of %s exceed any memory", (long long)d->rows, names[i]);
   return MUON_OK;
 }
 
@@ -56,6 +120,10 @@ size_t norm_workspace(const muon_layernorm_desc* d) {
 }
 
 int64_t ld_of(int64_t ld, int64_t cols) { return ld ? ld : cols; }
+Area rows_area(const muon_layernorm_desc* d, const void* p, int64_t ld) {
+  const int es = elem_size(d->x_dtype);
+  return area(p, d->rows, ld_of(ld, d->cols) * es, 1, 0, d->cols * es);
+}
 
 // -------------------------------------------------------------- attention --
 int check_attention(const muon_attention_desc* d) {
@@ -107,24 +175,21 @@ int check_heads(const muon_attention_desc* d, const muon_heads* v, const char* n
 size_t attention_part_bytes(const muon_attention_desc* d, int splits) {
   return splits > 1 ? (size_t)splits * d->tokens * d->kv_heads * 2 * d->head_dim * sizeof(float) : 0;
 }
-// Whether two blocks of rows * cols elements share one.  Decided where their
-// leading dimensions agree (views of one buffer).
-bool rows_meet(const muon_layernorm_desc* d, const void* p, int64_t ld_p, const void* q, int64_t ld_q) {
-  const uint64_t es = elem_size(d->x_dtype), w = d->cols * es, ld = ld_of(ld_p, d->cols) * es;
-  if (!p || !q || ld_of(ld_p, d->cols) != ld_of(ld_q, d->cols)) return p && p == q;
-  const uint64_t a = (uint64_t)(uintptr_t)p, b = (uint64_t)(uintptr_t)q, apart = a < b ? b - a : a - b;
-  const uint64_t k = apart / ld, r = apart % ld, n = d->rows;  // the later block starts k rows and r bytes on
-  return (k < n && r < w) || (k + 1 < n && ld - r < w);
-}
 int splits_of(const muon_attention_desc* d) {
   return attention_splits(d->tokens, d->seqs, d->q_heads, d->kv_heads);
 }
+size_t lse_bytes(const muon_attention_desc* d) { return (size_t)d->q_heads * d->tokens * sizeof(float); }
 size_t attention_row_bytes(const muon_attention_desc* d) {  // one fp32 per query row
-  return align_up((size_t)d->q_heads * d->tokens * sizeof(float));
+  return align_up(lse_bytes(d));
 }
 size_t attention_workspace(const muon_attention_desc* d) {
   return 2 * attention_row_bytes(d) + align_up(attention_part_bytes(d, splits_of(d))) +
          kAlign;  // never 0, which means an error
+}
+
+Area heads_area(const muon_attention_desc* d, const HeadView& v, int heads) {
+  const int es = elem_size(d->dtype);
+  return area(v.data, d->tokens, v.token * es, heads, v.head * es, d->head_dim * es);
 }
 
 AttnArgs common_args(const muon_attention_desc* d, const int32_t* cu, uint32_t flags) {
@@ -152,11 +217,14 @@ int muon_layernorm_forward(const muon_layernorm_desc* d, const void* x, const vo
   if (int rc = check_norm(d)) return rc;
   if (d->rows == 0) return MUON_OK;
   if (!x || !y || !mean || !rstd) return fail(MUON_E_INVAL, "layer norm: x, y, mean or rstd is NULL");
-  if (rows_meet(d, x, d->ld_x, y, d->ld_y)) return fail(MUON_E_INVAL, "layer norm: y overlaps x");
   const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
   if (misaligned(x, es) || misaligned(y, es) || misaligned(weight, ps) || misaligned(bias, ps) ||
       misaligned(mean, 4) || misaligned(rstd, 4))
     return fail(MUON_E_INVAL, "layer norm: pointer not aligned to its element size");
+  const Operand ops[] = {{"y", rows_area(d, y, d->ld_y)},     {"mean", flat(mean, d->rows * 4)},
+                         {"rstd", flat(rstd, d->rows * 4)},   {"x", rows_area(d, x, d->ld_x)},
+                         {"weight", flat(weight, d->cols * ps)}, {"bias", flat(bias, d->cols * ps)}};
+  if (int rc = check_apart("layer norm", ops, 3, 6)) return rc;
   NormArgs a{};
   a.x = x, a.weight = weight, a.bias = bias, a.out = y, a.mean = mean, a.rstd = rstd;
   a.rows = d->rows, a.cols = (int32_t)d->cols, a.eps = d->eps;
@@ -179,11 +247,8 @@ int muon_layernorm_backward(const muon_layernorm_desc* d, const void* dy, const 
   if (int rc = check_norm(d)) return rc;
   if (!dx && !dweight && !dbias) return fail(MUON_E_INVAL, "layer norm: dx, dweight and dbias are all NULL");
   const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
-  if (d->rows > 0) {
-    if (!dy || !x || !mean || !rstd) return fail(MUON_E_INVAL, "layer norm: dy, x, mean or rstd is NULL");
-    if (rows_meet(d, dy, d->ld_dy, dx, d->ld_dx) || rows_meet(d, x, d->ld_x, dx, d->ld_dx))
-      return fail(MUON_E_INVAL, "layer norm: dx overlaps dy or x");
-  }
+  if (d->rows > 0 && (!dy || !x || !mean || !rstd))
+    return fail(MUON_E_INVAL, "layer norm: dy, x, mean or rstd is NULL");
   if (misaligned(x, es) || misaligned(dy, es) || misaligned(dx, es) || misaligned(weight, ps) || misaligned(mean, 4) ||
       misaligned(rstd, 4) || misaligned(dweight, 4) || misaligned(dbias, 4))
     return fail(MUON_E_INVAL, "layer norm: pointer not aligned to its element size");
@@ -195,6 +260,16 @@ int muon_layernorm_backward(const muon_layernorm_desc* d, const void* dy, const 
       return fail(MUON_E_WORKSPACE, "layer norm: workspace has %zu bytes, the call needs %zu", ws_bytes,
                   norm_workspace(d));
   }
+  const Operand ops[] = {{"dx", rows_area(d, dx, d->ld_dx)},
+                         {"dweight", flat(dweight, d->cols * 4)},
+                         {"dbias", flat(dbias, d->cols * 4)},
+                         {"workspace", flat(sums ? workspace : nullptr, norm_workspace(d))},
+                         {"dy", rows_area(d, dy, d->ld_dy)},
+                         {"x", rows_area(d, x, d->ld_x)},
+                         {"mean", flat(mean, d->rows * 4)},
+                         {"rstd", flat(rstd, d->rows * 4)},
+                         {"weight", flat(weight, d->cols * ps)}};
+  if (int rc = check_apart("layer norm", ops, 4, 9)) return rc;
   NormArgs a{};
   a.x = x, a.dy = dy, a.weight = weight, a.out = dx;
   a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
@@ -228,8 +303,11 @@ int muon_attention_forward(const muon_attention_desc* d, const int32_t* cu_seqle
   if (!rc) rc = check_heads(d, v, "v", d->kv_heads, false, &a.v);
   if (!rc) rc = check_heads(d, out, "out", d->q_heads, true, &a.o);
   if (rc) return rc;
-  if (a.o.data == a.q.data || a.o.data == a.k.data || a.o.data == a.v.data)
-    return fail(MUON_E_INVAL, "attention: out must not be an input");
+  const Operand ops[] = {{"out", heads_area(d, a.o, d->q_heads)}, {"lse", flat(lse, lse_bytes(d))},
+                         {"q", heads_area(d, a.q, d->q_heads)},   {"k", heads_area(d, a.k, d->kv_heads)},
+                         {"v", heads_area(d, a.v, d->kv_heads)},
+                         {"cu_seqlens", flat(cu_seqlens, ((size_t)d->seqs + 1) * 4)}};
+  if ((rc = check_apart("attention", ops, 2, 6))) return rc;
   a.lse = lse;
   const hipError_t e = launch_attention_forward(a, d->dtype == MUON_DTYPE_BF16, (hipStream_t)hip_stream);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "attention forward launch");
@@ -262,17 +340,18 @@ int muon_attention_backward(const muon_attention_desc* d, const int32_t* cu_seql
   if (!rc) rc = check_heads(d, dk, "dk", d->kv_heads, true, &a.dk);
   if (!rc) rc = check_heads(d, dv, "dv", d->kv_heads, true, &a.dv);
   if (rc) return rc;
-  const void* ins[] = {a.dout.data, a.q.data, a.k.data, a.v.data, a.o.data};
-  for (const void* p : ins)
-    if (p == a.dq.data || p == a.dk.data || p == a.dv.data)
-      return fail(MUON_E_INVAL, "attention: dq, dk and dv must not be inputs");
-  if (a.dq.data == a.dk.data || a.dq.data == a.dv.data || a.dk.data == a.dv.data)
-    return fail(MUON_E_INVAL, "attention: dq, dk and dv must be distinct");
   if (!workspace) return fail(MUON_E_WORKSPACE, "attention: workspace is NULL");
   if (misaligned(workspace, kAlign)) return fail(MUON_E_WORKSPACE, "attention: workspace is not 256-byte aligned");
   if (ws_bytes < attention_workspace(d))
     return fail(MUON_E_WORKSPACE, "attention: workspace has %zu bytes, the call needs %zu", ws_bytes,
                 attention_workspace(d));
+  const Operand ops[] = {{"dq", heads_area(d, a.dq, d->q_heads)},    {"dk", heads_area(d, a.dk, d->kv_heads)},
+                         {"dv", heads_area(d, a.dv, d->kv_heads)},   {"workspace", flat(workspace, attention_workspace(d))},
+                         {"dout", heads_area(d, a.dout, d->q_heads)}, {"q", heads_area(d, a.q, d->q_heads)},
+                         {"k", heads_area(d, a.k, d->kv_heads)},     {"v", heads_area(d, a.v, d->kv_heads)},
+                         {"out", heads_area(d, a.o, d->q_heads)},    {"lse", flat(lse, lse_bytes(d))},
+                         {"cu_seqlens", flat(cu_seqlens, ((size_t)d->seqs + 1) * 4)}};
+  if ((rc = check_apart("attention", ops, 4, 11))) return rc;
   a.lse = const_cast<float*>(lse);
   a.splits = splits_of(d);
   a.delta = (float*)workspace;

@@ -242,6 +242,81 @@ def test_reference_check_sees_a_wrong_value():
                 R.check(name, other[name][0], *good[name])
 
 
+# --------------------------------------------------- operands that share memory --
+Q = 1 << 20  # apart from P by more than any operand below
+
+
+def test_layer_norm_refuses_outputs_that_share_memory(lib):
+    """Statistics, parameter gradients and the workspace too, and rows of different steps."""
+    d = norm_desc()  # 8 rows of 64 bf16: 1024 bytes; fp32 parameters: 256 bytes
+    fwd = dict(x=P, weight=P + Q, bias=P + 2 * Q, y=P + 3 * Q, mean=P + 4 * Q, rstd=P + 5 * Q)
+    for over in (dict(mean=P + 1020), dict(rstd=P + Q + 252), dict(mean=P + 3 * Q), dict(rstd=P + 4 * Q + 28),
+                 dict(y=P + 2 * Q + 254), dict(mean=P + 2 * Q - 28), dict(y=P + 5 * Q - 1022)):
+        args = {**fwd, **over}
+        assert lib.muon_layernorm_forward(ctypes.byref(d), *args.values(), None) == INVAL, over
+        assert "overlap" in _lib.last_error()
+    strided = norm_desc(ld_x=128, ld_y=64)
+    for y in (P + 128, P - 512, P + 7 * 256 + 126):
+        assert lib.muon_layernorm_forward(ctypes.byref(strided), *{**fwd, "y": y}.values(), None) == INVAL
+        assert "overlap" in _lib.last_error()
+    need = lib.muon_layernorm_workspace_size(ctypes.byref(d))
+    bwd = dict(dy=P, x=P + Q, weight=P + 2 * Q, mean=P + 3 * Q, rstd=P + 4 * Q, dx=P + 5 * Q, dw=P + 6 * Q,
+               db=P + 7 * Q, ws=P + 8 * Q)
+    for over in (dict(dw=P), dict(db=P + Q + 1020), dict(dw=P + 7 * Q + 252), dict(dx=P + 6 * Q), dict(db=P + 3 * Q),
+                 dict(dw=P + 4 * Q + 28), dict(ws=P), dict(ws=P + 7 * Q), dict(ws=P + 5 * Q), dict(dx=P + 2 * Q),
+                 dict(dx=P + 3 * Q - 1020), dict(ws=P + 4 * Q)):
+        args = {**bwd, **over}
+        assert lib.muon_layernorm_backward(ctypes.byref(d), *args.values(), need, None) == INVAL, over
+        assert "overlap" in _lib.last_error()
+
+
+def test_layer_norm_refuses_rows_past_any_memory(lib):
+    assert lib.muon_layernorm_workspace_size(ctypes.byref(norm_desc(rows=1 << 40, ld_dy=1 << 31))) == 0
+    assert "exceed" in _lib.last_error()
+
+
+# (token stride, head stride, bytes from the first operand's start to the second's) for 100 tokens, 4 heads, 64 bf16
+FUSED = 12 * 64  # one buffer of (100, 12, 64)
+SHARED = [(FUSED, 64, 3 * 128), (FUSED, 64, -3 * 128), (FUSED, 64, 99 * FUSED * 2 + 3 * 128),
+          (FUSED, 64, 9 * 128),  # its last head is the first head of the next token
+          (FUSED, 192, 128 - 16), (FUSED, 192, 3 * 128), (64, 6400, 16), (64, 6400, 3 * 12800 + 99 * 128),
+          (64, 6400, -12800), (64, 6400, 12800 - 128)]
+
+
+@pytest.mark.parametrize("token,head,apart", SHARED, ids=str)
+def test_attention_refuses_outputs_inside_other_operands(lib, token, head, apart):
+    d = attn_desc(kv_heads=4)
+    far = {n: heads(4, P + (10 + i) * Q, token=token, head=head) for i, n in
+           enumerate(("q", "k", "v", "out", "dout", "dq", "dk", "dv"))}
+    far.update(cu=P, lse=P + Q, ws=P + 64 * Q)
+    for other in ("q", "k", "v"):
+        over = {**far, "out": heads(4, far[other].data + apart, token=token, head=head)}
+        assert attn_call(lib, d, False, **over) == INVAL, other
+        assert "overlap" in _lib.last_error()
+    for mine in ("dq", "dk", "dv"):
+        for other in set(("q", "k", "v", "out", "dout", "dq", "dk", "dv")) - {mine}:
+            over = {**far, mine: heads(4, far[other].data + apart, token=token, head=head)}
+            assert attn_call(lib, d, True, **over) == INVAL, (mine, other)
+            assert "overlap" in _lib.last_error()
+
+
+def test_attention_refuses_outputs_of_other_strides_and_flat_buffers(lib):
+    d = attn_desc(kv_heads=4)
+    far = {n: heads(4, P + (10 + i) * Q, token=FUSED) for i, n in
+           enumerate(("q", "k", "v", "out", "dout", "dq", "dk", "dv"))}
+    far.update(cu=P, lse=P + Q, ws=P + 64 * Q)
+    q, out, dq = far["q"].data, far["out"].data, far["dq"].data
+    for over in (dict(out=heads(4, q + 512, token=256)), dict(out=heads(4, q + 128, token=FUSED, head=128)),
+                 dict(lse=q), dict(lse=out + 99 * FUSED * 2), dict(lse=P - 1596), dict(cu=P + Q + 1596),
+                 dict(cu=out + 3 * 128), dict(out=heads(4, P - 16, token=FUSED))):
+        assert attn_call(lib, d, False, **{**far, **over}) == INVAL, over
+        assert "overlap" in _lib.last_error()
+    for over in (dict(ws=q + 256), dict(ws=dq), dict(ws=P + Q), dict(dq=heads(4, P - 128, token=FUSED)),
+                 dict(dk=heads(4, P + Q, token=FUSED)), dict(dv=heads(4, q + 512, token=256))):
+        assert attn_call(lib, d, True, **{**far, **over}) == INVAL, over
+        assert "overlap" in _lib.last_error()
+
+
 # ------------------------------------------------------------ the sources --
 def test_every_barrier_before_a_tile_is_overwritten_waits_for_lds_reads():
     """A copy into a tile may only start when every wave's reads of it have returned.  The compiler orders its LDS

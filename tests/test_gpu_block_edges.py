@@ -91,3 +91,53 @@ def test_attention_later_tokens_never_reach_earlier_ones(dim, dtype, extra):
             clean(name, got, after, [0])
             clean(name, got, everything, [1])
         assert not torch.isfinite(got["dv"][:t + 1, 0, 2].float()).any()
+
+
+# ------------------------------------------------ operands of one buffer that share nothing --
+@pytest.mark.parametrize("layout", ["tokens, heads", "heads, tokens", "tokens, heads, operands"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_operands_between_each_others_rows(layout, dtype):
+    """Inputs and outputs of one buffer: the same bits as in buffers of their own, and nothing else is written."""
+    n, H, D = 150, 2, 64
+    names = ("q", "k", "v", "dout", "out", "dq", "dk", "dv")
+    cu = cu_of([100, 50])
+    if layout == "tokens, heads":
+        buf = randn((n, 8 * H, D), 950, dtype).to(DEV)
+        view = {x: buf[:, i * H:(i + 1) * H] for i, x in enumerate(names)}
+    elif layout == "heads, tokens":
+        buf = randn((8 * H, n, D), 950, dtype).to(DEV)
+        view = {x: buf[i * H:(i + 1) * H].transpose(0, 1) for i, x in enumerate(names)}
+    else:
+        buf = randn((n, H, 8, D), 950, dtype).to(DEV)
+        view = {x: buf[:, :, i] for i, x in enumerate(names)}
+    q, k, v, do = (view[x].contiguous() for x in names[:4])
+    out, lse = lib.packed_attention_forward(q, k, v, cu)
+    want = dict(zip(names[5:], lib.packed_attention_backward(do, q, k, v, out, lse, cu)), out=out, q=q, k=k, v=v,
+                dout=do)
+    _, lse2 = lib.packed_attention_forward(view["q"], view["k"], view["v"], cu, out=view["out"])
+    lib.packed_attention_backward(view["dout"], view["q"], view["k"], view["v"], view["out"], lse2, cu,
+                                  dq=view["dq"], dk=view["dk"], dv=view["dv"])
+    assert torch.equal(lse, lse2)
+    for x in names:
+        assert torch.equal(view[x], want[x]), x
+
+
+def test_binding_refuses_outputs_that_share_memory():
+    n, H, D = 20, 2, 64
+    buf = torch.zeros(n, 4 * H, D, device=DEV, dtype=BF)
+    q, k, v = buf[:, :H], buf[:, H:2 * H], buf[:, 2 * H:3 * H]
+    cu = cu_of([n])
+    out, lse = lib.packed_attention_forward(q, k, v, cu)
+    x = torch.zeros(16, 64, device=DEV)
+    y, mean, rstd = lib.layer_norm_forward(x)
+    calls = [lambda: lib.packed_attention_forward(q, k, v, cu, out=buf[:, 1:1 + H]),
+             lambda: lib.packed_attention_forward(q, k, v, cu, out=buf.view(-1)[8:8 + n * H * D].view(n, H, D)),
+             lambda: lib.packed_attention_backward(out, q, k, v, out, lse, cu, dk=buf[:, 3 * H - 1:4 * H - 1]),
+             lambda: lib.packed_attention_backward(out, q, k, v, out, lse, cu, dq=buf[:, 3 * H:], dv=buf[:, 3 * H:]),
+             lambda: lib.layer_norm_forward(x[:8], out=x[1:9]),
+             lambda: lib.layer_norm_forward(x[:8, :32], out=x.view(-1)[:256].view(8, 32)),
+             lambda: lib.layer_norm_backward(y[:8], x[:8], mean[:8], rstd[:8], dx=y[7:15])]
+    for i, call in enumerate(calls):
+        with pytest.raises(lib._lib.MuonError, match="overlap"):
+            call()
+            raise AssertionError(f"call {i} was not refused")
