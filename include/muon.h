@@ -336,7 +336,9 @@ int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, con
  * to its tokens 0 .. i.  Query head h reads key/value head
  * h / (q_heads / kv_heads).  head_dim: a multiple of 8, at most 128.  dtype:
  * MUON_DTYPE_BF16 or MUON_DTYPE_F32, of every operand.  scale, from 2^-60 to
- * 2^60, multiplies the scores.
+ * 2^60, multiplies the scores.  (tokens / 128 + seqs + 1) * q_heads must stay
+ * below 2^24 (fp32 with head_dim up to 64: (tokens / 64 + seqs + 1) * q_heads
+ * below 2^23), or the call is refused (MUON_E_UNSUPPORTED).
  *
  * cu_seqlens is not checked (it is read on the device); offsets outside
  * [0, tokens] are clamped and decreasing ones make empty sequences, so no

@@ -1231,6 +1231,11 @@ int attention_splits(int64_t tokens, int seqs, int q_heads, int kv_heads) {
   return s;
 }
 
+int64_t attention_threads(int64_t tokens, int seqs, int q_heads, int dim, bool bf16) {
+  const bool narrow = !bf16 && dim <= 64;  // kNarrow
+  return slots_of(tokens, seqs, narrow ? 64 : 128) * q_heads * (narrow ? 512 : 256);
+}
+
 hipError_t launch_attention_forward(const AttnArgs& a, bool bf16, hipStream_t stream) {
   return bf16 ? by_dim<__bf16>(a, false, stream) : by_dim<float>(a, false, stream);
 }

@@ -19,6 +19,7 @@ constexpr int64_t kMaxStride = (int64_t)1 << 31;
 constexpr double kMaxElements = 0x1p56;  // byte offsets fit 64 bits
 constexpr int64_t kMaxTokenStride = 1 << 24;  // a 64-row tile stays within 32-bit byte offsets
 constexpr int64_t kMaxTokens = 0x7FFFFF00;
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;  // of one launch
 constexpr int kMaxSeqs = 1 << 24;
 constexpr int kMaxHeads = 1 << 16;
 constexpr int kMaxDim = 128;
@@ -142,7 +143,7 @@ int check_attention(const muon_attention_desc* d) {
   if (!(d->scale >= kMinScale && d->scale <= 1.f / kMinScale))
     return fail(MUON_E_INVAL, "attention: scale %g outside [2^-60, 2^60]", d->scale);
   if (d->reserved != 0) return fail(MUON_E_INVAL, "attention: reserved field must be 0");
-  if ((d->tokens / 64 + d->seqs + 1) * (int64_t)d->q_heads > 0x7FFFFFFF)
+  if (attention_threads(d->tokens, d->seqs, d->q_heads, d->head_dim, d->dtype == MUON_DTYPE_BF16) > kMaxThreads)
     return fail(MUON_E_UNSUPPORTED, "attention: %lld tokens, %d sequences and %d heads exceed one launch's grid",
                 (long long)d->tokens, d->seqs, d->q_heads);
   return MUON_OK;

@@ -79,6 +79,9 @@ struct AttnArgs {
 enum { kZeroOut = 1, kZeroLse = 2 };               // AttnArgs::zero_tail, forward
 enum { kZeroDq = 1, kZeroDk = 2, kZeroDv = 4 };    // and backward
 
+// Threads of the largest launch: one for the query rows.  (Twice as many a
+// block where blocks are few do not count.)
+int64_t attention_threads(int64_t tokens, int seqs, int q_heads, int dim, bool bf16);
 int attention_splits(int64_t tokens, int seqs, int q_heads, int kv_heads);
 hipError_t launch_attention_forward(const AttnArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_attention_backward(const AttnArgs& a, bool bf16, hipStream_t stream);

@@ -134,6 +134,23 @@ def test_attention_refuses_descriptors(lib, kw, code):
     assert lib.muon_attention_workspace_size(ctypes.byref(d)) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(dtype=0), dict(dtype=0, head_dim=128), dict(head_dim=128)], ids=str)
+def test_attention_refuses_what_one_launch_cannot_hold(lib, kw):
+    """A launch has fewer than 2^32 threads: blocks of 256 for 128 query rows, or 512 for 64 (fp32, heads up to 64)."""
+    rows, most = (64, (1 << 23) - 1) if kw == dict(dtype=0) else (128, (1 << 24) - 1)
+    for heads_, seqs in ((40, 2), (1, 1000), (1, most // 2), (40, 0)):
+        slots = most // heads_
+        last = min((slots - seqs - 1) * rows + rows - 1, 0x7FFFFF00)
+        ok, over = ({**kw, "tokens": t, "seqs": seqs, "q_heads": heads_, "kv_heads": heads_} for t in (last, last + 1))
+        assert lib.muon_attention_workspace_size(ctypes.byref(attn_desc(**ok))) > 0
+        if last < 0x7FFFFF00:
+            d = attn_desc(**over)
+            assert attn_call(lib, d, False) == UNSUP and attn_call(lib, d, True) == UNSUP
+            assert lib.muon_attention_workspace_size(ctypes.byref(d)) == 0 and "launch" in _lib.last_error()
+    d = attn_desc(**{**kw, "seqs": 1 << 24, "q_heads": 1, "kv_heads": 1})
+    assert attn_call(lib, d, False) == UNSUP
+
+
 @pytest.mark.parametrize("back", [False, True])
 def test_attention_refuses_operands(lib, back):
     d = attn_desc()

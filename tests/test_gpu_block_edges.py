@@ -141,3 +141,23 @@ def test_binding_refuses_outputs_that_share_memory():
         with pytest.raises(lib._lib.MuonError, match="overlap"):
             call()
             raise AssertionError(f"call {i} was not refused")
+
+
+# ------------------------------------------------------------ the largest launches --
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_most_sequences_of_one_launch(dtype):
+    """As many sequences as the launch's 2^32 threads allow, nearly all of them empty."""
+    n, D = 100, 32
+    seqs = (1 << 24) - 2 if dtype == BF else (1 << 23) - 2 - n // 64
+    q, k, v, do = (randn((n, 1, D), 960 + i, dtype) for i in range(4))
+    cu = torch.zeros(seqs + 1, dtype=torch.int32, device=DEV)
+    cu[seqs // 2:] = 40
+    cu[-1] = n
+    dev = [t.to(DEV) for t in (q, k, v, do)]
+    out, lse = lib.packed_attention_forward(*dev[:3], cu)
+    grads = lib.packed_attention_backward(dev[3], *dev[:3], out, lse, cu)
+    ref = R.attention(q, k, v, [40, 60], D ** -0.5, do)
+    for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        R.check(name, got, *ref[name])
+    with pytest.raises(lib._lib.MuonError, match="launch"):
+        lib.packed_attention_forward(*dev[:3], torch.zeros(seqs + 2, dtype=torch.int32, device=DEV))
