@@ -325,7 +325,7 @@ size_t muon_layernorm_workspace_size(const muon_layernorm_desc* desc);
 
 /* Gradients of the forward call: dx (x_dtype), dweight[cols] and dbias[cols]
  * (fp32, overwritten; zero when rows == 0).  Any of the three may be NULL, but
- * not all.  workspace (256-byte aligned) may be NULL when dweight and dbias are. */
+ * not all if there are rows.  workspace (256-byte aligned) may be NULL when dweight and dbias are. */
 int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, const void* x, const void* weight,
                             const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                             void* workspace, size_t ws_bytes, void* hip_stream);

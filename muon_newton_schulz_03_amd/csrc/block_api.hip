@@ -246,7 +246,8 @@ int muon_layernorm_backward(const muon_layernorm_desc* d, const void* dy, const 
                             void* workspace, size_t ws_bytes, void* hip_stream) {
   clear_error();
   if (int rc = check_norm(d)) return rc;
-  if (!dx && !dweight && !dbias) return fail(MUON_E_INVAL, "layer norm: dx, dweight and dbias are all NULL");
+  if (d->rows > 0 && !dx && !dweight && !dbias)
+    return fail(MUON_E_INVAL, "layer norm: dx, dweight and dbias are all NULL");
   const int es = elem_size(d->x_dtype), ps = elem_size(d->p_dtype);
   if (d->rows > 0 && (!dy || !x || !mean || !rstd))
     return fail(MUON_E_INVAL, "layer norm: dy, x, mean or rstd is NULL");

@@ -71,6 +71,13 @@ def test_layer_norm_refuses_pointers(lib):
     assert fwd(ctypes.byref(norm_desc(rows=0)), None, None, None, None, None, None, None) == 0
 
 
+def test_layer_norm_without_rows_needs_nothing(lib):
+    """The dx of an empty batch is an empty tensor, whose pointer is NULL: with no sums wanted there is nothing to do."""
+    d = ctypes.byref(norm_desc(rows=0))
+    assert lib.muon_layernorm_backward(d, *[None] * 9, 0, None) == 0
+    assert lib.muon_layernorm_backward(d, *[None] * 6, P, None, None, 0, None) == WORK
+
+
 @pytest.mark.parametrize("ld,apart", [(0, 2), (0, 128), (0, 7 * 128 + 126), (200, 2), (200, 126), (200, 400),
                                       (200, 400 - 126), (200, 6 * 400 + 274), (200, 7 * 400 + 126)])
 def test_layer_norm_refuses_overlapping_rows(lib, ld, apart):

@@ -161,3 +161,16 @@ def test_attention_most_sequences_of_one_launch(dtype):
         R.check(name, got, *ref[name])
     with pytest.raises(lib._lib.MuonError, match="launch"):
         lib.packed_attention_forward(*dev[:3], torch.zeros(seqs + 2, dtype=torch.int32, device=DEV))
+
+
+# ---------------------------------------------------------------------- no rows --
+@pytest.mark.parametrize("need_weight", [False, True])
+@pytest.mark.parametrize("need_bias", [False, True])
+def test_layer_norm_gradients_of_an_empty_batch(need_weight, need_bias):
+    for shape in ((0, 96), (3, 0, 96)):
+        x = torch.empty(shape, device=DEV, dtype=BF)
+        y, mean, rstd = lib.layer_norm_forward(x)
+        dx, dw, db = lib.layer_norm_backward(y, x, mean, rstd, need_weight=need_weight, need_bias=need_bias)
+        assert dx.shape == shape and dx.dtype == BF
+        for g, need in ((dw, need_weight), (db, need_bias)):
+            assert (g is not None and g.shape == (96,) and (g == 0).all()) if need else g is None
