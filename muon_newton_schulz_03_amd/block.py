@@ -2,6 +2,12 @@
 
 Each has a forward and a backward call; the caller keeps what the backward
 call needs (its inputs, and the statistics that the forward call returns).
+Where torch records gradients (grad mode is on and an input requires grad),
+the forward calls take part: y and out carry a graph whose backward pass is
+the backward call.  It is differentiable once, and the statistics (mean, rstd,
+lse) pass no gradient on: one that arrives there raises.  The backward calls
+themselves return plain values.  A given output cannot be recorded, so with
+such inputs it is refused.
 Every call runs in the HIP library on the current torch stream of the
 tensors' device, which need not be the current device; this module checks
 the tensors, allocates outputs that are not given, and the workspace, with
@@ -15,6 +21,8 @@ import math
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import AttentionDesc, Heads, LayerNormDesc
@@ -85,6 +93,33 @@ class _On:
             self.guard.__exit__(*exc)
 
 
+_grad_on = torch.is_grad_enabled
+
+
+def _requires_grad(t) -> bool:
+    return getattr(t, "requires_grad", False)  # False for None, and for what is no tensor (refused later)
+
+
+def _recorded(a, b, c) -> bool:
+    """Whether torch differentiates with respect to one of these inputs."""
+    if _grad_on() and (_requires_grad(a) or _requires_grad(b) or _requires_grad(c)):
+        return True
+    return forward_ad._current_level >= 0 and any(
+        isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in (a, b, c))
+
+
+def _refuse_recorded(**given) -> None:
+    for name, t in given.items():
+        if t is not None:
+            raise ValueError(f"{name} cannot be given where gradients are recorded (use torch.no_grad() and the "
+                             "backward call, or leave it out)")
+
+
+def _only_values(name: str, *grads) -> None:
+    if any(g is not None for g in grads):
+        raise RuntimeError(f"{name} pass no gradient on: detach them")
+
+
 def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
                        eps: float = 1e-5, out: Optional[torch.Tensor] = None
                        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
@@ -93,6 +128,13 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, b
     x: float32 or bfloat16, with a contiguous last dimension and rows of one
     stride.  weight and bias (one dtype, float32 or bfloat16) may be None.
     """
+    if _recorded(x, weight, bias):
+        _refuse_recorded(out=out)
+        return _LayerNorm.apply(x, weight, bias, eps)
+    return _norm_forward(x, weight, bias, eps, out)
+
+
+def _norm_forward(x, weight, bias, eps, out=None):
     lib = _lib.load()
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x is not a device tensor")
@@ -125,6 +167,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     dx has x's dtype; dweight and dbias are float32, and None where not needed.
     mean and rstd are the forward call's.
     """
+    return _norm_backward(dy, x, mean, rstd, weight, dx, True, need_weight, need_bias)
+
+
+def _norm_backward(dy, x, mean, rstd, weight, dx, need_x, need_weight, need_bias):
     lib = _lib.load()
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x is not a device tensor")
@@ -140,13 +186,16 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         if t.shape != x.shape[:-1] or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and of x's leading shape")
     pt, w = _param(weight, "weight", cols, dev, None)
+    own = dx is None
     with _On(dev):
-        if dx is None:
+        if dx is not None:
+            _check(dx, "dx", dev, x.dtype)
+            if dx.shape != x.shape:
+                raise ValueError("dx must have x's shape")
+        elif need_x:
             dx = x.new_empty(x.shape)
-        _check(dx, "dx", dev, x.dtype)
-        if dx.shape != x.shape:
-            raise ValueError("dx must have x's shape")
-        d = LayerNormDesc(rows, cols, ld, 0, _rows(dy, "dy")[2], _rows(dx, "dx")[2], _DTYPES[x.dtype],
+        d = LayerNormDesc(rows, cols, ld, 0, _rows(dy, "dy")[2], 0 if own else _rows(dx, "dx")[2],
+                          _DTYPES[x.dtype],
                           _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], 0.0, 0)
         dw = x.new_empty(cols, dtype=torch.float32) if need_weight else None
         db = x.new_empty(cols, dtype=torch.float32) if need_bias else None
@@ -157,10 +206,37 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                 raise _lib.MuonError(_lib.MUON_E_INVAL, _lib.last_error())
             ws = x.new_empty(nbytes, dtype=torch.uint8)
         _lib.check(lib.muon_layernorm_backward(
-            ctypes.byref(d), dy.data_ptr(), x.data_ptr(), w, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-            None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
+            ctypes.byref(d), dy.data_ptr(), x.data_ptr(), w, mean.data_ptr(), rstd.data_ptr(),
+            None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+            None if db is None else db.data_ptr(),
             None if ws is None else ws.data_ptr(), nbytes, _stream(dev.index)))
     return dx, dw, db
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = _norm_forward(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.set_materialize_grads(False)
+        ctx.params = [None if p is None else p.dtype for p in (weight, bias)]
+        return y, mean, rstd
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dmean, drstd):
+        _only_values("layer norm's mean and rstd", dmean, drstd)
+        need = ctx.needs_input_grad
+        if dy is None or not any(need[:3]):
+            return None, None, None, None
+        x, weight, mean, rstd = ctx.saved_tensors
+        try:
+            _rows(dy, "dy")
+        except ValueError:  # the gradient of a sum, for example, repeats one value
+            dy = dy.contiguous()
+        dx, dw, db = _norm_backward(dy, x, mean, rstd, weight, None, need[0], need[1], need[2])
+        dw, db = (g if g is None else g.to(dtype) for g, dtype in zip((dw, db), ctx.params))
+        return dx, dw, db, None
 
 
 def _heads(t: torch.Tensor, name: str, device, dtype, shape) -> Heads:
@@ -212,6 +288,13 @@ def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     the backward call.  Rows behind the last sequence are zero in results that
     this call allocates and left as they were in those given.
     """
+    if _recorded(q, k, v):
+        _refuse_recorded(out=out, lse=lse)
+        return _Attention.apply(q, k, v, cu_seqlens, scale)
+    return _attention_forward(q, k, v, cu_seqlens, scale, out, lse)
+
+
+def _attention_forward(q, k, v, cu_seqlens, scale, out=None, lse=None):
     lib = _lib.load()
     d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
     dev, flags = q.device, 0
@@ -271,3 +354,27 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
             ctypes.byref(hv), ctypes.byref(ho), lse.data_ptr(), ctypes.byref(gq), ctypes.byref(gk), ctypes.byref(gv),
             flags, ws.data_ptr(), nbytes, _stream(dev.index)))
     return dq, dk, dv
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale):
+        out, lse = _attention_forward(q, k, v, cu_seqlens, scale)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        ctx.scale = scale
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dlse):
+        _only_values("attention's lse", dlse)
+        if dout is None:
+            return None, None, None, None, None
+        q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
+        token, head, elem = dout.stride()
+        size = dout.element_size()
+        if elem != 1 or token > 1 << 24 or any(n % 16 for n in (token * size, head * size, dout.data_ptr())):
+            dout = dout.contiguous()  # the gradient of a sum, for example, repeats one value
+        grads = packed_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=ctx.scale)
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None)

@@ -227,6 +227,20 @@ def test_binding_refuses_tensors_before_any_call():
             rows(bad, "x")
 
 
+def test_binding_refuses_given_outputs_where_gradients_are_recorded():
+    """Before anything else: writing into a given tensor would lose the gradients without a word."""
+    x, y = torch.zeros(4, 8, requires_grad=True), torch.zeros(4, 8)
+    q, cu = torch.zeros(4, 2, 8, requires_grad=True), torch.zeros(2, dtype=torch.int32)
+    calls = [lambda: block.layer_norm_forward(x, out=y), lambda: block.layer_norm_forward(y, x[0], out=y),
+             lambda: block.packed_attention_forward(q, y, y, cu, out=y),
+             lambda: block.packed_attention_forward(y, y, q, cu, lse=y)]
+    for call in calls:
+        with pytest.raises(ValueError, match="recorded"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):
+            call()
+
+
 # ------------------------------------------------- the reference's own pins --
 def test_reference_gradients_against_differences():
     """The fp64 formulas' gradients equal autograd's, and central differences, on the CPU."""

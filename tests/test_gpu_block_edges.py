@@ -174,3 +174,167 @@ def test_layer_norm_gradients_of_an_empty_batch(need_weight, need_bias):
         assert dx.shape == shape and dx.dtype == BF
         for g, need in ((dw, need_weight), (db, need_bias)):
             assert (g is not None and g.shape == (96,) and (g == 0).all()) if need else g is None
+
+
+# --------------------------------------------------------------- torch's gradients --
+def leaves(*tensors):
+    return [t.detach().clone().requires_grad_(True) for t in tensors]
+
+
+@pytest.mark.parametrize("dtype,pdtype", [(BF, F32), (BF, BF), (F32, F32)])
+def test_layer_norm_takes_part_in_autograd(dtype, pdtype):
+    x, dy = randn((3, 7, 96), 970, dtype).to(DEV), randn((3, 7, 96), 971, dtype).to(DEV)
+    w, b = (1 + randn((96,), 972, std=0.2)).to(pdtype).to(DEV), randn((96,), 973, pdtype).to(DEV)
+    y0, mean, rstd = lib.layer_norm_forward(x, w, b)
+    assert not y0.requires_grad
+    want = lib.layer_norm_backward(dy, x, mean, rstd, w)
+    for wanted in ((1, 1, 1), (1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 1, 1)):
+        args = [t.clone().requires_grad_(bool(n)) for t, n in zip((x, w, b), wanted)]
+        y, _, _ = lib.layer_norm_forward(*args)
+        assert torch.equal(y, y0)
+        y.backward(dy)
+        for t, g, n in zip(args, want, wanted):
+            assert (t.grad is None) if not n else (t.grad.dtype == t.dtype and torch.equal(t.grad, g.to(t.dtype)))
+    xl, = leaves(x)  # without parameters; the gradient of a sum repeats one value; a gradient of other strides
+    y, mean, rstd = lib.layer_norm_forward(xl)
+    y.sum().backward()
+    assert torch.equal(xl.grad, lib.layer_norm_backward(torch.ones_like(x), x, mean, rstd)[0])
+    xl, = leaves(x)
+    lib.layer_norm_forward(xl, w, b)[0].transpose(0, 2).backward(dy.transpose(0, 2))
+    assert torch.equal(xl.grad, want[0])
+    with torch.no_grad():
+        y, _, _ = lib.layer_norm_forward(xl, w, b)
+    assert not y.requires_grad and torch.equal(y, y0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_takes_part_in_autograd(dtype):
+    T, H, G, D = 150, 4, 2, 64
+    cu = cu_of([100, 45])
+    qkv, do = randn((T, H + 2 * G, D), 980, dtype).to(DEV), randn((T, H, D), 981, dtype).to(DEV)
+    cut = lambda t: (t[:, :H], t[:, H:H + G], t[:, H + G:])  # noqa: E731
+    out0, lse0 = lib.packed_attention_forward(*cut(qkv), cu)
+    want = lib.packed_attention_backward(do, *cut(qkv), out0, lse0, cu)
+    leaf, = leaves(qkv)  # slices of one projection
+    out, lse = lib.packed_attention_forward(*cut(leaf), cu)
+    assert torch.equal(out, out0) and torch.equal(lse, lse0)
+    out.backward(do)
+    assert torch.equal(leaf.grad, torch.cat(want, 1))
+    for wanted in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0)):
+        args = [t.clone().requires_grad_(bool(n)) for t, n in zip(cut(qkv), wanted)]
+        lib.packed_attention_forward(*args, cu)[0].backward(do)
+        for t, g, n in zip(args, want, wanted):
+            assert (t.grad is None) if not n else torch.equal(t.grad, g)
+    for weight in (torch.ones((), device=DEV, dtype=dtype).expand(T, H, D), do.transpose(0, 1).contiguous().transpose(0, 1),
+                   torch.cat([do[..., :1], do], 2)[..., 1:], do[:, :1].expand(T, H, D)):
+        leaf, = leaves(qkv)
+        lib.packed_attention_forward(*cut(leaf), cu)[0].backward(weight)
+        g = lib.packed_attention_backward(weight.contiguous(), *cut(qkv), out0, lse0, cu)
+        assert torch.equal(leaf.grad, torch.cat(g, 1))
+    k1, v1 = leaves(qkv[:, H:H + 1], qkv[:, H + 1:H + 2])  # one head's memory for all: its gradient is their sum
+    out, _ = lib.packed_attention_forward(qkv[:, :H], k1.expand(T, H, D), v1.expand(T, H, D), cu)
+    out.backward(do)
+    ref = R.attention(qkv[:145, :H].cpu(), k1.detach()[:145].cpu(), v1.detach()[:145].cpu(), [100, 45], D ** -0.5,
+                      do[:145].cpu())
+    for g, name in ((k1.grad, "dk"), (v1.grad, "dv")):
+        value, bound = ref[name]
+        # four heads' results, each rounded, and torch's sum of them in this type
+        loose = 8 * R.unit(dtype) * (value.abs() + R.attention(
+            qkv[:145, :H].abs().cpu(), k1.detach()[:145].abs().cpu(), v1.detach()[:145].abs().cpu(), [100, 45],
+            D ** -0.5, do[:145].abs().cpu())["dv"][0].abs().amax())
+        R.check(name, g[:145], value, bound + loose)
+
+
+def test_gradients_that_would_be_lost_are_refused():
+    x, w = leaves(randn((6, 64), 990).to(DEV), randn((64,), 991).to(DEV))
+    q, k, v = leaves(*(randn((20, 2, 32), 992 + i).to(DEV) for i in range(3)))
+    cu = cu_of([20])
+    y, mean, rstd = lib.layer_norm_forward(x, w)
+    out, lse = lib.packed_attention_forward(q, k, v, cu)
+    for loss in (mean.sum() + y.sum(), rstd.sum(), lse.square().sum(), out.sum() + lse.sum()):
+        with pytest.raises(RuntimeError, match="pass no gradient on"):
+            torch.autograd.grad(loss, [x, w, q, k, v], retain_graph=True, allow_unused=True)
+    for z, t in ((y, x), (out, q)):  # differentiable once
+        g, = torch.autograd.grad(z.square().sum(), t, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.sum().backward()
+    buf = torch.zeros(6, 64, device=DEV)
+    with pytest.raises(ValueError, match="recorded"):
+        lib.layer_norm_forward(x, w, out=buf)
+    with pytest.raises(ValueError, match="recorded"):
+        lib.packed_attention_forward(q, k, v, cu, lse=torch.zeros(2, 20, device=DEV))
+    xd, qd, kd, vd = (t.detach() for t in (x, q, k, v))
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            lib.layer_norm_forward(torch.autograd.forward_ad.make_dual(xd, buf))
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            lib.packed_attention_forward(torch.autograd.forward_ad.make_dual(qd, kd), kd, vd, cu)
+    with pytest.raises(RuntimeError):
+        torch.vmap(lambda t: lib.layer_norm_forward(t)[0])(xd.view(2, 3, 64))
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda t: lib.layer_norm_forward(t)[0].sum())(xd)
+
+
+def block_loss(t, p):
+    """A block's forward pass on recorded tensors, as a model calls the operators."""
+    H, D, T = 4, 64, t["x"].shape[0]
+    y, _, _ = lib.layer_norm_forward(p["x"], p["w"], p["b"])
+    qkv = (y @ p["wqkv"]).view(T, 3 * H, D)
+    o, _ = lib.packed_attention_forward(qkv[:, :H], qkv[:, H:2 * H], qkv[:, 2 * H:], t["cu"])
+    return (o.reshape(T, H * D) @ p["wo"] * t["dout"]).sum()
+
+
+def block_data(lengths, seed):
+    T, width = sum(lengths), 256
+    t = dict(x=randn((T, width), seed), w=1 + randn((width,), seed + 1, std=0.1), b=randn((width,), seed + 2),
+             wqkv=randn((width, 3 * width), seed + 3, std=width ** -0.5), wo=randn((width, width), seed + 4, std=width ** -0.5),
+             dout=randn((T, width), seed + 5))
+    return {k: v.to(DEV) for k, v in t.items()}
+
+
+def test_block_under_autograd_on_streams_and_in_a_graph():
+    """A block recorded by torch against fp64 autograd, the same on another stream, and captured forward and backward."""
+    lengths, names = [70, 1, 129], ("x", "w", "b", "wqkv", "wo")
+    t = block_data(lengths, 1000)
+    t["cu"] = cu_of(lengths)
+    p = {n: leaves(t[n])[0] for n in names}
+    block_loss(t, p).backward()
+    got = {n: p[n].grad.clone() for n in names}
+    c = {n: t[n].double().cpu().requires_grad_(n in names) for n in (*names, "dout")}
+    T, H, D = sum(lengths), 4, 64
+    y = torch.nn.functional.layer_norm(c["x"], (H * D,), c["w"], c["b"], 1e-5)
+    qkv = (y @ c["wqkv"]).view(T, 3 * H, D).permute(1, 0, 2)
+    doc = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths))
+    i = torch.arange(T)
+    hidden = (doc[:, None] != doc[None]) | (i[None] > i[:, None])
+    s = (qkv[:H] @ qkv[H:2 * H].transpose(1, 2) * D ** -0.5).masked_fill(hidden, float("-inf"))
+    o = (torch.softmax(s, 2) @ qkv[2 * H:]).permute(1, 0, 2).reshape(T, H * D)
+    (o @ c["wo"] * c["dout"]).sum().backward()
+    for n in names:
+        rel = ((got[n].double().cpu() - c[n].grad).norm() / c[n].grad.norm()).item()
+        say(f"[gpu] block under autograd d{n}: rel {rel:.2e}")
+        assert rel <= 5 * 800 * 2.0 ** -24, (n, rel)  # five chained fp32 sums of at most 800 terms
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        p2 = {n: leaves(t[n])[0] for n in names}
+        block_loss(t, p2).backward()
+    side.synchronize()
+    for n in names:
+        assert torch.equal(p2[n].grad, got[n]), n
+    del p2
+    p3 = {n: leaves(t[n])[0] for n in names}  # leaves that no eager graph holds
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        grads = torch.autograd.grad(block_loss(t, p3), [p3[n] for n in names])
+    for rep in range(3):
+        with torch.no_grad():
+            p3["x"].copy_(randn(tuple(t["x"].shape), 1010 + rep).to(DEV))
+        t["cu"].copy_(cu_of([[70, 1, 129], [200, 0, 0], [64, 64, 72]][rep]))
+        graph.replay()
+        torch.cuda.synchronize()
+        q = {n: leaves(p3[n])[0] for n in names}
+        want = torch.autograd.grad(block_loss(t, q), [q[n] for n in names])
+        for n, a, b in zip(names, grads, want):
+            assert torch.equal(a, b), (rep, n)
