@@ -115,6 +115,20 @@ def _refuse_recorded(**given) -> None:
                              "backward call, or leave it out)")
 
 
+def _given(*outputs) -> list:
+    """The outputs that the caller gave, checked: torch must not take them for results of something else."""
+    outputs = [t for t in outputs if t is not None]
+    if outputs and _grad_on() and any(map(_requires_grad, outputs)):
+        raise ValueError("a given output requires grad, and writing into it would not be recorded")
+    return outputs
+
+
+def _written(outputs: list) -> None:
+    """Tells torch that given outputs were written, so that a graph that saved one notices."""
+    if outputs:
+        torch.autograd.graph.increment_version(outputs)
+
+
 def _only_values(name: str, *grads) -> None:
     if any(g is not None for g in grads):
         raise RuntimeError(f"{name} pass no gradient on: detach them")
@@ -144,17 +158,19 @@ def _norm_forward(x, weight, bias, eps, out=None):
     pt, w = _param(weight, "weight", cols, x.device, None)
     pt, b = _param(bias, "bias", cols, x.device, pt)
     with _On(x.device):
-        y = x.new_empty(x.shape) if out is None else out
+        y, given = x.new_empty(x.shape) if out is None else out, None
         if out is not None:
             _check(y, "out", x.device, x.dtype)
             if y.shape != x.shape:
                 raise ValueError("out must have x's shape")
+            given = _given(out)
         mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
         rstd = torch.empty_like(mean)
         d = LayerNormDesc(rows, cols, ld, 0 if out is None else _rows(y, "out")[2], 0, 0, _DTYPES[x.dtype],
                           _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], eps, 0)
         _lib.check(lib.muon_layernorm_forward(ctypes.byref(d), x.data_ptr(), w, b, y.data_ptr(), mean.data_ptr(),
                                               rstd.data_ptr(), _stream(x.device.index)))
+    _written(given)
     return y, mean, rstd
 
 
@@ -186,15 +202,16 @@ def _norm_backward(dy, x, mean, rstd, weight, dx, need_x, need_weight, need_bias
         if t.shape != x.shape[:-1] or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and of x's leading shape")
     pt, w = _param(weight, "weight", cols, dev, None)
-    own = dx is None
+    given = None
     with _On(dev):
         if dx is not None:
             _check(dx, "dx", dev, x.dtype)
             if dx.shape != x.shape:
                 raise ValueError("dx must have x's shape")
+            given = _given(dx)
         elif need_x:
             dx = x.new_empty(x.shape)
-        d = LayerNormDesc(rows, cols, ld, 0, _rows(dy, "dy")[2], 0 if own else _rows(dx, "dx")[2],
+        d = LayerNormDesc(rows, cols, ld, 0, _rows(dy, "dy")[2], 0 if given is None else _rows(dx, "dx")[2],
                           _DTYPES[x.dtype],
                           _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], 0.0, 0)
         dw = x.new_empty(cols, dtype=torch.float32) if need_weight else None
@@ -210,6 +227,7 @@ def _norm_backward(dy, x, mean, rstd, weight, dx, need_x, need_weight, need_bias
             None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
             None if db is None else db.data_ptr(),
             None if ws is None else ws.data_ptr(), nbytes, _stream(dev.index)))
+    _written(given)
     return dx, dw, db
 
 
@@ -297,7 +315,7 @@ def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
 def _attention_forward(q, k, v, cu_seqlens, scale, out=None, lse=None):
     lib = _lib.load()
     d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
-    dev, flags = q.device, 0
+    dev, flags, given = q.device, 0, _given(out, lse)
     with _On(dev):
         if out is None:
             out, flags = q.new_empty(q.shape), flags | _lib.ATTENTION_ZERO_OUT
@@ -309,6 +327,7 @@ def _attention_forward(q, k, v, cu_seqlens, scale, out=None, lse=None):
         _lib.check(lib.muon_attention_forward(
             ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
             ctypes.byref(ho), lse.data_ptr(), flags, _stream(dev.index)))
+    _written(given)
     return out, lse
 
 
@@ -332,7 +351,7 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     """
     lib = _lib.load()
     d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
-    dev, flags = q.device, 0
+    dev, flags, given = q.device, 0, _given(dq, dk, dv)
     _check_lse(lse, q)
     dtype, qs, ks = q.dtype, q.shape, k.shape
     hdo, ho = _heads(dout, "dout", dev, dtype, qs), _heads(out, "out", dev, dtype, qs)
@@ -353,6 +372,7 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
             ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hdo), ctypes.byref(hq), ctypes.byref(hk),
             ctypes.byref(hv), ctypes.byref(ho), lse.data_ptr(), ctypes.byref(gq), ctypes.byref(gk), ctypes.byref(gv),
             flags, ws.data_ptr(), nbytes, _stream(dev.index)))
+    _written(given)
     return dq, dk, dv
 
 

@@ -264,6 +264,13 @@ def test_gradients_that_would_be_lost_are_refused():
     with pytest.raises(ValueError, match="recorded"):
         lib.packed_attention_forward(q, k, v, cu, lse=torch.zeros(2, 20, device=DEV))
     xd, qd, kd, vd = (t.detach() for t in (x, q, k, v))
+    st = lib.layer_norm_forward(xd)[1:]
+    o, l = lib.packed_attention_forward(qd, kd, vd, cu)
+    for call in (lambda: lib.layer_norm_forward(xd, out=x), lambda: lib.layer_norm_backward(buf, xd, *st, dx=x * 1),
+                 lambda: lib.packed_attention_forward(qd, kd, vd, cu, out=q * 1),
+                 lambda: lib.packed_attention_backward(o, qd, kd, vd, o, l, cu, dk=k * 1)):
+        with pytest.raises(ValueError, match="requires grad"):
+            call()
     with torch.autograd.forward_ad.dual_level():
         with pytest.raises((RuntimeError, NotImplementedError)):
             lib.layer_norm_forward(torch.autograd.forward_ad.make_dual(xd, buf))
@@ -273,6 +280,31 @@ def test_gradients_that_would_be_lost_are_refused():
         torch.vmap(lambda t: lib.layer_norm_forward(t)[0])(xd.view(2, 3, 64))
     with pytest.raises(RuntimeError):
         torch.func.grad(lambda t: lib.layer_norm_forward(t)[0].sum())(xd)
+
+
+def test_a_graph_that_saved_a_given_output_notices_that_it_was_written():
+    x = randn((6, 64), 995).to(DEV)
+    q = randn((20, 2, 32), 996).to(DEV)
+    cu = cu_of([20])
+    y, mean, rstd = lib.layer_norm_forward(x)
+    out, lse = lib.packed_attention_forward(q, q, q, cu)
+    writes = [((6, 64), lambda t: lib.layer_norm_forward(x, out=t)),
+              ((6, 64), lambda t: lib.layer_norm_backward(y, x, mean, rstd, dx=t)),
+              ((20, 2, 32), lambda t: lib.packed_attention_forward(q, q, q, cu, out=t)),
+              ((2, 20), lambda t: lib.packed_attention_forward(q, q, q, cu, lse=t)),
+              ((20, 2, 32), lambda t: lib.packed_attention_backward(out, q, q, q, out, lse, cu, dq=t)),
+              ((20, 2, 32), lambda t: lib.packed_attention_backward(out, q, q, q, out, lse, cu, dk=t)),
+              ((20, 2, 32), lambda t: lib.packed_attention_backward(out, q, q, q, out, lse, cu, dv=t))]
+    for i, (shape, write) in enumerate(writes):
+        leaf, saved = torch.ones(shape, device=DEV, requires_grad=True), torch.ones(shape, device=DEV)
+        loss = (leaf * saved).sum()
+        write(saved)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+            raise AssertionError(f"write {i} went unnoticed")
+    with torch.inference_mode():
+        given = torch.empty_like(x)
+        assert torch.equal(lib.layer_norm_forward(x, out=given)[0], y)
 
 
 def block_loss(t, p):
