@@ -370,3 +370,73 @@ def test_block_under_autograd_on_streams_and_in_a_graph():
         want = torch.autograd.grad(block_loss(t, q), [q[n] for n in names])
         for n, a, b in zip(names, grads, want):
             assert torch.equal(a, b), (rep, n)
+
+
+# ------------------------------------------------------- groups split over blocks --
+def splits_of(T, seqs, H, G, D, dtype):
+    """The parts that a group's query heads are split into, from the workspace: two rows' words, and the parts."""
+    d = lib._lib.AttentionDesc(T, seqs, H, G, D, int(dtype == BF), 1.0, 0)
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    rest = lib._lib.load().muon_attention_workspace_size(d) - 2 * up(H * T * 4) - 256
+    return max(1, rest // (T * G * 2 * D * 4))
+
+
+def check_attention(lengths, H, G, D, dtype, seed, tail=0):
+    T, n = sum(lengths) + tail, sum(lengths)
+    q, k, v, do = (randn((T, h, D), seed + i, dtype) for i, h in enumerate((H, G, G, H)))
+    dev = [t.to(DEV) for t in (q, k, v, do)]
+    for t in dev:
+        t[n:] = float("nan")  # never read
+    got = run_attention(*dev, cu_of(lengths))
+    ref = R.attention(q, k, v, lengths, D ** -0.5, do)
+    for name, x in got.items():
+        R.check(name, x, *ref[name])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,G", [(8, 2), (6, 3), (9, 3)])
+@pytest.mark.parametrize("D", [32, 64, 80, 128])
+def test_attention_split_groups(H, G, D, dtype):
+    """Partial dK and dV of several key/value heads, summed by a launch of their own."""
+    for lengths, tail in (([1100], 0), ([1300], 77)):
+        splits = splits_of(sum(lengths) + tail, 1, H, G, D, dtype)
+        say(f"[gpu] split groups {lengths} tail {tail} heads {H}/{G} dim {D} {dtype}: {splits} parts")
+        assert splits == H // G
+        check_attention(lengths, H, G, D, dtype, 1100, tail)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_split_groups_of_many_heads(dtype):
+    """Splits in grids that take one group of waves a block (bf16), of two sequences, and of groups in parts of
+    several heads."""
+    for lengths, H, G, parts in (([400, 650], 192, 48, 4), ([900], 64, 16, 4), ([700, 500], 256, 32, 4)):
+        splits = splits_of(sum(lengths), len(lengths), H, G, 32, dtype)
+        say(f"[gpu] split groups {lengths} heads {H}/{G} {dtype}: {splits} parts")
+        assert splits == parts
+        check_attention(lengths, H, G, 32, dtype, 1200)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_split_groups_see_no_masked_nan(D, dtype):
+    n, H, G, t = 1100, 8, 2, 601
+    assert splits_of(n, 1, H, G, D, dtype) == 4
+    q, k, v, do = (randn((n, h, D), 1300 + i, dtype) for i, h in enumerate((H, G, G, H)))
+    ref = R.attention(q, k, v, [n], D ** -0.5, do)
+    q[t, 5, 3], do[t, 6, 7] = float("nan"), float("inf")  # heads of key/value head 1
+    got = run_attention(q, k, v, do, cu_of([n]))
+    for name in ("dk", "dv"):
+        x = got[name].cpu()
+        R.check(name, x[:, :1], *(r[:, :1] for r in ref[name]))
+        R.check(name, x[t + 1:, 1], *(r[t + 1:, 1] for r in ref[name]))
+    assert not torch.isfinite(got["dv"][:t + 1, 1, 7].float()).any()
+
+
+# -------------------------------------------------------------- searches for a tile --
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("seqs", [63, 64, 65, 128, 129, 192, 193, 255, 256, 257, 300])
+def test_attention_sequence_counts(seqs, dtype):
+    """Around every step of the searches for a block's tile: short sequences, empty ones, and some of several tiles."""
+    lengths = [129 + i * 53 % 272 if i % 29 == 3 else i * 37 % 41 for i in range(seqs)]
+    check_attention(lengths, 2, 1, 32, dtype, 1400, tail=seqs % 3 * 70)
+    check_attention(lengths[::-1], 2, 2, 32, dtype, 1410, tail=0)
