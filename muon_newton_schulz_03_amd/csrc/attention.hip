@@ -876,7 +876,6 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
     const int head = head0 + min(n / nq, hpp - 1), row0 = n < total ? (qt0 + n % nq) * QR : st.len;
     cp.seek(a.q, head, a.dout, head, st.start + (int64_t)row0, st.len - row0, w);
     cp.template copy<1>(lds[grp][b][0], w, lane);
-    // rows past the end get zeros, which q and dout have there too: p = 1, ds = 0, and neither adds anything
     if (w < 2)
       dma_b32(buffer_of((w ? a.delta : a.lse2) + (int64_t)head * a.tokens + st.start + row0,
                         4 * min(st.len - row0, QR)), lds_offset(stat[grp][b][w]), 4 * lane);
@@ -886,14 +885,15 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
     for (int t = 0; t < DT; ++t) dk[t] = f32x16{}, dv[t] = f32x16{};
     copy(0);
     wait_tiles();
-    for (int it = 0; it * NG < total; ++it) {  // past the last tile: zeros, which add nothing
+    for (int it = 0; it * NG < total; ++it) {
       const char *ql = lds[grp][it & 1][0], *dl = lds[grp][it & 1][1];
       const float *ll = stat[grp][it & 1][0], *el = stat[grp][it & 1][1];
       const int q0 = (qt0 + (it * NG + grp) % nq) * QR;
+      const int end = it * NG + grp < total ? st.len : 0;  // of the rows in this tile
       if ((it + 1) * NG < total) copy(it + 1);
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        if (q0 + 32 * j + 31 < kw) continue;  // rows before every key of this wave
+        if (q0 + 32 * j + 31 < kw || q0 + 32 * j >= end) continue;  // rows before every key of this wave, or none
         f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
         for (int q = 0; q < ST; ++q) s = Elem<T>::mma(Tl::row_frag(ql, 32 * j + col, q, h), kf[q], s);
@@ -911,10 +911,13 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
             ds[i] = p[i] * (dp[i] - del[e]);
           }
         }
-        if (q0 + 32 * j < kw + 31) {
+        // A row before some key, or past the last one: it is all zeros, but 0 times a key's infinity is NaN.
+        if (q0 + 32 * j < kw + 31 || q0 + 32 * j + 32 > end) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (q0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3) < ki) p[i] = ds[i] = 0.f;
+          for (int i = 0; i < 16; ++i) {
+            const int row = q0 + 32 * j + 8 * (i >> 2) + 4 * h + (i & 3);
+            if (row < ki || row >= end) p[i] = ds[i] = 0.f;
+          }
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -1047,10 +1050,11 @@ __global__ __launch_bounds__(NG * kThreads, kDkvWaves<DP>) void attention_dkv_bf
 #pragma unroll
     for (int i = 0; i < kSlots - 1; ++i) copy();
     const int total = ((st.len - st.row0 + QR - 1) / QR * hpp + NG - 1) / NG;
-    for (int i = 0; i < total; ++i) {  // a group's rows past the last: zeros, which add nothing
+    for (int i = 0; i < total; ++i) {
       wait_but<(kSlots - 2) * (Pair::kN + 1)>();
       copy();
       const char* sl = ring + (i & (kSlots - 1)) * kSlot;
+      const int end = NG > 1 && rhead >= head0 + hpp ? 0 : st.len;  // of the rows in this slot
 #pragma unroll 1
       for (int j = 0; j < QR; j += 32) {
         if (careful.value && row + j + 31 < kw) continue;  // rows before every key of this wave
@@ -1071,10 +1075,13 @@ __global__ __launch_bounds__(NG * kThreads, kDkvWaves<DP>) void attention_dkv_bf
           else
             dp = Elem<T>::mma(Tl::row_frag(ol, col, q, h), Tl::row_frag(vt, 32 * w + col, q, h), dp);
         }
-        if (row + j < kw + 31) {  // a row before some key
+        // A row before some key, or past the last one: it is all zeros, but 0 times a key's infinity is NaN.
+        if (row + j < kw + 31 || row + j + 32 > end) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (row + j + 8 * (e >> 2) + 4 * h + (e & 3) < ki) s[e] = -__builtin_inff(), dp[e] = 0.f;
+          for (int e = 0; e < 16; ++e) {
+            const int r = row + j + 8 * (e >> 2) + 4 * h + (e & 3) - ki;  // rows behind the lane's key
+            if ((uint32_t)r >= (uint32_t)max(end - ki, 0)) s[e] = -__builtin_inff(), dp[e] = 0.f;
+          }
         }
         float p[16], ds[16];
 #pragma unroll

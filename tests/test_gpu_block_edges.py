@@ -93,6 +93,29 @@ def test_attention_later_tokens_never_reach_earlier_ones(dim, dtype, extra):
         assert not torch.isfinite(got["dv"][:t + 1, 0, 2].float()).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("n,H,G,extra", [(33, 2, 1, 0), (65, 2, 2, 0), (300, 4, 2, 0), (300, 4, 2, 40), (1100, 8, 2, 0)])
+def test_attention_gradients_of_keys_with_scores_of_minus_infinity(n, H, G, extra, dim, dtype):
+    """Such keys have weight 0: their dk and dv are zero, whatever the sequence's length, and all other gradients those
+    of keys whose weights vanish (the reference's have scores below -120, and so weights below 1e-50)."""
+    q, k, v, do = (randn((n, h, dim), 940 + i, dtype) for i, h in enumerate((H, G, G, H)))
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    dead = [1, 2, 30, n - 2] + list(range(40, min(n - 3, 200)))
+    far = k.clone()
+    far[dead, :, 0] = -2.0 ** 12
+    k[dead, :, 0] = float("-inf")
+    got = run_attention(q, k, v, do, cu_of([n] + [0] * extra))
+    ref = R.attention(q, far, v, [n], dim ** -0.5, do, dtype)
+    for name in ("dk", "dv"):
+        assert (got[name][dead] == 0).all(), name
+    for name, x in got.items():
+        if name == "dq":  # -inf times a weight of 0: the formula has NaN in this place
+            R.check(name, x[..., 1:], *(t[..., 1:] for t in ref[name]))
+        else:
+            R.check(name, x, *ref[name])
+
+
 # ------------------------------------------------ operands of one buffer that share nothing --
 @pytest.mark.parametrize("layout", ["tokens, heads", "heads, tokens", "tokens, heads, operands"])
 @pytest.mark.parametrize("dtype", [BF, F32])
