@@ -343,7 +343,7 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&acc)[DP / 32], const T* 
 template <class T, int DP, int NG>
 constexpr int kForwardWaves = sizeof(T) == 4 ? (DP == 32 ? 4 : 2) : DP == 32 ? 5 : DP == 64 ? 4 : DP == 96 && NG == 1 ? 3 : 2;
 template <class T, int DP, int NG>
-constexpr int kDqWaves = sizeof(T) == 4 ? (DP == 32 ? 3 : 2) : DP == 32 ? 4 : DP == 64 && NG == 1 ? 3 : 2;
+constexpr int kDqWaves = sizeof(T) == 4 ? (DP == 32 ? 3 : DP == 128 ? 1 : 2) : DP == 32 ? 4 : DP == 64 && NG == 1 ? 3 : 2;
 template <int DP>
 constexpr int kDkvWaves = DP == 32 ? 4 : DP == 64 ? 3 : 2;
 struct Yes {
@@ -1198,8 +1198,13 @@ hipError_t backward_dp(const AttnArgs& a, hipStream_t stream) {
       e = launch_kernel(attention_dkv_kernel<DP, 2, 4>, grid_of(a, a.kv_heads * a.splits, 64), 512, a, stream);
   } else {
     const int64_t gq = grid_of(a, a.q_heads, 128), gk = grid_of(a, a.kv_heads * a.splits, 128);
-    e = two_groups(a, gq) ? launch_kernel(attention_dq_kernel<T, DP, 4, 2>, gq, 512, a, stream)
-                          : launch_kernel(attention_dq_kernel<T, DP, 4, 1>, gq, 256, a, stream);
+    // fp32 at heads of 128: one group and one wave a SIMD.  With two of either, 145 registers spill: 2048 tokens of
+    // 12 heads 977 and 1079 us backward, 128 tokens of 8/2 heads 188 and 202.
+    if constexpr (sizeof(T) == 4 && DP == 128)
+      e = launch_kernel(attention_dq_kernel<T, DP, 4, 1>, gq, 256, a, stream);
+    else
+      e = two_groups(a, gq) ? launch_kernel(attention_dq_kernel<T, DP, 4, 2>, gq, 512, a, stream)
+                            : launch_kernel(attention_dq_kernel<T, DP, 4, 1>, gq, 256, a, stream);
     if (e != hipSuccess) return e;
     if constexpr (sizeof(T) == 2)
       e = two_groups(a, gk) ? launch_kernel(attention_dkv_bf16_kernel<DP, 2>, gk, 512, a, stream)
