@@ -96,14 +96,12 @@ class _On:
 _grad_on = torch.is_grad_enabled
 
 
-def _requires_grad(t) -> bool:
-    return getattr(t, "requires_grad", False)  # False for None, and for what is no tensor (refused later)
-
-
 def _recorded(a, b, c) -> bool:
-    """Whether torch differentiates with respect to one of these inputs."""
-    if _grad_on() and (_requires_grad(a) or _requires_grad(b) or _requires_grad(c)):
-        return True
+    """Whether torch differentiates with respect to one of these inputs (None, or no tensor: refused later, is none)."""
+    if _grad_on():
+        for t in (a, b, c):
+            if getattr(t, "requires_grad", False):
+                return True
     return forward_ad._current_level >= 0 and any(
         isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in (a, b, c))
 
@@ -118,15 +116,13 @@ def _refuse_recorded(**given) -> None:
 def _given(*outputs) -> list:
     """The outputs that the caller gave, checked: torch must not take them for results of something else."""
     outputs = [t for t in outputs if t is not None]
-    if outputs and _grad_on() and any(map(_requires_grad, outputs)):
+    if _grad_on() and any([t.requires_grad for t in outputs]):
         raise ValueError("a given output requires grad, and writing into it would not be recorded")
     return outputs
 
 
-def _written(outputs: list) -> None:
-    """Tells torch that given outputs were written, so that a graph that saved one notices."""
-    if outputs:
-        torch.autograd.graph.increment_version(outputs)
+# Tells torch that tensors were written, so that a graph that saved one notices.
+_written = torch.autograd.graph.increment_version
 
 
 def _only_values(name: str, *grads) -> None:
@@ -170,7 +166,8 @@ def _norm_forward(x, weight, bias, eps, out=None):
                           _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], eps, 0)
         _lib.check(lib.muon_layernorm_forward(ctypes.byref(d), x.data_ptr(), w, b, y.data_ptr(), mean.data_ptr(),
                                               rstd.data_ptr(), _stream(x.device.index)))
-    _written(given)
+    if given:
+        _written(given)
     return y, mean, rstd
 
 
@@ -227,7 +224,8 @@ def _norm_backward(dy, x, mean, rstd, weight, dx, need_x, need_weight, need_bias
             None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
             None if db is None else db.data_ptr(),
             None if ws is None else ws.data_ptr(), nbytes, _stream(dev.index)))
-    _written(given)
+    if given:
+        _written(given)
     return dx, dw, db
 
 
@@ -315,7 +313,7 @@ def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
 def _attention_forward(q, k, v, cu_seqlens, scale, out=None, lse=None):
     lib = _lib.load()
     d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
-    dev, flags, given = q.device, 0, _given(out, lse)
+    dev, flags, given = q.device, 0, None if out is None and lse is None else (out, lse)
     with _On(dev):
         if out is None:
             out, flags = q.new_empty(q.shape), flags | _lib.ATTENTION_ZERO_OUT
@@ -324,10 +322,12 @@ def _attention_forward(q, k, v, cu_seqlens, scale, out=None, lse=None):
             flags |= _lib.ATTENTION_ZERO_LSE
         ho = _heads(out, "out", dev, q.dtype, q.shape)
         _check_lse(lse, q)
+        given = given and _given(*given)
         _lib.check(lib.muon_attention_forward(
             ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hq), ctypes.byref(hk), ctypes.byref(hv),
             ctypes.byref(ho), lse.data_ptr(), flags, _stream(dev.index)))
-    _written(given)
+    if given:
+        _written(given)
     return out, lse
 
 
@@ -351,7 +351,7 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     """
     lib = _lib.load()
     d, hq, hk, hv = _attention(q, k, v, cu_seqlens, scale)
-    dev, flags, given = q.device, 0, _given(dq, dk, dv)
+    dev, flags, given = q.device, 0, (dq, dk, dv)
     _check_lse(lse, q)
     dtype, qs, ks = q.dtype, q.shape, k.shape
     hdo, ho = _heads(dout, "dout", dev, dtype, qs), _heads(out, "out", dev, dtype, qs)
@@ -364,6 +364,7 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
             dv, flags = q.new_empty(ks), flags | _lib.ATTENTION_ZERO_DV
         gq, gk = _heads(dq, "dq", dev, dtype, qs), _heads(dk, "dk", dev, dtype, ks)
         gv = _heads(dv, "dv", dev, dtype, ks)
+        given = _given(*given)
         nbytes = lib.muon_attention_workspace_size(ctypes.byref(d))
         if nbytes == 0:
             raise _lib.MuonError(_lib.MUON_E_INVAL, _lib.last_error())
@@ -372,7 +373,8 @@ def packed_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
             ctypes.byref(d), cu_seqlens.data_ptr(), ctypes.byref(hdo), ctypes.byref(hq), ctypes.byref(hk),
             ctypes.byref(hv), ctypes.byref(ho), lse.data_ptr(), ctypes.byref(gq), ctypes.byref(gk), ctypes.byref(gv),
             flags, ws.data_ptr(), nbytes, _stream(dev.index)))
-    _written(given)
+    if given:
+        _written(given)
     return dq, dk, dv
 
 

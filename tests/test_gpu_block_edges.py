@@ -463,3 +463,18 @@ def test_attention_sequence_counts(seqs, dtype):
     lengths = [129 + i * 53 % 272 if i % 29 == 3 else i * 37 % 41 for i in range(seqs)]
     check_attention(lengths, 2, 1, 32, dtype, 1400, tail=seqs % 3 * 70)
     check_attention(lengths[::-1], 2, 2, 32, dtype, 1410, tail=0)
+
+
+def test_binding_refuses_outputs_that_are_no_tensors():
+    x, q, cu = torch.zeros(4, 64, device=DEV), torch.zeros(8, 2, 64, device=DEV), cu_of([8])
+    y, mean, rstd = lib.layer_norm_forward(x)
+    out, lse = lib.packed_attention_forward(q, q, q, cu)
+    for bad in ("out", 3.0, [1]):
+        for call in (lambda: lib.layer_norm_forward(x, out=bad), lambda: lib.layer_norm_backward(y, x, mean, rstd, dx=bad),
+                     lambda: lib.layer_norm_forward(x, bad), lambda: lib.layer_norm_forward(bad),
+                     lambda: lib.packed_attention_forward(q, q, q, cu, out=bad),
+                     lambda: lib.packed_attention_forward(q, q, q, cu, lse=bad),
+                     lambda: lib.packed_attention_forward(q, bad, q, cu),
+                     lambda: lib.packed_attention_backward(out, q, q, q, out, lse, cu, dk=bad)):
+            with pytest.raises(ValueError, match="not a device tensor"):
+                call()
