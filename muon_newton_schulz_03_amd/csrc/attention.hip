@@ -21,14 +21,15 @@
 //     products instead of 5): adding dQ from the other kernel would need
 //     atomics, whose order changes results.
 //   * Registers decide: one wave alone on a SIMD issues a vector operation
-//     every 3 ns, two or more every 1.2 ns, so every kernel is shaped to have
-//     two to four waves a SIMD.  Hand-pipelined versions with one wave, or a
-//     tile of scores ahead, were slower or no faster (dK/dV at heads of 128:
-//     757 us against 507 now).
+//     every 3 ns, two or more every 1.2 ns, so the kernels are shaped to have
+//     two to four waves a SIMD; in fp32, dK/dV at heads above 64 and dQ at 128
+//     have one.  Hand-pipelined versions with one wave, or a tile of scores
+//     ahead, were slower or no faster (bf16 dK/dV at heads of 128: 757 us
+//     against 507 now).
 //   * What bounds the long bf16 runs: matrix and vector operations of the
-//     waves on a SIMD overlap in part; the MFMA units are busy 46 to 52% of
+//     waves on a SIMD overlap in part; the MFMA units are busy 45 to 52% of
 //     the time (a library GEMM: 69%).  Rates on 8192 tokens, 16 query and 4
-//     key/value heads of 128: forward 978, dQ 1030, dK/dV 1085 TFLOP/s of their
+//     key/value heads of 128: forward 978, dQ 1051, dK/dV 1085 TFLOP/s of their
 //     own products (library GEMM of 8192^3: 1410).
 #include "block_internal.h"
 #include "device_common.h"
@@ -539,8 +540,8 @@ __device__ __forceinline__ void zero_rows(const HeadView& v, int head, int row0,
 // vector operations at heads of 64 (per 64 keys and 32 rows: 156 of them, 740
 // clocks, against 512 of MFMA; 64 keys at a time rather than 32: 67 and 82 us
 // on 16384 packed tokens) and by the overlap of both at 128.  Times: 16384
-// tokens in 24 sequences, 12 heads of 64: 61 us (640 TFLOP/s of the visible
-// pairs); 16384 tokens, 16/4 heads of 128: 1061 us (1036 TFLOP/s).
+// tokens in 24 sequences, 12 heads of 64: 64 us (614 TFLOP/s of the visible
+// pairs); 16384 tokens, 16/4 heads of 128: 1077 us (1021 TFLOP/s).
 template <class T>
 struct Cfg {
   static constexpr int kKeys = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
@@ -695,8 +696,8 @@ __global__ __launch_bounds__(NG * WR * 64, (kForwardWaves<T, DP, NG>)) void atte
 // in bf16, -delta and -lse / scale, from which it starts its products' sums.
 // The forward kernel's layout, with dO's fragments in registers beside Q's and
 // no running maximum; ds is rounded to bf16 for its product.  Times: 16384
-// tokens in 24 sequences, 12 heads of 64: 87 us (676 TFLOP/s); 8192 tokens,
-// 16/4 heads of 128: 400 us (1030).
+// tokens in 24 sequences, 12 heads of 64: 89 us (661 TFLOP/s); 8192 tokens,
+// 16/4 heads of 128: 392 us (1051).
 template <class T, int DP, int WR, int NG>
 __global__ __launch_bounds__(NG * WR * 64, (kDqWaves<T, DP, NG>)) void attention_dq_kernel(AttnArgs a) {
   typedef typename Elem<T>::Frag Frag;
@@ -835,7 +836,7 @@ __global__ __launch_bounds__(NG * WR * 64, (kDqWaves<T, DP, NG>)) void attention
 // dK and dV of 32 WR keys of one key/value head, over the query heads of its
 // group (or of one part of it) and the query rows from the keys on, in fp32.
 // Bound by the fp32 MFMA (157 TFLOP/s): 2048 tokens in 5 sequences, 12 heads of
-// 64, 77 us with NG = 4 (MFMA busy 43%).
+// 64, 73 us with NG = 4 (MFMA busy 40%).
 template <int DP, int WR, int NG>
 __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_kernel(AttnArgs a) {
   typedef float T;

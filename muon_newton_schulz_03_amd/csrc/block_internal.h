@@ -63,9 +63,9 @@ struct AttnArgs {
   HeadView q, k, v, o;
   HeadView dout, dq, dk, dv;  // backward only
   float* lse;                 // (q_heads, tokens)
-  float* delta;               // backward workspace: (q_heads, tokens)
-  float* lse2;                // and again, lse / log 2
-  float* part;                // backward: partial dK, dV (see AttnSumArgs); null when one block owns a whole group
+  float* delta;               // backward workspace: (q_heads, tokens), delta; bf16: -delta
+  float* lse2;                // and again, lse / log 2; bf16: -lse / scale
+  float* part;                // backward: partial dK, dV, [split][token][kv head][2][dim]; null without splits
   const int32_t* cu;          // (seqs + 1) token offsets of the packed sequences
   int64_t tokens;
   int32_t seqs;

@@ -6,11 +6,11 @@
 // All arithmetic is fp32; the variance is the mean square of the centred
 // values, taken from registers, so a large common offset cancels nothing.
 //
-// Bound by memory: each operand moves once.  65536 x 768 in bf16: forward 35 us
-// (201 MB, 5.7 TB/s), backward 53 us (302 MB, 5.7 TB/s) and 4 us for the
-// parameter gradients' second stage, where a plain copy of 100 MB to 100 MB
-// reaches 7.1 TB/s from the Infinity Cache and one of 2 GiB 5.0; with inputs
-// that no cache holds, 44 us forward.
+// Bound by memory: each operand moves once.  65536 x 768 in bf16 with inputs
+// that no cache holds: forward 44 us (201 MB, 4.6 TB/s), both directions 101 us
+// (504 MB, 5.0 TB/s), where a plain copy of 2 GiB reaches 5.0 TB/s.  Where the
+// Infinity Cache holds the inputs (a copy of 100 MB: 7.1 TB/s): forward 36 us,
+// backward 54 us, and 5 us for the parameter gradients' second stage.
 #include "block_internal.h"
 #include "device_common.h"
 
@@ -229,7 +229,9 @@ __global__ __launch_bounds__(kThreads) void norm_forward_long_kernel(NormArgs a)
 // --------------------------------------------------------------- backward --
 // As the forward pass; every thread also sums its columns of dw and db over
 // its rows, the rows of a block are added through LDS, and the block's sums
-// go to part[block] (fixed order: the result does not depend on timing).
+// go to part[block] (fixed order: the result does not depend on timing).  Under
+// the bound of four waves a SIMD, rows of 256 threads and two vectors spill 12
+// registers with fp32 parameters, 2 with bf16.
 template <class T, class P, int TPR, int NV, bool PART>
 __global__ __launch_bounds__(kThreads, (kAhead<T, PART> && NV <= 2 ? 4 : 1)) void norm_backward_kernel(NormArgs a) {
   constexpr int VEC = kVec<T>;
