@@ -302,7 +302,8 @@ int muon_fused_limits(muon_plan* plan, int32_t spin_limit, int32_t dep_bias);
 /* Layer norm of `rows` rows of `cols` elements (cols <= 2^20).  Leading
  * dimensions are in elements (0 is read as cols).  x, y, dy and dx have
  * x_dtype; weight and bias have p_dtype, and a NULL one counts as ones or
- * zeros.  Arithmetic is fp32.  No alignment beyond an element's is needed. */
+ * zeros.  Arithmetic is fp32.  No alignment beyond an element's is needed.
+ * rows times a leading dimension is at most 2^56. */
 typedef struct muon_layernorm_desc {
   int64_t rows;
   int64_t cols;
