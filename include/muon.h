@@ -397,7 +397,8 @@ int muon_attention_forward(const muon_attention_desc* desc, const int32_t* cu_se
 size_t muon_attention_workspace_size(const muon_attention_desc* desc);
 
 /* Gradients of the forward call, from its inputs, its out and lse, and dout.
- * dq, dk and dv are overwritten (they may be slices of one buffer); dk and dv sum over the query heads of their group. */
+ * dq, dk and dv are overwritten (they may be slices of one buffer); dk and dv
+ * sum over the query heads of their group. */
 int muon_attention_backward(const muon_attention_desc* desc, const int32_t* cu_seqlens, const muon_heads* dout,
                             const muon_heads* q, const muon_heads* k, const muon_heads* v, const muon_heads* out,
                             const float* lse, const muon_heads* dq, const muon_heads* dk, const muon_heads* dv,

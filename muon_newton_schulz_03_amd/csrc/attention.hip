@@ -271,17 +271,16 @@ __device__ __forceinline__ void store_row(T* row, const f32x16 (&acc)[DP / 32], 
 
 // ---------------------------------------------- what a mask hides, no one sees --
 // A masked pair has weight 0, but 0 times a NaN or an infinity is NaN, and a
-// matrix instruction multiplies every pair of its block.  A block that is
-// masked as a whole is skipped; for the wave's block on the diagonal, every
-// pass ends with a test of the accumulators (0 x each, summed: a few dozen
-// operations a wave), and where one is not finite the thread block makes its
-// pass again, carefully: in the block on the diagonal, values of the right
-// operand that are not finite are taken as 0, and added afterwards to the rows
-// that see them.  The careful pass is code of its own, behind the first: one
-// loop with both ways in it cost 50 to 130 registers.  Times with the test and
-// without, forward and backward: 8192 tokens of 12 heads of 64 131 / 417 and
-// 133 / 421 us, 16/4 heads of 128 280 / 914 and 276 / 911; nothing but NaN takes
-// three times as long.
+// matrix instruction multiplies every pair of its block.  So every pass ends
+// with a test of the accumulators (0 x each, summed: a few dozen operations a
+// wave), and where one is not finite the thread block makes its pass again,
+// carefully: products that are masked as a whole are skipped, and in those on
+// the diagonal the streamed side's values that are not finite are taken as 0,
+// and added afterwards to the rows that see them.  The careful pass is code of
+// its own, behind the first: one loop with both ways in it cost 50 to 130
+// registers.  Times with the test and without, forward and backward: 8192
+// tokens of 12 heads of 64 131 / 417 and 133 / 421 us, 16/4 heads of 128
+// 280 / 914 and 276 / 911; nothing but NaN takes three times as long.
 template <class T>
 __device__ __forceinline__ typename Elem<T>::Frag finite_part(typename Elem<T>::Frag f, bool diag) {
   float v[8];
@@ -342,17 +341,20 @@ __device__ __forceinline__ void add_not_finite(f32x16 (&acc)[DP / 32], const T* 
 // Waves a SIMD that the first pass's registers leave room for.  As launch
 // bounds they make the careful pass spill where it would take more.
 template <class T, int DP, int NG>
-constexpr int kForwardWaves = sizeof(T) == 4 ? (DP == 32 ? 4 : 2) : DP == 32 ? 5 : DP == 64 ? 4 : DP == 96 && NG == 1 ? 3 : 2;
+constexpr int kForwardWaves = sizeof(T) == 4 ? (DP == 32 ? 4 : 2)
+                              : DP == 32     ? 5
+                              : DP == 64     ? 4
+                              : DP == 96     ? (NG == 1 ? 3 : 2)
+                                             : 2;
 template <class T, int DP, int NG>
-constexpr int kDqWaves = sizeof(T) == 4 ? (DP == 32 ? 3 : DP == 128 ? 1 : 2) : DP == 32 ? 4 : DP == 64 && NG == 1 ? 3 : 2;
+constexpr int kDqWaves = sizeof(T) == 4 ? (DP == 32    ? 3
+                                           : DP == 128 ? 1
+                                                       : 2)
+                         : DP == 32     ? 4
+                         : DP == 64     ? (NG == 1 ? 3 : 2)
+                                        : 2;
 template <int DP>
 constexpr int kDkvWaves = DP == 32 ? 4 : DP == 64 ? 3 : 2;
-struct Yes {
-  static constexpr bool value = true;
-};
-struct No {
-  static constexpr bool value = false;
-};
 
 // Adds the other groups of waves' accumulators to the first's, in order,
 // through LDS (kJoin bytes); true in the others, whose work is done.
@@ -648,9 +650,9 @@ __global__ __launch_bounds__(NG * WR * 64, (kForwardWaves<T, DP, NG>)) void atte
       wait_tiles();
     }
   };
-  pass(No{});
+  pass(std::false_type{});
   if (any_nan<NG * WR>(not_finite(o), flags, grp * WR + w)) {
-    pass(Yes{});
+    pass(std::true_type{});
     const int k0 = qw / KT * KT;
     if (grp == 0 && qi < st.len)
       add_not_finite<T, DP>(o, (const T*)a.v.data + (st.start + (int64_t)k0) * a.v.token + kvh * a.v.head, a.v.token,
@@ -815,10 +817,10 @@ __global__ __launch_bounds__(NG * WR * 64, (kDqWaves<T, DP, NG>)) void attention
     }
     return off;
   };
-  if (kFix && st.row0 == 0) delta += pass(No{});
-  float off = pass(No{});
+  if (kFix && st.row0 == 0) delta += pass(std::false_type{});
+  float off = pass(std::false_type{});
   if (any_nan<NG * WR>(not_finite(dq), flags, grp * WR + w)) {
-    off = pass(Yes{});
+    off = pass(std::true_type{});
     const int k0 = qw / KT * KT;
     if (grp == 0 && valid)
       add_not_finite<T, DP>(dq, (const T*)a.k.data + (st.start + (int64_t)k0) * a.k.token + kvh * a.k.head, a.k.token,
@@ -926,7 +928,10 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
 #pragma unroll
           for (int t = 0; t < DT; ++t) {
             Frag of = Tl::col_frag(dl, 32 * j + 16 * u, t, lane), qf = Tl::col_frag(ql, 32 * j + 16 * u, t, lane);
-            if (careful.value) of = finite_part<T>(of, q0 + 32 * j < kw + 31), qf = finite_part<T>(qf, q0 + 32 * j < kw + 31);
+            if (careful.value) {
+              const bool diag = q0 + 32 * j < kw + 31;
+              of = finite_part<T>(of, diag), qf = finite_part<T>(qf, diag);
+            }
             dv[t] = Elem<T>::mma(of, pf, dv[t]);
             dk[t] = Elem<T>::mma(qf, sf, dk[t]);
           }
@@ -935,9 +940,9 @@ __global__ __launch_bounds__(NG * WR * 64, DP <= 64 ? 2 : 1) void attention_dkv_
       wait_tiles();
     }
   };
-  pass(No{});
+  pass(std::false_type{});
   if (any_nan<NG * WR>(not_finite(dk) + not_finite(dv), flags, grp * WR + w)) {
-    pass(Yes{});
+    pass(std::true_type{});
     if (grp == 0 && valid)
       for (int head = head0; head < head0 + hpp; ++head) {
         const int64_t t0 = st.start + (int64_t)kw;
@@ -1106,10 +1111,10 @@ __global__ __launch_bounds__(NG * kThreads, kDkvWaves<DP>) void attention_dkv_bf
       for (int g = 0; g < NG; ++g) next(rhead, row);
     }
   };
-  pass(No{});
+  pass(std::false_type{});
   if (any_nan<NG * WR>(not_finite(dk) + not_finite(dv), flags, grp * WR + w)) {
     wait_tiles();  // the copies of rows past the last
-    pass(Yes{});
+    pass(std::true_type{});
     if (grp == 0 && valid)
       for (int head = head0; head < head0 + hpp; ++head) {
         const int64_t t0 = st.start + (int64_t)kw;

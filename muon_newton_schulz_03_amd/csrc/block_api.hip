@@ -348,7 +348,8 @@ int muon_attention_backward(const muon_attention_desc* d, const int32_t* cu_seql
     return fail(MUON_E_WORKSPACE, "attention: workspace has %zu bytes, the call needs %zu", ws_bytes,
                 attention_workspace(d));
   const Operand ops[] = {{"dq", heads_area(d, a.dq, d->q_heads)},    {"dk", heads_area(d, a.dk, d->kv_heads)},
-                         {"dv", heads_area(d, a.dv, d->kv_heads)},   {"workspace", flat(workspace, attention_workspace(d))},
+                         {"dv", heads_area(d, a.dv, d->kv_heads)},
+                         {"workspace", flat(workspace, attention_workspace(d))},
                          {"dout", heads_area(d, a.dout, d->q_heads)}, {"q", heads_area(d, a.q, d->q_heads)},
                          {"k", heads_area(d, a.k, d->kv_heads)},     {"v", heads_area(d, a.v, d->kv_heads)},
                          {"out", heads_area(d, a.o, d->q_heads)},    {"lse", flat(lse, lse_bytes(d))},
