@@ -351,7 +351,9 @@ int muon_layernorm_backward(const muon_layernorm_desc* desc, const void* dy, con
  *
  * bf16: products take bf16 operands (probabilities and score gradients are
  * rounded to bf16 for theirs) and accumulate in fp32, where softmax
- * statistics are held.  fp32: fp32 throughout.  A score of -inf has weight 0; a
+ * statistics are held.  fp32: fp32 throughout.  Scores and lse are fp32 numbers:
+ * a weight is off by about 2^-22 of itself times its score's magnitude, and from
+ * magnitudes of 2^30 on a row may be NaN.  A score of -inf has weight 0; a
  * row of nothing else is NaN.  What the mask hides does not count, whatever it
  * holds: a NaN or infinity in a token's k or v reaches the outputs of that
  * token and of later ones in its sequence, one in its q or dout the dk and dv
