@@ -8,6 +8,9 @@ the backward call.  It is differentiable once, and the statistics (mean, rstd,
 lse) pass no gradient on: one that arrives there raises.  The backward calls
 themselves return plain values.  A given output cannot be recorded, so with
 such inputs it is refused.
+A recorded backward pass may be captured in a graph under torch's own rule:
+forward and backward in the same capture, and no eager graph of the same
+leaves alive (torch ends the process otherwise, whatever the operators).
 Every call runs in the HIP library on the current torch stream of the
 tensors' device, which need not be the current device; this module checks
 the tensors, allocates outputs that are not given, and the workspace, with
