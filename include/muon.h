@@ -285,7 +285,11 @@ int muon_fused_limits(muon_plan* plan, int32_t spin_limit, int32_t dep_bias);
  * and an attention whose gradients end in those matrices: layer norm, and
  * causal attention over packed sequences (the overview page "The NanoGPT
  * speedrun", record #12, trains on documents packed into one long sequence
- * with document masking).  Both have a forward and a backward call.
+ * with document masking).  What that attention reads are queries and keys that
+ * are normalised for each head and rotated by position (the same page, records
+ * #2 and #5), and what the first block reads are rows of an embedding table:
+ * the embedding lookup, and the query/key norm with rotation.  Each has a
+ * forward and a backward call.
  *
  * They follow the conventions of the step: the caller owns every buffer, the
  * library allocates nothing and never waits for the device; every pointer is a
@@ -404,6 +408,113 @@ size_t muon_attention_workspace_size(const muon_attention_desc* desc);
 int muon_attention_backward(const muon_attention_desc* desc, const int32_t* cu_seqlens, const muon_heads* dout,
                             const muon_heads* q, const muon_heads* k, const muon_heads* v, const muon_heads* out,
                             const float* lse, const muon_heads* dq, const muon_heads* dk, const muon_heads* dv,
+                            uint32_t flags, void* workspace, size_t ws_bytes, void* hip_stream);
+
+#define MUON_INDEX_I32 0
+#define MUON_INDEX_I64 1
+
+/* Norm of queries and keys for each head, with the position rotation in the
+ * same pass: per token and head, with x the head's head_dim elements,
+ *   z = x * weight / sqrt(mean(x^2) + eps),
+ * and then, in the first `dim` elements of the rotation, each pair (a, b) is
+ * turned by its angle, position * frequency:
+ *   (a, b) <- (a cos - b sin, b cos + a sin).
+ * q and k have heads and weights of their own (weights: p_dtype, head_dim
+ * elements, the same for every head; NULL counts as ones).  head_dim: a
+ * multiple of 8, at most 128.  dtype: of q, k and every operand in their shape.
+ *
+ * Positions: `positions` (device, one per token, position_dtype; any value),
+ * or NULL: the offset within the token's sequence, with cu_seqlens (device,
+ * seqs + 1 int32, as in attention), and the token's number without it.  Rows
+ * behind the last sequence of cu_seqlens, if it is given, are never read; in
+ * each output they are left as they were, or set to zero when the output's
+ * flag is given.  cu_seqlens is not checked: with offsets that are not in
+ * order, positions are undefined, but no access leaves the operands.
+ *
+ * Arithmetic is fp32, results are rounded once.  Angles are exact to 2^-31
+ * turns at positions of magnitude up to 2^32, and off by up to 2^-63 turns
+ * times a farther position.  Squares are fp32 numbers, too: mean(x^2) + eps has
+ * to lie between 2^-120 and 2^120. */
+typedef struct muon_qk_norm_desc {
+  int64_t tokens;
+  int32_t seqs; /* of cu_seqlens */
+  int32_t q_heads;
+  int32_t k_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  int32_t p_dtype;
+  int32_t position_dtype; /* MUON_INDEX_* */
+  float eps;              /* >= 0 */
+  int32_t reserved;       /* must be 0 */
+} muon_qk_norm_desc;
+
+#define MUON_PAIRS_HALVES 0     /* elements i and i + dim / 2 */
+#define MUON_PAIRS_NEIGHBOURS 1 /* elements 2 i and 2 i + 1 */
+
+/* frequencies: host array of dim / 2 angles in radians per position, each
+ * within [-64, 64], read during the call.  dim: a multiple of 8, at most
+ * head_dim; 0, or a NULL rotation, turns nothing. */
+typedef struct muon_rotation {
+  const double* frequencies;
+  int32_t dim;
+  int32_t pairs;
+} muon_rotation;
+
+#define MUON_QK_ZERO_Q 1 /* zero the rows of q_out (backward: dq) behind the last sequence */
+#define MUON_QK_ZERO_K 2 /* and of k_out, dk */
+
+int muon_qk_norm_forward(const muon_qk_norm_desc* desc, const muon_rotation* rotation, const int32_t* cu_seqlens,
+                         const void* positions, const muon_heads* q, const muon_heads* k, const void* q_weight,
+                         const void* k_weight, const muon_heads* q_out, const muon_heads* k_out, uint32_t flags,
+                         void* hip_stream);
+
+/* Bytes of device workspace muon_qk_norm_backward needs for its weight
+ * gradients; 0 on invalid arguments.  Host-only. */
+size_t muon_qk_norm_workspace_size(const muon_qk_norm_desc* desc);
+
+/* Gradients of the forward call, from its inputs and the gradients dq_out and
+ * dk_out of its outputs: dq, dk, and dq_weight and dk_weight (fp32, head_dim
+ * elements, overwritten; zero without tokens), of which either may be NULL.
+ * workspace (256-byte aligned) may be NULL when both are. */
+int muon_qk_norm_backward(const muon_qk_norm_desc* desc, const muon_rotation* rotation, const int32_t* cu_seqlens,
+                          const void* positions, const muon_heads* dq_out, const muon_heads* dk_out,
+                          const muon_heads* q, const muon_heads* k, const void* q_weight, const void* k_weight,
+                          const muon_heads* dq, const muon_heads* dk, float* dq_weight, float* dk_weight,
+                          uint32_t flags, void* workspace, size_t ws_bytes, void* hip_stream);
+
+/* Embedding: a table of `vocab` rows (below 2^30) of `cols` elements (at most
+ * 2^20), and `tokens` ids (at most 2^30; id_dtype).  Leading dimensions are in
+ * elements (0 is read as cols); no alignment beyond an element's is needed.
+ * An id outside [0, vocab), such as the padding of a batch, has a row of zeros
+ * and passes no gradient on. */
+typedef struct muon_embedding_desc {
+  int64_t tokens;
+  int64_t vocab;
+  int64_t cols;
+  int64_t ld_table; /* of table and dtable */
+  int64_t ld_out;   /* of out and dout */
+  int32_t table_dtype;
+  int32_t out_dtype;
+  int32_t id_dtype; /* MUON_INDEX_* */
+  float scale;      /* finite */
+  int32_t reserved; /* must be 0 */
+} muon_embedding_desc;
+
+/* out[t] = scale * table[ids[t]], in fp32, rounded once.  tokens == 0 does nothing. */
+int muon_embedding_forward(const muon_embedding_desc* desc, const void* ids, const void* table, void* out,
+                           void* hip_stream);
+
+/* Bytes of device workspace muon_embedding_backward needs; 0 on invalid
+ * arguments.  Host-only. */
+size_t muon_embedding_workspace_size(const muon_embedding_desc* desc);
+
+#define MUON_EMBEDDING_ACCUMULATE 1 /* add to dtable instead of overwriting it */
+
+/* Gradient of the forward call: dtable[v] = scale * sum of dout[t] over the
+ * tokens with ids[t] == v, summed in fp32 and rounded once (dtable:
+ * table_dtype, dout: out_dtype).  Rows of no token are set to zero, or with
+ * MUON_EMBEDDING_ACCUMULATE neither read nor written. */
+int muon_embedding_backward(const muon_embedding_desc* desc, const void* ids, const void* dout, void* dtable,
                             uint32_t flags, void* workspace, size_t ws_bytes, void* hip_stream);
 
 #ifdef __cplusplus

@@ -28,10 +28,16 @@ EXPORTS = ("muon_version", "muon_workspace_size", "muon_init", "muon_step", "muo
            "muon_last_error", "muon_describe", "muon_profile_enable", "muon_profile_select", "muon_profile_read",
            "muon_step_scratch", "muon_check", "muon_fused_limits",
            "muon_layernorm_forward", "muon_layernorm_workspace_size", "muon_layernorm_backward",
-           "muon_attention_forward", "muon_attention_workspace_size", "muon_attention_backward")
+           "muon_attention_forward", "muon_attention_workspace_size", "muon_attention_backward",
+           "muon_qk_norm_forward", "muon_qk_norm_workspace_size", "muon_qk_norm_backward",
+           "muon_embedding_forward", "muon_embedding_workspace_size", "muon_embedding_backward")
 
 ATTENTION_ZERO_OUT, ATTENTION_ZERO_LSE = 1, 2
 ATTENTION_ZERO_DQ, ATTENTION_ZERO_DK, ATTENTION_ZERO_DV = 1, 2, 4
+MUON_INDEX_I32, MUON_INDEX_I64 = 0, 1
+PAIRS_HALVES, PAIRS_NEIGHBOURS = 0, 1
+QK_ZERO_Q, QK_ZERO_K = 1, 2
+EMBEDDING_ACCUMULATE = 1
 
 
 class MatrixDesc(ctypes.Structure):
@@ -68,6 +74,24 @@ class AttentionDesc(ctypes.Structure):
 
 class Heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class QkNormDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("seqs", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("p_dtype", ctypes.c_int32), ("position_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class RotationDesc(ctypes.Structure):
+    _fields_ = [("frequencies", ctypes.POINTER(ctypes.c_double)), ("dim", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+
+class EmbeddingDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld_table", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("table_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 class MuonError(RuntimeError):
@@ -138,6 +162,20 @@ def load() -> ctypes.CDLL:
     lib.muon_attention_backward.restype = ctypes.c_int
     lib.muon_attention_backward.argtypes = ([P(AttentionDesc), vp] + [hp] * 5 + [vp] + [hp] * 3 +
                                             [ctypes.c_uint32, vp, ctypes.c_size_t, vp])
+    rp = P(RotationDesc)
+    lib.muon_qk_norm_forward.restype = ctypes.c_int
+    lib.muon_qk_norm_forward.argtypes = [P(QkNormDesc), rp, vp, vp, hp, hp, vp, vp, hp, hp, ctypes.c_uint32, vp]
+    lib.muon_qk_norm_workspace_size.restype = ctypes.c_size_t
+    lib.muon_qk_norm_workspace_size.argtypes = [P(QkNormDesc)]
+    lib.muon_qk_norm_backward.restype = ctypes.c_int
+    lib.muon_qk_norm_backward.argtypes = ([P(QkNormDesc), rp, vp, vp, hp, hp, hp, hp, vp, vp, hp, hp, vp, vp,
+                                           ctypes.c_uint32, vp, ctypes.c_size_t, vp])
+    lib.muon_embedding_forward.restype = ctypes.c_int
+    lib.muon_embedding_forward.argtypes = [P(EmbeddingDesc)] + [vp] * 4
+    lib.muon_embedding_workspace_size.restype = ctypes.c_size_t
+    lib.muon_embedding_workspace_size.argtypes = [P(EmbeddingDesc)]
+    lib.muon_embedding_backward.restype = ctypes.c_int
+    lib.muon_embedding_backward.argtypes = [P(EmbeddingDesc), vp, vp, vp, ctypes.c_uint32, vp, ctypes.c_size_t, vp]
     _lib = lib
     return lib
 

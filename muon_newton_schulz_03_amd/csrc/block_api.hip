@@ -1,5 +1,6 @@
 // Host side of the transformer block's operators: argument checks, workspace
-// layout and launches of layer norm and packed causal attention.  See
+// layout and launches of the embedding, layer norm, query/key norm with
+// rotation and packed causal attention.  See
 // include/muon.h for the contract of every entry point.
 #include <hip/hip_runtime.h>
 
@@ -22,7 +23,8 @@ constexpr int64_t kMaxTokens = 0x7FFFFF00;
 constexpr int64_t kMaxThreads = 0xFFFFFFFF;  // of one launch
 constexpr int kMaxSeqs = 1 << 24;
 constexpr int kMaxHeads = 1 << 16;
-constexpr int kMaxDim = 128;
+constexpr int64_t kMaxIds = 1 << 30;
+constexpr double kMaxFrequency = 64.;  // radians a position
 constexpr float kMinScale = 0x1p-60f;  // lse / scale stays finite
 constexpr size_t kAlign = 256;
 
@@ -149,29 +151,39 @@ int check_attention(const muon_attention_desc* d) {
   return MUON_OK;
 }
 
-int check_heads(const muon_attention_desc* d, const muon_heads* v, const char* name, int heads, bool written,
-                HeadView* out) {
-  if (!v || !v->data) return fail(MUON_E_INVAL, "attention: %s is NULL", name);
-  const int es = elem_size(d->dtype);
+// One (tokens, heads, head_dim) operand of the operator `what`.
+struct HeadShape {
+  const char* what;
+  int64_t tokens;
+  int dim, dtype;
+};
+int check_heads(const HeadShape& d, const muon_heads* v, const char* name, int heads, bool written, HeadView* out) {
+  if (!v || !v->data) return fail(MUON_E_INVAL, "%s: %s is NULL", d.what, name);
+  const int es = elem_size(d.dtype);
   // a stride that no address uses does not matter
-  const int64_t token = d->tokens > 1 ? v->token_stride : 0, head = heads > 1 ? v->head_stride : 0;
+  const int64_t token = d.tokens > 1 ? v->token_stride : 0, head = heads > 1 ? v->head_stride : 0;
   if (token < 0 || head < 0 || token > kMaxTokenStride || head > kMaxStride)
-    return fail(MUON_E_INVAL, "attention: %s: strides %lld, %lld outside [0, 2^24] and [0, 2^31]", name,
+    return fail(MUON_E_INVAL, "%s: %s: strides %lld, %lld outside [0, 2^24] and [0, 2^31]", d.what, name,
                 (long long)token, (long long)head);
   if (misaligned(v->data, 16) || token * es % 16 || head * es % 16)
-    return fail(MUON_E_UNSUPPORTED, "attention: %s must start, and step from token to token and head to head, at "
-                "multiples of 16 bytes", name);
+    return fail(MUON_E_UNSUPPORTED, "%s: %s must start, and step from token to token and head to head, at "
+                "multiples of 16 bytes", d.what, name);
   if (written) {
-    const int64_t dim = d->head_dim;
-    const bool by_token = (d->tokens <= 1 || token >= (heads - 1) * head + dim) && (heads <= 1 || head >= dim);
-    const bool by_head = (heads <= 1 || head >= (d->tokens - 1) * token + dim) && (d->tokens <= 1 || token >= dim);
+    const int64_t dim = d.dim;
+    const bool by_token = (d.tokens <= 1 || token >= (heads - 1) * head + dim) && (heads <= 1 || head >= dim);
+    const bool by_head = (heads <= 1 || head >= (d.tokens - 1) * token + dim) && (d.tokens <= 1 || token >= dim);
     if (!by_token && !by_head)
-      return fail(MUON_E_INVAL, "attention: rows of the output %s overlap (strides %lld, %lld)", name, (long long)token,
-                  (long long)head);
+      return fail(MUON_E_INVAL, "%s: rows of the output %s overlap (strides %lld, %lld)", d.what, name,
+                  (long long)token, (long long)head);
   }
   *out = HeadView{v->data, token, head};
   return MUON_OK;
 }
+Area heads_area(const HeadShape& d, const HeadView& v, int heads) {
+  const int es = elem_size(d.dtype);
+  return area(v.data, d.tokens, v.token * es, heads, v.head * es, d.dim * es);
+}
+HeadShape shape_of(const muon_attention_desc* d) { return HeadShape{"attention", d->tokens, d->head_dim, d->dtype}; }
 
 size_t attention_part_bytes(const muon_attention_desc* d, int splits) {
   return splits > 1 ? (size_t)splits * d->tokens * d->kv_heads * 2 * d->head_dim * sizeof(float) : 0;
@@ -186,11 +198,6 @@ size_t attention_row_bytes(const muon_attention_desc* d) {  // one fp32 per quer
 size_t attention_workspace(const muon_attention_desc* d) {
   return 2 * attention_row_bytes(d) + align_up(attention_part_bytes(d, splits_of(d))) +
          kAlign;  // never 0, which means an error
-}
-
-Area heads_area(const muon_attention_desc* d, const HeadView& v, int heads) {
-  const int es = elem_size(d->dtype);
-  return area(v.data, d->tokens, v.token * es, heads, v.head * es, d->head_dim * es);
 }
 
 AttnArgs common_args(const muon_attention_desc* d, const int32_t* cu, uint32_t flags) {
@@ -208,9 +215,290 @@ AttnArgs common_args(const muon_attention_desc* d, const int32_t* cu, uint32_t f
   return a;
 }
 
+// ---------------------------------------------------- query and key norms --
+int check_qk(const muon_qk_norm_desc* d, const muon_rotation* r) {
+  if (!d) return fail(MUON_E_INVAL, "query/key norm descriptor is NULL");
+  if (d->tokens < 0 || d->tokens > kMaxTokens)
+    return fail(MUON_E_INVAL, "query/key norm: tokens=%lld outside [0, %lld]", (long long)d->tokens,
+                (long long)kMaxTokens);
+  if (d->seqs < 0 || d->seqs > kMaxSeqs)
+    return fail(MUON_E_INVAL, "query/key norm: seqs=%d outside [0, %d]", d->seqs, kMaxSeqs);
+  if (d->q_heads <= 0 || d->k_heads <= 0 || d->q_heads > kMaxHeads || d->k_heads > kMaxHeads)
+    return fail(MUON_E_INVAL, "query/key norm: q_heads=%d or k_heads=%d outside [1, %d]", d->q_heads, d->k_heads,
+                kMaxHeads);
+  if (d->head_dim <= 0 || d->head_dim > kMaxDim || d->head_dim % 8)
+    return fail(MUON_E_UNSUPPORTED, "query/key norm: head_dim=%d must be a multiple of 8, at most %d", d->head_dim,
+                kMaxDim);
+  if (d->dtype != MUON_DTYPE_F32 && d->dtype != MUON_DTYPE_BF16)
+    return fail(MUON_E_UNSUPPORTED, "query/key norm: dtype %d unsupported", d->dtype);
+  if (d->p_dtype != MUON_DTYPE_F32 && d->p_dtype != MUON_DTYPE_BF16)
+    return fail(MUON_E_UNSUPPORTED, "query/key norm: p_dtype %d unsupported", d->p_dtype);
+  if (d->position_dtype != MUON_INDEX_I32 && d->position_dtype != MUON_INDEX_I64)
+    return fail(MUON_E_UNSUPPORTED, "query/key norm: position_dtype %d unsupported", d->position_dtype);
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps))
+    return fail(MUON_E_INVAL, "query/key norm: eps must be finite and not negative");
+  if (d->reserved != 0) return fail(MUON_E_INVAL, "query/key norm: reserved field must be 0");
+  if (!r) return MUON_OK;
+  if (r->dim < 0 || r->dim > d->head_dim || r->dim % 8)
+    return fail(MUON_E_UNSUPPORTED, "query/key norm: a rotation of %d elements must be a multiple of 8, at most "
+                "head_dim=%d", r->dim, d->head_dim);
+  if (r->pairs != MUON_PAIRS_HALVES && r->pairs != MUON_PAIRS_NEIGHBOURS)
+    return fail(MUON_E_INVAL, "query/key norm: pairs %d unknown", r->pairs);
+  if (r->dim > 0 && !r->frequencies) return fail(MUON_E_INVAL, "query/key norm: frequencies is NULL");
+  for (int i = 0; i < r->dim / 2; ++i)
+    if (!(std::fabs(r->frequencies[i]) <= kMaxFrequency))
+      return fail(MUON_E_INVAL, "query/key norm: frequency %g of pair %d outside [-%g, %g]", r->frequencies[i], i,
+                  kMaxFrequency, kMaxFrequency);
+  return MUON_OK;
+}
+
+// A frequency in radians as the fraction of a turn, in units of 2^-64 (modulo
+// whole turns, which no position sees).
+uint64_t turn_of(double frequency) {
+  const long double turns = (long double)frequency / 6.283185307179586476925286766559L;
+  const long double part = std::floor((turns - std::floor(turns)) * 0x1p64L + 0.5L);
+  return part >= 0x1p64L ? 0 : (uint64_t)part;
+}
+
+size_t qk_workspace(const muon_qk_norm_desc* d) { return align_up((size_t)2 * kQkBlocks * d->head_dim * sizeof(float)); }
+
+// What both calls share: the views, the rotation and the split over blocks.
+int qk_args(const muon_qk_norm_desc* d, const muon_rotation* r, const int32_t* cu, const void* positions,
+            uint32_t flags, const muon_heads* q, const muon_heads* k, const muon_heads* oq, const muon_heads* ok,
+            const char* nq, const char* nk, const void* q_weight, const void* k_weight, QkArgs* a) {
+  if (flags & ~(uint32_t)(MUON_QK_ZERO_Q | MUON_QK_ZERO_K))
+    return fail(MUON_E_INVAL, "query/key norm: unknown flags 0x%x", flags);
+  if (misaligned(cu, 4)) return fail(MUON_E_INVAL, "query/key norm: cu_seqlens is misaligned");
+  if (misaligned(positions, d->position_dtype == MUON_INDEX_I64 ? 8 : 4))
+    return fail(MUON_E_INVAL, "query/key norm: positions are misaligned");
+  const int ps = elem_size(d->p_dtype);
+  if (misaligned(q_weight, ps) || misaligned(k_weight, ps))
+    return fail(MUON_E_INVAL, "query/key norm: a weight is not aligned to its element size");
+  const HeadShape shape{"query/key norm", d->tokens, d->head_dim, d->dtype};
+  int rc = check_heads(shape, q, "q", d->q_heads, false, &a->side[0].x);
+  if (!rc) rc = check_heads(shape, k, "k", d->k_heads, false, &a->side[1].x);
+  if (!rc) rc = check_heads(shape, oq, nq, d->q_heads, true, &a->side[0].out);
+  if (!rc) rc = check_heads(shape, ok, nk, d->k_heads, true, &a->side[1].out);
+  if (rc) return rc;
+  a->side[0].weight = q_weight, a->side[1].weight = k_weight;
+  a->side[0].heads = d->q_heads, a->side[1].heads = d->k_heads;
+  a->side[0].zero_tail = (flags & MUON_QK_ZERO_Q) != 0, a->side[1].zero_tail = (flags & MUON_QK_ZERO_K) != 0;
+  a->cu = cu, a->positions = positions;
+  a->tokens = d->tokens, a->seqs = d->seqs, a->dim = d->head_dim;
+  a->rotated = r ? r->dim : 0;
+  a->p_bf16 = d->p_dtype == MUON_DTYPE_BF16, a->pos64 = d->position_dtype == MUON_INDEX_I64;
+  a->eps = d->eps;
+  for (int i = 0; i < a->rotated / 2; ++i) a->turns[i] = turn_of(r->frequencies[i]);
+  return MUON_OK;
+}
+
+// -------------------------------------------------------------- embedding --
+int check_embedding(const muon_embedding_desc* d) {
+  if (!d) return fail(MUON_E_INVAL, "embedding descriptor is NULL");
+  if (d->tokens < 0 || d->tokens > kMaxIds)
+    return fail(MUON_E_INVAL, "embedding: tokens=%lld outside [0, 2^30]", (long long)d->tokens);
+  if (d->vocab <= 0 || d->vocab >= kMaxIds)
+    return fail(MUON_E_INVAL, "embedding: vocab=%lld outside [1, 2^30)", (long long)d->vocab);
+  if (d->cols <= 0 || d->cols > kMaxCols)
+    return fail(MUON_E_INVAL, "embedding: cols=%lld outside [1, 2^20]", (long long)d->cols);
+  const int64_t lds[] = {d->ld_table, d->ld_out};
+  const char* names[] = {"ld_table", "ld_out"};
+  for (int i = 0; i < 2; ++i)
+    if (lds[i] != 0 && (lds[i] < d->cols || lds[i] > kMaxStride))
+      return fail(MUON_E_INVAL, "embedding: %s=%lld is below cols=%lld or above 2^31", names[i], (long long)lds[i],
+                  (long long)d->cols);
+  if (d->table_dtype != MUON_DTYPE_F32 && d->table_dtype != MUON_DTYPE_BF16)
+    return fail(MUON_E_UNSUPPORTED, "embedding: table_dtype %d unsupported", d->table_dtype);
+  if (d->out_dtype != MUON_DTYPE_F32 && d->out_dtype != MUON_DTYPE_BF16)
+    return fail(MUON_E_UNSUPPORTED, "embedding: out_dtype %d unsupported", d->out_dtype);
+  if (d->id_dtype != MUON_INDEX_I32 && d->id_dtype != MUON_INDEX_I64)
+    return fail(MUON_E_UNSUPPORTED, "embedding: id_dtype %d unsupported", d->id_dtype);
+  if (!std::isfinite(d->scale)) return fail(MUON_E_INVAL, "embedding: scale must be finite");
+  if (d->reserved != 0) return fail(MUON_E_INVAL, "embedding: reserved field must be 0");
+  return MUON_OK;
+}
+int id_size(const muon_embedding_desc* d) { return d->id_dtype == MUON_INDEX_I64 ? 8 : 4; }
+Area table_area(const muon_embedding_desc* d, const void* p) {
+  const int es = elem_size(d->table_dtype);
+  return area(p, d->vocab, ld_of(d->ld_table, d->cols) * es, 1, 0, d->cols * es);
+}
+Area out_area(const muon_embedding_desc* d, const void* p) {
+  const int es = elem_size(d->out_dtype);
+  return area(p, d->tokens, ld_of(d->ld_out, d->cols) * es, 1, 0, d->cols * es);
+}
+
+// The backward call's workspace: sorted entries twice, digit counts, a byte for
+// each row of the table, and two partial rows for each chunk.
+EmbedGradArgs embed_layout(const muon_embedding_desc* d, void* workspace, size_t* bytes) {
+  EmbedGradArgs a{};
+  a.tokens = d->tokens, a.vocab = d->vocab, a.cols = (int32_t)d->cols;
+  plan_embed(a);
+  char* p = (char*)workspace;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    char* q = p ? p + at : nullptr;
+    at += align_up(n);
+    return q;
+  };
+  for (EmbedEntry*& e : a.entry) e = (EmbedEntry*)take((size_t)d->tokens * sizeof(EmbedEntry));
+  a.hist = (uint32_t*)take(((size_t)a.blocks << a.digit) * sizeof(uint32_t));
+  a.present = (uint8_t*)take((size_t)d->vocab);
+  const size_t chunks = ((size_t)d->tokens + kEmbedChunk - 1) / kEmbedChunk;
+  a.part = (float*)take(chunks * 2 * (size_t)d->cols * sizeof(float));
+  *bytes = at;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
+
+int muon_embedding_forward(const muon_embedding_desc* d, const void* ids, const void* table, void* out,
+                           void* hip_stream) {
+  clear_error();
+  if (int rc = check_embedding(d)) return rc;
+  if (d->tokens == 0) return MUON_OK;
+  if (!ids || !table || !out) return fail(MUON_E_INVAL, "embedding: ids, table or out is NULL");
+  if (misaligned(ids, id_size(d)) || misaligned(table, elem_size(d->table_dtype)) ||
+      misaligned(out, elem_size(d->out_dtype)))
+    return fail(MUON_E_INVAL, "embedding: pointer not aligned to its element size");
+  const Operand ops[] = {{"out", out_area(d, out)}, {"table", table_area(d, table)},
+                         {"ids", flat(ids, (size_t)d->tokens * id_size(d))}};
+  if (int rc = check_apart("embedding", ops, 1, 3)) return rc;
+  EmbedArgs a{};
+  a.ids = ids, a.table = table, a.out = out;
+  a.tokens = d->tokens, a.vocab = d->vocab, a.cols = (int32_t)d->cols;
+  a.ld_table = ld_of(d->ld_table, d->cols), a.ld_out = ld_of(d->ld_out, d->cols);
+  a.id64 = d->id_dtype == MUON_INDEX_I64, a.scale = d->scale;
+  const hipError_t e = launch_embed_forward(a, d->table_dtype == MUON_DTYPE_BF16, d->out_dtype == MUON_DTYPE_BF16,
+                                            (hipStream_t)hip_stream);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "embedding forward launch");
+}
+
+size_t muon_embedding_workspace_size(const muon_embedding_desc* d) {
+  clear_error();
+  if (check_embedding(d)) return 0;
+  size_t bytes;
+  embed_layout(d, nullptr, &bytes);
+  return bytes + kAlign;
+}
+
+int muon_embedding_backward(const muon_embedding_desc* d, const void* ids, const void* dout, void* dtable,
+                            uint32_t flags, void* workspace, size_t ws_bytes, void* hip_stream) {
+  clear_error();
+  if (int rc = check_embedding(d)) return rc;
+  if (flags & ~(uint32_t)MUON_EMBEDDING_ACCUMULATE) return fail(MUON_E_INVAL, "embedding: unknown flags 0x%x", flags);
+  if (d->tokens == 0 && flags) return MUON_OK;
+  if (!dtable || (d->tokens > 0 && (!ids || !dout)))
+    return fail(MUON_E_INVAL, "embedding: ids, dout or dtable is NULL");
+  if (misaligned(ids, id_size(d)) || misaligned(dtable, elem_size(d->table_dtype)) ||
+      misaligned(dout, elem_size(d->out_dtype)))
+    return fail(MUON_E_INVAL, "embedding: pointer not aligned to its element size");
+  if (!workspace) return fail(MUON_E_WORKSPACE, "embedding: workspace is NULL");
+  if (misaligned(workspace, kAlign)) return fail(MUON_E_WORKSPACE, "embedding: workspace is not 256-byte aligned");
+  size_t need;
+  EmbedGradArgs a = embed_layout(d, workspace, &need);
+  if (ws_bytes < need)
+    return fail(MUON_E_WORKSPACE, "embedding: workspace has %zu bytes, the call needs %zu", ws_bytes, need);
+  const Operand ops[] = {{"dtable", table_area(d, dtable)},
+                         {"workspace", flat(workspace, need)},
+                         {"dout", out_area(d, dout)},
+                         {"ids", flat(ids, (size_t)d->tokens * id_size(d))}};
+  if (int rc = check_apart("embedding", ops, 2, 4)) return rc;
+  a.ids = ids, a.dout = dout, a.dtable = dtable;
+  a.ld_dout = ld_of(d->ld_out, d->cols), a.ld_dtable = ld_of(d->ld_table, d->cols);
+  a.id64 = d->id_dtype == MUON_INDEX_I64, a.scale = d->scale;
+  a.accumulate = (flags & MUON_EMBEDDING_ACCUMULATE) != 0;
+  const hipError_t e = launch_embed_backward(a, d->table_dtype == MUON_DTYPE_BF16, d->out_dtype == MUON_DTYPE_BF16,
+                                             (hipStream_t)hip_stream);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "embedding backward launch");
+}
+
+int muon_qk_norm_forward(const muon_qk_norm_desc* d, const muon_rotation* rotation, const int32_t* cu_seqlens,
+                         const void* positions, const muon_heads* q, const muon_heads* k, const void* q_weight,
+                         const void* k_weight, const muon_heads* q_out, const muon_heads* k_out, uint32_t flags,
+                         void* hip_stream) {
+  clear_error();
+  if (int rc = check_qk(d, rotation)) return rc;
+  if (d->tokens == 0) return MUON_OK;
+  QkArgs a{};
+  if (int rc = qk_args(d, rotation, cu_seqlens, positions, flags, q, k, q_out, k_out, "q_out", "k_out", q_weight,
+                       k_weight, &a))
+    return rc;
+  const HeadShape shape{"query/key norm", d->tokens, d->head_dim, d->dtype};
+  const size_t params = (size_t)d->head_dim * elem_size(d->p_dtype);
+  const Operand ops[] = {{"q_out", heads_area(shape, a.side[0].out, d->q_heads)},
+                         {"k_out", heads_area(shape, a.side[1].out, d->k_heads)},
+                         {"q", heads_area(shape, a.side[0].x, d->q_heads)},
+                         {"k", heads_area(shape, a.side[1].x, d->k_heads)},
+                         {"q_weight", flat(q_weight, params)},
+                         {"k_weight", flat(k_weight, params)},
+                         {"cu_seqlens", flat(cu_seqlens, ((size_t)d->seqs + 1) * 4)},
+                         {"positions", flat(positions, (size_t)d->tokens * (a.pos64 ? 8 : 4))}};
+  if (int rc = check_apart("query/key norm", ops, 2, 8)) return rc;
+  const bool bf16 = d->dtype == MUON_DTYPE_BF16;
+  plan_qk(a, bf16, false);
+  const hipError_t e = launch_qk(a, bf16, rotation ? rotation->pairs : 0, false, (hipStream_t)hip_stream);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "query/key norm forward launch");
+}
+
+size_t muon_qk_norm_workspace_size(const muon_qk_norm_desc* d) {
+  clear_error();
+  if (check_qk(d, nullptr)) return 0;
+  return qk_workspace(d) + kAlign;
+}
+
+int muon_qk_norm_backward(const muon_qk_norm_desc* d, const muon_rotation* rotation, const int32_t* cu_seqlens,
+                          const void* positions, const muon_heads* dq_out, const muon_heads* dk_out,
+                          const muon_heads* q, const muon_heads* k, const void* q_weight, const void* k_weight,
+                          const muon_heads* dq, const muon_heads* dk, float* dq_weight, float* dk_weight,
+                          uint32_t flags, void* workspace, size_t ws_bytes, void* hip_stream) {
+  clear_error();
+  if (int rc = check_qk(d, rotation)) return rc;
+  const bool sums = dq_weight || dk_weight;
+  if (misaligned(dq_weight, 4) || misaligned(dk_weight, 4))
+    return fail(MUON_E_INVAL, "query/key norm: a weight gradient is not aligned to its element size");
+  if (sums) {
+    if (!workspace) return fail(MUON_E_WORKSPACE, "query/key norm: workspace is NULL");
+    if (misaligned(workspace, kAlign))
+      return fail(MUON_E_WORKSPACE, "query/key norm: workspace is not 256-byte aligned");
+    if (ws_bytes < qk_workspace(d))
+      return fail(MUON_E_WORKSPACE, "query/key norm: workspace has %zu bytes, the call needs %zu", ws_bytes,
+                  qk_workspace(d));
+  }
+  const HeadShape shape{"query/key norm", d->tokens, d->head_dim, d->dtype};
+  const size_t params = (size_t)d->head_dim * elem_size(d->p_dtype), grads = (size_t)d->head_dim * 4;
+  QkArgs a{};
+  if (d->tokens > 0) {
+    int rc = qk_args(d, rotation, cu_seqlens, positions, flags, q, k, dq, dk, "dq", "dk", q_weight, k_weight, &a);
+    if (!rc) rc = check_heads(shape, dq_out, "dq_out", d->q_heads, false, &a.side[0].dy);
+    if (!rc) rc = check_heads(shape, dk_out, "dk_out", d->k_heads, false, &a.side[1].dy);
+    if (rc) return rc;
+  }
+  const Operand ops[] = {{"dq", heads_area(shape, a.side[0].out, d->q_heads)},
+                         {"dk", heads_area(shape, a.side[1].out, d->k_heads)},
+                         {"dq_weight", flat(dq_weight, grads)},
+                         {"dk_weight", flat(dk_weight, grads)},
+                         {"workspace", flat(sums ? workspace : nullptr, qk_workspace(d))},
+                         {"dq_out", heads_area(shape, a.side[0].dy, d->q_heads)},
+                         {"dk_out", heads_area(shape, a.side[1].dy, d->k_heads)},
+                         {"q", heads_area(shape, a.side[0].x, d->q_heads)},
+                         {"k", heads_area(shape, a.side[1].x, d->k_heads)},
+                         {"q_weight", flat(q_weight, params)},
+                         {"k_weight", flat(k_weight, params)},
+                         {"cu_seqlens", flat(cu_seqlens, ((size_t)d->seqs + 1) * 4)},
+                         {"positions", flat(positions, (size_t)d->tokens * (a.pos64 ? 8 : 4))}};
+  if (int rc = check_apart("query/key norm", ops, 5, 13)) return rc;
+  a.part = sums ? (float*)workspace : nullptr;
+  const bool bf16 = d->dtype == MUON_DTYPE_BF16;
+  plan_qk(a, bf16, true);
+  hipError_t e = hipSuccess;
+  if (d->tokens > 0) e = launch_qk(a, bf16, rotation ? rotation->pairs : 0, true, (hipStream_t)hip_stream);
+  if (e == hipSuccess && sums)
+    e = launch_qk_sum(QkSumArgs{a.part, {dq_weight, dk_weight}, {a.side[0].blocks, a.side[1].blocks}, d->head_dim},
+                      (hipStream_t)hip_stream);
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "query/key norm backward launch");
+}
 
 int muon_layernorm_forward(const muon_layernorm_desc* d, const void* x, const void* weight, const void* bias, void* y,
                            float* mean, float* rstd, void* hip_stream) {
@@ -299,15 +587,16 @@ int muon_attention_forward(const muon_attention_desc* d, const int32_t* cu_seqle
   if (d->tokens == 0) return MUON_OK;
   if (!cu_seqlens || misaligned(cu_seqlens, 4)) return fail(MUON_E_INVAL, "attention: cu_seqlens is NULL or misaligned");
   if (!lse || misaligned(lse, 4)) return fail(MUON_E_INVAL, "attention: lse is NULL or misaligned");
+  const HeadShape shape = shape_of(d);
   AttnArgs a = common_args(d, cu_seqlens, flags);
-  int rc = check_heads(d, q, "q", d->q_heads, false, &a.q);
-  if (!rc) rc = check_heads(d, k, "k", d->kv_heads, false, &a.k);
-  if (!rc) rc = check_heads(d, v, "v", d->kv_heads, false, &a.v);
-  if (!rc) rc = check_heads(d, out, "out", d->q_heads, true, &a.o);
+  int rc = check_heads(shape, q, "q", d->q_heads, false, &a.q);
+  if (!rc) rc = check_heads(shape, k, "k", d->kv_heads, false, &a.k);
+  if (!rc) rc = check_heads(shape, v, "v", d->kv_heads, false, &a.v);
+  if (!rc) rc = check_heads(shape, out, "out", d->q_heads, true, &a.o);
   if (rc) return rc;
-  const Operand ops[] = {{"out", heads_area(d, a.o, d->q_heads)}, {"lse", flat(lse, lse_bytes(d))},
-                         {"q", heads_area(d, a.q, d->q_heads)},   {"k", heads_area(d, a.k, d->kv_heads)},
-                         {"v", heads_area(d, a.v, d->kv_heads)},
+  const Operand ops[] = {{"out", heads_area(shape, a.o, d->q_heads)}, {"lse", flat(lse, lse_bytes(d))},
+                         {"q", heads_area(shape, a.q, d->q_heads)},   {"k", heads_area(shape, a.k, d->kv_heads)},
+                         {"v", heads_area(shape, a.v, d->kv_heads)},
                          {"cu_seqlens", flat(cu_seqlens, ((size_t)d->seqs + 1) * 4)}};
   if ((rc = check_apart("attention", ops, 2, 6))) return rc;
   a.lse = lse;
@@ -332,27 +621,28 @@ int muon_attention_backward(const muon_attention_desc* d, const int32_t* cu_seql
   if (d->tokens == 0) return MUON_OK;
   if (!cu_seqlens || misaligned(cu_seqlens, 4)) return fail(MUON_E_INVAL, "attention: cu_seqlens is NULL or misaligned");
   if (!lse || misaligned(lse, 4)) return fail(MUON_E_INVAL, "attention: lse is NULL or misaligned");
+  const HeadShape shape = shape_of(d);
   AttnArgs a = common_args(d, cu_seqlens, flags);
-  int rc = check_heads(d, dout, "dout", d->q_heads, false, &a.dout);
-  if (!rc) rc = check_heads(d, q, "q", d->q_heads, false, &a.q);
-  if (!rc) rc = check_heads(d, k, "k", d->kv_heads, false, &a.k);
-  if (!rc) rc = check_heads(d, v, "v", d->kv_heads, false, &a.v);
-  if (!rc) rc = check_heads(d, out, "out", d->q_heads, false, &a.o);
-  if (!rc) rc = check_heads(d, dq, "dq", d->q_heads, true, &a.dq);
-  if (!rc) rc = check_heads(d, dk, "dk", d->kv_heads, true, &a.dk);
-  if (!rc) rc = check_heads(d, dv, "dv", d->kv_heads, true, &a.dv);
+  int rc = check_heads(shape, dout, "dout", d->q_heads, false, &a.dout);
+  if (!rc) rc = check_heads(shape, q, "q", d->q_heads, false, &a.q);
+  if (!rc) rc = check_heads(shape, k, "k", d->kv_heads, false, &a.k);
+  if (!rc) rc = check_heads(shape, v, "v", d->kv_heads, false, &a.v);
+  if (!rc) rc = check_heads(shape, out, "out", d->q_heads, false, &a.o);
+  if (!rc) rc = check_heads(shape, dq, "dq", d->q_heads, true, &a.dq);
+  if (!rc) rc = check_heads(shape, dk, "dk", d->kv_heads, true, &a.dk);
+  if (!rc) rc = check_heads(shape, dv, "dv", d->kv_heads, true, &a.dv);
   if (rc) return rc;
   if (!workspace) return fail(MUON_E_WORKSPACE, "attention: workspace is NULL");
   if (misaligned(workspace, kAlign)) return fail(MUON_E_WORKSPACE, "attention: workspace is not 256-byte aligned");
   if (ws_bytes < attention_workspace(d))
     return fail(MUON_E_WORKSPACE, "attention: workspace has %zu bytes, the call needs %zu", ws_bytes,
                 attention_workspace(d));
-  const Operand ops[] = {{"dq", heads_area(d, a.dq, d->q_heads)},    {"dk", heads_area(d, a.dk, d->kv_heads)},
-                         {"dv", heads_area(d, a.dv, d->kv_heads)},
+  const Operand ops[] = {{"dq", heads_area(shape, a.dq, d->q_heads)},    {"dk", heads_area(shape, a.dk, d->kv_heads)},
+                         {"dv", heads_area(shape, a.dv, d->kv_heads)},
                          {"workspace", flat(workspace, attention_workspace(d))},
-                         {"dout", heads_area(d, a.dout, d->q_heads)}, {"q", heads_area(d, a.q, d->q_heads)},
-                         {"k", heads_area(d, a.k, d->kv_heads)},     {"v", heads_area(d, a.v, d->kv_heads)},
-                         {"out", heads_area(d, a.o, d->q_heads)},    {"lse", flat(lse, lse_bytes(d))},
+                         {"dout", heads_area(shape, a.dout, d->q_heads)}, {"q", heads_area(shape, a.q, d->q_heads)},
+                         {"k", heads_area(shape, a.k, d->kv_heads)},     {"v", heads_area(shape, a.v, d->kv_heads)},
+                         {"out", heads_area(shape, a.o, d->q_heads)},    {"lse", flat(lse, lse_bytes(d))},
                          {"cu_seqlens", flat(cu_seqlens, ((size_t)d->seqs + 1) * 4)}};
   if ((rc = check_apart("attention", ops, 4, 11))) return rc;
   a.lse = const_cast<float*>(lse);

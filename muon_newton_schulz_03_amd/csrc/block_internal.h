@@ -1,5 +1,6 @@
-// Launch arguments of the transformer block's operators (layer norm, packed
-// causal attention), shared by their host entry points and kernels.
+// Launch arguments of the transformer block's operators (embedding, layer
+// norm, query/key norm with rotation, packed causal attention), shared by
+// their host entry points and kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -59,6 +60,8 @@ struct HeadView {
   int64_t head;
 };
 
+constexpr int kMaxDim = 128;  // of a head
+
 struct AttnArgs {
   HeadView q, k, v, o;
   HeadView dout, dq, dk, dv;  // backward only
@@ -85,5 +88,89 @@ int64_t attention_threads(int64_t tokens, int seqs, int q_heads, int dim, bool b
 int attention_splits(int64_t tokens, int seqs, int q_heads, int kv_heads);
 hipError_t launch_attention_forward(const AttnArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_attention_backward(const AttnArgs& a, bool bf16, hipStream_t stream);
+
+
+// ---------------------------------------------------- query and key norms --
+// One side, queries or keys.
+struct QkSide {
+  HeadView x, out;     // out: y, or dx
+  HeadView dy;         // backward only
+  const void* weight;  // null: ones
+  int32_t heads;
+  int32_t chunk;       // heads a thread takes in turn
+  int32_t blocks;      // of the launch, which has the queries' blocks first
+  int32_t zero_tail;   // set out's rows behind the last sequence to zero
+};
+
+struct QkArgs {
+  QkSide side[2];
+  const int32_t* cu;       // null: no sequences, every token counts
+  const void* positions;   // null: offset within the sequence (without sequences, the token's number)
+  float* part;             // backward: weight gradients of each block, [blocks][dim]; null: not wanted
+  int64_t tokens;
+  int32_t seqs;
+  int32_t dim;
+  int32_t rotated;         // elements of a head that turn, the first ones
+  int32_t p_bf16;
+  int32_t pos64;
+  float eps;
+  uint64_t turns[kMaxDim / 2];  // a pair's turn per position, as a fraction of 2^64
+};
+
+struct QkSumArgs {
+  const float* part;
+  float* dweight[2];  // either may be null
+  int32_t blocks[2];
+  int32_t dim;
+};
+
+constexpr int kQkBlocks = 1024;  // of a side, at most
+enum { kPairHalves = 0, kPairNeighbours = 1 };
+// Fills in the sides' chunk and blocks.
+void plan_qk(QkArgs& a, bool bf16, bool backward);
+hipError_t launch_qk(const QkArgs& a, bool bf16, int pairs, bool backward, hipStream_t stream);
+hipError_t launch_qk_sum(const QkSumArgs& a, hipStream_t stream);
+
+// -------------------------------------------------------------- embedding --
+struct EmbedArgs {
+  const void* ids;
+  const void* table;
+  void* out;
+  int64_t tokens, vocab, ld_table, ld_out;
+  int32_t cols;
+  int32_t id64;
+  int32_t rows;    // tokens of a block
+  uint32_t magic;  // 2^32 / vectors of a row, rounded up (rows > 1)
+  float scale;
+};
+hipError_t launch_embed_forward(const EmbedArgs& a, bool table_bf16, bool out_bf16, hipStream_t stream);
+
+struct EmbedEntry {
+  uint32_t id;  // vocab: an id outside the table
+  uint32_t token;
+};
+struct EmbedGradArgs {
+  const void* ids;
+  const void* dout;
+  void* dtable;
+  int64_t tokens, vocab, ld_dout, ld_dtable;
+  int32_t cols;
+  int32_t id64;
+  int32_t accumulate;
+  float scale;
+  // workspace
+  EmbedEntry* entry[2];  // tokens each
+  uint32_t* hist;        // [blocks][1 << digit]
+  uint8_t* present;      // vocab
+  float* part;           // [chunks][2][cols]
+  // sort
+  int32_t blocks, segment;  // blocks of a pass, and tokens of each
+  int32_t digit, passes;    // bits of a digit
+  int32_t pass;             // this launch's
+};
+constexpr int kEmbedChunk = 32;   // sorted tokens a wave sums
+constexpr int kMaxDigit = 10;
+void plan_embed(EmbedGradArgs& a);
+hipError_t launch_embed_backward(const EmbedGradArgs& a, bool table_bf16, bool out_bf16, hipStream_t stream);
 
 }  // namespace muon

@@ -1,0 +1,340 @@
+"""The embedding and the query/key norm with rotation on the GPU against their fp64 definitions.
+
+Tolerances are the elementwise bounds of token_reference (derived from the
+roundings of the computation); sizes are those at which vectors, lanes, tiles,
+chunks, sort passes and sequences end badly.
+"""
+import itertools
+
+import pytest
+import torch
+
+import block_reference as B
+import muon_newton_schulz_03_amd as lib
+import token_reference as R
+from muon_harness import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def randn(shape, seed, dtype=F32, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def randint(lo, hi, shape, seed, dtype=torch.int64):
+    return torch.randint(lo, hi, shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+def cu_of(lengths):
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    return torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+
+# ---------------------------------------------------- query and key norms --
+def qk_case(T, H, G, D, dtype, seed, rot=None, pairs="halves", weights=None, lengths=None, positions=None, eps=1e-6,
+            layout="fused", std=1.0, freqs=None):
+    rot = D if rot is None else rot
+    rotation = lib.Rotation(rot, pairs=pairs, frequencies=freqs) if rot else None
+    qkv = (randn((T, H + 2 * G, D), seed, F32, std) * torch.exp(0.5 * randn((T, 1, 1), seed + 1))).to(dtype)
+    do = randn((T, H + G, D), seed + 2, dtype)
+    w = [None, None] if weights is None else [(1 + 0.3 * randn((D,), seed + 3 + i)).to(weights) for i in (0, 1)]
+    dev, ddo = qkv.to(DEV), do.to(DEV)
+    if layout != "fused":  # heads before tokens in memory
+        dev, ddo = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (dev, ddo))
+    used = sum(lengths) if lengths is not None else T
+    dev[used:], ddo[used:] = float("nan"), float("nan")  # behind the last sequence: never read
+    q, k = dev[:, :H], dev[:, H:H + G]
+    how = dict(q_weight=None if w[0] is None else w[0].to(DEV), k_weight=None if w[1] is None else w[1].to(DEV),
+               cu_seqlens=None if lengths is None else cu_of(lengths),
+               positions=None if positions is None else positions.to(DEV), eps=eps)
+    qo, ko = lib.qk_norm_forward(q, k, rotation, **how)
+    dq, dk, dqw, dkw = lib.qk_norm_backward(ddo[:, :H], ddo[:, H:], q, k, rotation, need_q_weight=True,
+                                            need_k_weight=True, **how)
+    torch.cuda.synchronize()
+    pos = R.positions_of(T, lengths, positions)[:used]
+    turns = R.angles(pos, rotation.frequencies if rotation else [])
+    worst = 0.0
+    for name, lo, hi, y, dx, dw, wt in (("q", 0, H, qo, dq, dqw, w[0]), ("k", H, H + G, ko, dk, dkw, w[1])):
+        ref = R.qk_norm(qkv[:used, lo:hi], wt, turns, rot, pairs, eps, do[:used, lo:hi])
+        worst = max(worst, B.check(name, y[:used], *ref["y"]), B.check("d" + name, dx[:used], *ref["dx"]),
+                    B.check(f"d{name}_weight", dw, *ref["dw"]))
+        assert (y[used:] == 0).all() and (dx[used:] == 0).all()
+    return worst
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 32, 40, 56, 64, 72, 80, 96, 104, 112, 120, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+def test_qk_norm_sizes(D, dtype, pairs):
+    """Every head size's lanes, with all, part and none of the head turning."""
+    for i, rot in enumerate(sorted({0, 8, 16, D // 16 * 8, D})):
+        if rot > D:
+            continue
+        say(f"[gpu] qk norm D={D} rot={rot} {dtype} {pairs}")
+        worst = qk_case(37, 3, 2, D, dtype, 100 + i, rot, pairs, (None, F32, BF)[i % 3], lengths=[20, 0, 1, 16])
+        say(f"[gpu]   worst error {worst:.3f} of its bound")
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 63, 64, 65, 1000, 4099])
+@pytest.mark.parametrize("heads", [(1, 1), (12, 12), (16, 2), (9, 17)])
+def test_qk_norm_tokens_and_heads(T, heads):
+    qk_case(T, *heads, 64, BF, 200, weights=F32)
+
+
+def test_qk_norm_blocks_take_several_tiles():
+    """More tiles of tokens and heads than a launch has blocks."""
+    qk_case(70001, 2, 1, 32, BF, 210, weights=F32, lengths=[70000])
+    qk_case(33000, 1, 4, 128, F32, 211, pairs="neighbours", weights=BF)
+
+
+@pytest.mark.parametrize("lengths", [[], [0], [0, 0, 5, 0], [1] * 70, [3] * 300, [64, 1, 65], [5000, 1, 0, 2]])
+@pytest.mark.parametrize("tail", [0, 1, 130])
+def test_qk_norm_sequences(lengths, tail):
+    """Positions restart in each sequence; rows behind the last one are not read."""
+    if sum(lengths) + tail:
+        qk_case(sum(lengths) + tail, 4, 2, 64, BF, 220, lengths=lengths, weights=BF)
+
+
+def test_qk_norm_positions_given_with_sequences():
+    """Positions count as they are given, and the last offset still ends the rows."""
+    pos = randint(0, 5000, (50,), 1, torch.int32)
+    qk_case(50, 3, 1, 64, BF, 230, lengths=[10, 30], positions=pos)
+    qk_case(50, 3, 1, 64, F32, 231, lengths=[10, 30], positions=pos.long(), layout="heads")
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_qk_norm_far_and_negative_positions(dtype):
+    """Angles are exact at every position that the type holds."""
+    top = torch.iinfo(torch.int32).max if dtype == torch.int32 else 1 << 44
+    pos = torch.tensor([0, 1, -1, 1 << 20, -(1 << 20) - 3, top, -top, top - 1, 123456789, -987654321], dtype=dtype)
+    for seed, (d, pairs) in enumerate(itertools.product((F32, BF), ("halves", "neighbours"))):
+        qk_case(10, 2, 2, 64, d, 240 + seed, pairs=pairs, positions=pos)
+
+
+def test_qk_norm_frequencies():
+    """Frequencies of the caller's: zeros keep a pair, negative ones turn it back, fast ones wrap."""
+    f = [1.0, 0.0, -0.25, 64.0, -64.0, 3.141592653589793, 1e-9, 0.5]
+    qk_case(300, 2, 1, 64, F32, 250, rot=16, freqs=f)
+    qk_case(300, 2, 1, 64, BF, 251, rot=16, freqs=f, pairs="neighbours")
+
+
+def test_qk_norm_layouts():
+    for layout, dtype in itertools.product(("fused", "heads"), (BF, F32)):
+        qk_case(133, 6, 2, 80, dtype, 260, rot=32, layout=layout, lengths=[100, 30], weights=dtype)
+
+
+def test_qk_norm_scales_and_zero_rows():
+    """Heads of any scale; a head of zeros stays zero and its gradient is dz / sqrt(eps)."""
+    qk_case(40, 2, 2, 64, BF, 270, std=1e-12, eps=0.0)
+    qk_case(40, 2, 2, 64, BF, 271, std=1e12)
+    q = torch.zeros(4, 1, 64, device=DEV)
+    g = randn((4, 1, 64), 272).to(DEV)
+    qo, _ = lib.qk_norm_forward(q, q.clone(), eps=1e-4)
+    dq, _, _, _ = lib.qk_norm_backward(g, g, q, q.clone(), eps=1e-4)
+    assert (qo == 0).all() and torch.allclose(dq, g * 100, rtol=1e-6, atol=0)
+
+
+def test_qk_norm_writes_only_its_outputs():
+    """Outputs in slices of wider buffers; rows behind the last sequence stay as they were."""
+    T, H, G, D = 75, 4, 2, 64
+    qkv = randn((T, H + 2 * G, D), 280, BF).to(DEV)
+    q, k, rot, cu = qkv[:, :H], qkv[:, H:H + G], lib.Rotation(D), cu_of([30, 33])
+    w = randn((D,), 281).to(DEV)
+    how = dict(cu_seqlens=cu, q_weight=w, k_weight=w)
+    qo, ko = lib.qk_norm_forward(q, k, rot, **how)
+    buf = torch.full((T, H + 2 * G, D), 7.0, dtype=BF, device=DEV)
+    keep = qkv.clone()
+    lib.qk_norm_forward(q, k, rot, q_out=buf[:, :H], k_out=buf[:, H + G:], **how)
+    assert torch.equal(buf[:63, :H], qo[:63]) and torch.equal(buf[:63, H + G:], ko[:63])
+    assert (buf[63:] == 7).all() and (buf[:, H:H + G] == 7).all()
+    do = randn((T, H + G, D), 282, BF).to(DEV)
+    dq, dk, dqw, dkw = lib.qk_norm_backward(do[:, :H], do[:, H:], q, k, rot, **how)
+    buf.fill_(7.0)
+    got = lib.qk_norm_backward(do[:, :H], do[:, H:], q, k, rot, dq=buf[:, :H], dk=buf[:, H:H + G], **how)
+    assert torch.equal(buf[:63, :H], dq[:63]) and torch.equal(buf[:63, H:H + G], dk[:63])
+    assert (buf[63:] == 7).all() and (buf[:, H + G:] == 7).all()
+    assert torch.equal(got[2], dqw) and torch.equal(got[3], dkw) and torch.equal(qkv, keep)
+
+
+def test_qk_norm_nan_stays_in_its_head():
+    q, k = randn((20, 4, 64), 290, BF).to(DEV), randn((20, 2, 64), 291, BF).to(DEV)
+    q[3, 1, 5], k[7, 0, 63] = float("nan"), float("inf")
+    rot = lib.Rotation(64)
+    for out in (lib.qk_norm_forward(q, k, rot), lib.qk_norm_backward(q.clone(), k.clone(), q, k, rot)[:2]):
+        bad = [(~torch.isfinite(t.float())).any(2) for t in out]
+        assert bad[0][3, 1] and bad[0].sum() == 1 and bad[1][7, 0] and bad[1].sum() == 1
+
+
+def test_qk_norm_without_tokens():
+    e = torch.empty(0, 4, 64, device=DEV)
+    w = torch.ones(64, device=DEV)
+    qo, ko = lib.qk_norm_forward(e, e, lib.Rotation(64))
+    dq, dk, dqw, dkw = lib.qk_norm_backward(e, e, e, e, lib.Rotation(64), q_weight=w, k_weight=w)
+    assert qo.shape == ko.shape == dq.shape == dk.shape == (0, 4, 64) and (dqw == 0).all() and (dkw == 0).all()
+    z = torch.zeros(5, 4, 64, device=DEV)  # tokens, but no sequence
+    qo, _ = lib.qk_norm_forward(z + 1, z + 2, cu_seqlens=cu_of([]))
+    _, _, dqw, _ = lib.qk_norm_backward(z + 1, z + 1, z + 1, z + 2, q_weight=w, k_weight=w, cu_seqlens=cu_of([]))
+    assert (qo == 0).all() and (dqw == 0).all()
+
+
+def test_qk_norm_bad_offsets_stay_inside():
+    """Offsets out of order or out of range: only positions are undefined."""
+    q = randn((200, 2, 64), 295, BF).to(DEV)
+    for cu in ([0, 150, 20, 200], [0, 5000], [0, -7, 100], [50, 60, 2147483647], [0, 10, -2147483648]):
+        qo, ko = lib.qk_norm_forward(q, q.clone(), lib.Rotation(64), cu_seqlens=torch.tensor(cu, dtype=torch.int32,
+                                                                                              device=DEV))
+        assert torch.isfinite(qo.float()).all() and torch.equal(qo, ko)
+
+
+def test_qk_norm_token_strides_past_32_bits():
+    T, step = 300, 1 << 23  # 2.5e9 elements from the first token to the last
+    buf = torch.empty((T - 1) * step + 4 * 64, dtype=BF, device=DEV)
+    view = torch.as_strided(buf, (T, 4, 64), (step, 64, 1))
+    src = randn((T, 4, 64), 296, BF).to(DEV)
+    view.copy_(src)
+    rot = lib.Rotation(64)
+    want = lib.qk_norm_forward(src[:, :2], src[:, 2:], rot)
+    got = lib.qk_norm_forward(view[:, :2], view[:, 2:], rot)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    lib.qk_norm_forward(src[:, :2], src[:, 2:], rot, q_out=view[:, :2], k_out=view[:, 2:])
+    assert torch.equal(view[:, :2], want[0]) and torch.equal(view[:, 2:], want[1])
+
+
+# -------------------------------------------------------------- embedding --
+def embed_case(ids, V, C, table_dtype, dtype, seed, scale=1.0, accumulate=False):
+    table, dout = randn((V, C), seed, table_dtype), randn((*ids.shape, C), seed + 1, dtype)
+    old = randn((V, C), seed + 2, table_dtype) if accumulate else None
+    dev = ids.to(DEV)
+    out = lib.embedding_forward(table.to(DEV), dev, scale=scale, dtype=dtype)
+    given = None if old is None else old.to(DEV)
+    dtable = lib.embedding_backward(dout.to(DEV), dev, V, scale=scale, dtype=table_dtype, dtable=given,
+                                    accumulate=accumulate)
+    torch.cuda.synchronize()
+    ref = R.embedding(table, ids, scale, dtype, dout, table_dtype, old)
+    return max(B.check("out", out, *ref["out"]), B.check("dtable", dtable, *ref["dtable"]))
+
+
+@pytest.mark.parametrize("C", [1, 3, 4, 7, 8, 9, 64, 100, 255, 256, 257, 512, 520, 768, 1001, 2048, 2056, 8200])
+@pytest.mark.parametrize("table_dtype,dtype", [(BF, BF), (F32, BF), (BF, F32), (F32, F32)])
+def test_embedding_widths(C, table_dtype, dtype):
+    say(f"[gpu] embedding width {C} {table_dtype} -> {dtype}")
+    ids = randint(-1, 42, (133,), 300, torch.int32)  # -1 and 41 lie outside
+    worst = embed_case(ids, 41, C, table_dtype, dtype, 301, scale=1.7)
+    say(f"[gpu]   worst error {worst:.3f} of its bound")
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 1023, 1024, 1025, 2049, 5000, 20000])
+@pytest.mark.parametrize("V", [1, 2, 255, 256, 1023, 1024, 50257])
+def test_embedding_tokens_and_vocabularies(T, V):
+    ids = randint(0, V, (T,), 310 + T)
+    embed_case(ids, V, 24, F32, BF, 311, scale=-0.5)
+
+
+@pytest.mark.parametrize("T", [33, 640, 2080, 5000, 70000])
+def test_embedding_long_runs(T):
+    """Ids that fill many chunks of the sorted list, alone and between others."""
+    embed_case(torch.full((T,), 7), 9, 40, F32, F32, 320)
+    ids = randint(0, 300, (T,), 321)
+    ids[randint(0, T, (T,), 322)] = 123
+    embed_case(ids, 300, 40, BF, BF, 323)
+    embed_case(torch.arange(T) // 33, 70000 // 33 + 1, 16, BF, F32, 324)
+
+
+@pytest.mark.parametrize("T,V,C", [(300001, 3001, 8), (1100000, 50304, 4), (5000, (1 << 20) - 1, 4),
+                                   (5000, 1 << 20, 4), (3000, (1 << 22) + 5, 2), (500, (1 << 29) + 3, 1)])
+def test_embedding_sort_passes(T, V, C):
+    """Segments of several rounds, and one to three passes over the ids' bits."""
+    say(f"[gpu] embedding sort T={T} V={V}")
+    if V < 1 << 25:
+        embed_case(randint(0, V, (T,), 330), V, C, F32, F32, 331)
+        return
+    ids = randint(0, V, (T,), 330)  # too large a table for the reference: look at the rows that count
+    dout = randn((T, C), 332)
+    g = lib.embedding_backward(dout.to(DEV), ids.to(DEV), V)
+    rows, at = torch.unique(ids, return_inverse=True)
+    want = torch.zeros(rows.numel(), C, dtype=torch.float64).index_add_(0, at, dout.double())
+    assert (g[rows.to(DEV)].double().cpu() - want).abs().max() < 1e-5
+    assert int((g != 0).sum()) == int((want != 0).sum())
+
+
+def test_embedding_ids_outside():
+    """Negative ids, the vocabulary's size and beyond, in both types: zeros, and no gradient."""
+    ids = torch.tensor([0, 5, -1, 6, 7, -(1 << 62), (1 << 62) + 3, (1 << 32) + 2, 2], dtype=torch.int64)
+    embed_case(ids, 6, 16, BF, BF, 340)
+    embed_case(ids.clamp(-(1 << 31), (1 << 31) - 1).int(), 6, 16, F32, F32, 341)
+    embed_case(torch.full((3000,), -1), 6, 16, F32, F32, 342)
+
+
+@pytest.mark.parametrize("T", [5, 3000, 40000])
+@pytest.mark.parametrize("table_dtype,dtype", [(BF, BF), (F32, BF)])
+def test_embedding_accumulates(T, table_dtype, dtype):
+    embed_case(randint(-3, 2000, (T,), 350), 2000, 72, table_dtype, dtype, 351, scale=0.3, accumulate=True)
+
+
+def test_embedding_shapes_and_strides():
+    """ids of any shape; table, out, dout and dtable as columns of wider buffers, off 16-byte boundaries."""
+    ids = randint(0, 50, (3, 7, 5), 360)
+    embed_case(ids, 50, 33, BF, BF, 361)
+    for dtype, off in itertools.product((BF, F32), (0, 1, 8)):
+        wide, cols = randn((50, 120), 362, dtype).to(DEV), slice(off, off + 64)
+        table = wide[:, cols]
+        want = lib.embedding_forward(table.contiguous(), ids.to(DEV), scale=2.5)
+        buf = torch.full((105, 120), 3.0, dtype=dtype, device=DEV)
+        lib.embedding_forward(table, ids.reshape(-1).to(DEV), scale=2.5, out=buf[:, cols])
+        assert torch.equal(buf[:, cols].reshape(want.shape), want)
+        assert (buf[:, :off] == 3).all() and (buf[:, off + 64:] == 3).all()
+        dout = randn((105, 120), 363, dtype).to(DEV)[:, cols]
+        want = lib.embedding_backward(dout.contiguous(), ids.reshape(-1).to(DEV), 50, dtype=dtype)
+        grad = torch.full((50, 120), 3.0, dtype=dtype, device=DEV)
+        lib.embedding_backward(dout, ids.reshape(-1).to(DEV), 50, dtable=grad[:, cols])
+        assert torch.equal(grad[:, cols], want)
+        assert (grad[:, :off] == 3).all() and (grad[:, off + 64:] == 3).all()
+
+
+def test_embedding_without_tokens():
+    ids = torch.empty(0, dtype=torch.int64, device=DEV)
+    table = randn((9, 16), 370).to(DEV)
+    assert lib.embedding_forward(table, ids).shape == (0, 16)
+    assert (lib.embedding_backward(torch.empty(0, 16, device=DEV), ids, 9) == 0).all()
+    old = table.clone()
+    lib.embedding_backward(torch.empty(0, 16, device=DEV), ids, 9, dtable=old, accumulate=True)
+    assert torch.equal(old, table)
+
+
+def test_embedding_offsets_past_32_bits():
+    """Rows 2^31 bytes apart in the table, the output and their gradients."""
+    ld, cols = 1 << 30, 40
+    buf = torch.empty(4 * ld + cols, dtype=BF, device=DEV)
+    far = torch.as_strided(buf, (5, cols), (ld, 1))
+    src, ids = randn((5, cols), 380, BF).to(DEV), torch.tensor([4, 0, 4, 3, 1], device=DEV)
+    far.copy_(src)
+    want = src[ids]
+    assert torch.equal(lib.embedding_forward(far, ids), want)
+    lib.embedding_forward(src, ids, out=far)
+    assert torch.equal(far, want)
+    want = lib.embedding_backward(src, ids, 5, dtype=BF)
+    far.copy_(src)
+    assert torch.equal(lib.embedding_backward(far, ids, 5, dtype=BF), want)
+    lib.embedding_backward(src, ids, 5, dtable=far)
+    assert torch.equal(far, want)
+
+
+def test_embedding_nan_stays_in_its_row():
+    ids = randint(0, 20, (3000,), 390).to(DEV)
+    dout = randn((3000, 24), 391).to(DEV)
+    dout[1234] = float("nan")
+    bad = (~torch.isfinite(lib.embedding_backward(dout, ids, 20))).any(1)
+    assert bad[ids[1234]] and bad.sum() == 1
+
+
+def test_embedding_gradient_is_reproducible():
+    ids = randint(0, 3000, (50000,), 395).to(DEV)
+    dout = randn((50000, 96), 396, BF).to(DEV)
+    first = lib.embedding_backward(dout, ids, 3000)
+    for _ in range(3):
+        assert torch.equal(lib.embedding_backward(dout, ids, 3000), first)
