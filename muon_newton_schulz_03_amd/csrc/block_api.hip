@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "../../include/muon.h"
 #include "block_internal.h"
@@ -252,15 +253,24 @@ int check_qk(const muon_qk_norm_desc* d, const muon_rotation* r) {
   return MUON_OK;
 }
 
-// A frequency in radians as the fraction of a turn, in units of 2^-64 (modulo
-// whole turns, which no position sees).
+// A frequency in radians (at most 64) as the fraction of a turn, in units of
+// 2^-64, modulo whole turns, which no position sees.  In integers: the mantissa
+// times 2 / pi in units of 2^-64, shifted to its place and rounded.  (32 of
+// them took 9 us in long doubles, this way 0.5.)
 uint64_t turn_of(double frequency) {
-  const long double turns = (long double)frequency / 6.283185307179586476925286766559L;
-  const long double part = std::floor((turns - std::floor(turns)) * 0x1p64L + 0.5L);
-  return part >= 0x1p64L ? 0 : (uint64_t)part;
+  constexpr uint64_t kTwoOverPi = 0xA2F9836E4E44152Aull;
+  uint64_t bits;
+  std::memcpy(&bits, &frequency, sizeof bits);
+  // frequency / 2 pi 2^64 = mantissa 2^(exponent - 1075) (2 / pi) 2^64 / 4
+  const int shift = 1077 - (int)(bits >> 52 & 0x7FF);  // at least 48
+  if (shift > 118) return 0;
+  const uint64_t mantissa = (bits & 0xFFFFFFFFFFFFFull) | 1ull << 52;
+  const unsigned __int128 product = (unsigned __int128)mantissa * kTwoOverPi;
+  const uint64_t turn = (uint64_t)((product + ((unsigned __int128)1 << (shift - 1))) >> shift);
+  return bits >> 63 ? 0 - turn : turn;
 }
 
-size_t qk_workspace(const muon_qk_norm_desc* d) { return align_up((size_t)2 * kQkBlocks * d->head_dim * sizeof(float)); }
+size_t qk_workspace(const muon_qk_norm_desc* d) { return align_up((size_t)kQkBlocks * 2 * d->head_dim * sizeof(float)); }
 
 // What both calls share: the views, the rotation and the split over blocks.
 int qk_args(const muon_qk_norm_desc* d, const muon_rotation* r, const int32_t* cu, const void* positions,
@@ -437,8 +447,9 @@ int muon_qk_norm_forward(const muon_qk_norm_desc* d, const muon_rotation* rotati
                          {"positions", flat(positions, (size_t)d->tokens * (a.pos64 ? 8 : 4))}};
   if (int rc = check_apart("query/key norm", ops, 2, 8)) return rc;
   const bool bf16 = d->dtype == MUON_DTYPE_BF16;
-  plan_qk(a, bf16, false);
-  const hipError_t e = launch_qk(a, bf16, rotation ? rotation->pairs : 0, false, (hipStream_t)hip_stream);
+  const int pairs = rotation ? rotation->pairs : kPairHalves;
+  plan_qk(a, bf16, pairs);
+  const hipError_t e = launch_qk(a, bf16, pairs, false, (hipStream_t)hip_stream);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "query/key norm forward launch");
 }
 
@@ -491,11 +502,12 @@ int muon_qk_norm_backward(const muon_qk_norm_desc* d, const muon_rotation* rotat
   if (int rc = check_apart("query/key norm", ops, 5, 13)) return rc;
   a.part = sums ? (float*)workspace : nullptr;
   const bool bf16 = d->dtype == MUON_DTYPE_BF16;
-  plan_qk(a, bf16, true);
+  const int pairs = rotation ? rotation->pairs : kPairHalves;
+  plan_qk(a, bf16, pairs);
   hipError_t e = hipSuccess;
-  if (d->tokens > 0) e = launch_qk(a, bf16, rotation ? rotation->pairs : 0, true, (hipStream_t)hip_stream);
+  if (d->tokens > 0) e = launch_qk(a, bf16, pairs, true, (hipStream_t)hip_stream);
   if (e == hipSuccess && sums)
-    e = launch_qk_sum(QkSumArgs{a.part, {dq_weight, dk_weight}, {a.side[0].blocks, a.side[1].blocks}, d->head_dim},
+    e = launch_qk_sum(QkSumArgs{a.part, {dq_weight, dk_weight}, d->tokens > 0 ? a.blocks : 0, d->head_dim},
                       (hipStream_t)hip_stream);
   return e == hipSuccess ? MUON_OK : hip_fail(e, "query/key norm backward launch");
 }

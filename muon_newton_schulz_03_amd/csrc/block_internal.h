@@ -97,8 +97,6 @@ struct QkSide {
   HeadView dy;         // backward only
   const void* weight;  // null: ones
   int32_t heads;
-  int32_t chunk;       // heads a thread takes in turn
-  int32_t blocks;      // of the launch, which has the queries' blocks first
   int32_t zero_tail;   // set out's rows behind the last sequence to zero
 };
 
@@ -106,13 +104,17 @@ struct QkArgs {
   QkSide side[2];
   const int32_t* cu;       // null: no sequences, every token counts
   const void* positions;   // null: offset within the sequence (without sequences, the token's number)
-  float* part;             // backward: weight gradients of each block, [blocks][dim]; null: not wanted
+  float* part;             // backward: weight gradients of each block, [blocks][2][dim]; null: not wanted
   int64_t tokens;
   int32_t seqs;
   int32_t dim;
   int32_t rotated;         // elements of a head that turn, the first ones
   int32_t p_bf16;
   int32_t pos64;
+  int32_t blocks;
+  int32_t apart;           // 1: even blocks take the queries, odd ones the keys
+  int32_t wide, wide_log;  // heads of a token that a wave takes at once, a power of two
+  int32_t pair_lanes;      // log2 of the lanes that compute a token's angles
   float eps;
   uint64_t turns[kMaxDim / 2];  // a pair's turn per position, as a fraction of 2^64
 };
@@ -120,14 +122,14 @@ struct QkArgs {
 struct QkSumArgs {
   const float* part;
   float* dweight[2];  // either may be null
-  int32_t blocks[2];
+  int32_t blocks;
   int32_t dim;
 };
 
-constexpr int kQkBlocks = 1024;  // of a side, at most
+constexpr int kQkBlocks = 1024;  // at most: four waves a SIMD
 enum { kPairHalves = 0, kPairNeighbours = 1 };
-// Fills in the sides' chunk and blocks.
-void plan_qk(QkArgs& a, bool bf16, bool backward);
+// Fills in the launch's layout: blocks, wide, pair_lanes.
+void plan_qk(QkArgs& a, bool bf16, int pairs);
 hipError_t launch_qk(const QkArgs& a, bool bf16, int pairs, bool backward, hipStream_t stream);
 hipError_t launch_qk_sum(const QkSumArgs& a, hipStream_t stream);
 

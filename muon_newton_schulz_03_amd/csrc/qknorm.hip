@@ -19,8 +19,9 @@
 namespace muon {
 namespace {
 
-// Sum over groups of N neighbouring lanes (4, 8 or 16), the same in all of
-// them: lanes exchanged within quads, then quads and halves mirrored.
+// Sum over groups of N neighbouring lanes (8, 16 or 32), the same in all of
+// them: lanes exchanged within quads, then quads and halves mirrored, then rows
+// of 16 exchanged.
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
   return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
@@ -29,8 +30,9 @@ template <int N>
 __device__ __forceinline__ float lanes_sum(float v) {
   v = dpp_add<0xB1>(v);                         // quad_perm 1 0 3 2
   v = dpp_add<0x4E>(v);                         // quad_perm 2 3 0 1
-  if constexpr (N > 4) v = dpp_add<0x141>(v);   // row_half_mirror
+  v = dpp_add<0x141>(v);                        // row_half_mirror
   if constexpr (N > 8) v = dpp_add<0x140>(v);   // row_mirror
+  if constexpr (N > 16) v += __shfl_xor(v, 16);
   return v;
 }
 
@@ -75,25 +77,45 @@ __device__ __forceinline__ void pack(const float* v, u32x4& r) { r = pack8_bf16(
 __device__ __forceinline__ void pack(const float* v, u32x2& r) { r = pack4_bf16(v[0], v[1], v[2], v[3]); }
 __device__ __forceinline__ void pack(const float* v, f32x4& r) { r = f32x4{v[0], v[1], v[2], v[3]}; }
 
-// The two members of N pairs from a thread's two vectors, and back.
-template <int N, bool NEIGH>
-__device__ __forceinline__ void to_pairs(const float* v, float* a, float* b) {
+// The same vector of another lane.
+template <class R>
+__device__ __forceinline__ R from_lane(R v, int lane) {
+  constexpr int N = sizeof(R) / 4;
+  typedef int words __attribute__((ext_vector_type(N)));
+  words w = __builtin_bit_cast(words, v);
 #pragma unroll
-  for (int e = 0; e < N; ++e) a[e] = v[NEIGH ? 2 * e : e], b[e] = v[NEIGH ? 2 * e + 1 : N + e];
-}
-template <int N, bool NEIGH>
-__device__ __forceinline__ void from_pairs(const float* a, const float* b, float* v) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) v[NEIGH ? 2 * e : e] = a[e], v[NEIGH ? 2 * e + 1 : N + e] = b[e];
+  for (int i = 0; i < N; ++i) w[i] = __builtin_amdgcn_ds_bpermute(4 * lane, w[i]);
+  return __builtin_bit_cast(R, w);
 }
 
-__device__ __forceinline__ float param(const void* p, bool bf16, int at) {
-  return !p ? 1.f : bf16 ? (float)*gv<__bf16>((const __bf16*)p + at) : *gv<float>((const float*)p + at);
+template <int N>
+__device__ __forceinline__ void read_angles(const float* p, float* v) {
+  if constexpr (N == 2) {
+    const f32x2 r = *(const f32x2*)p;
+    v[0] = r[0], v[1] = r[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) unpack(*(const f32x4*)(p + i), v + i);
+  }
 }
 
-// The start of the token's sequence: the last offset at or before it.
-__device__ __forceinline__ int64_t sequence_start(const int32_t* cu, int seqs, int64_t token) {
+// A span of tokens of one sequence: [start, end).
+struct Span {
+  int64_t start, end;
+};
+// The one that holds the token, which is the same in all lanes: the offsets come through scalar loads.
+__device__ __forceinline__ Span span_of(const int32_t* cu, int seqs, int64_t token) {
+  const MUON_CONST int32_t* c = (const MUON_CONST int32_t*)(const void*)cu;
   int lo = 0, hi = seqs;  // cu[lo] <= token < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (c[mid] <= token) lo = mid;
+    else hi = mid;
+  }
+  return Span{c[lo], c[hi]};
+}
+__device__ __forceinline__ int64_t start_of(const int32_t* cu, int seqs, int64_t token) {
+  int lo = 0, hi = seqs;
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
     if (*gv<int32_t>(cu + mid) <= token) lo = mid;
@@ -102,218 +124,300 @@ __device__ __forceinline__ int64_t sequence_start(const int32_t* cu, int seqs, i
   return *gv<int32_t>(cu + lo);
 }
 
-// A group of LPH lanes holds one token's head, a lane two vectors of VEC
-// elements that form VEC pairs; the lanes keep their place in the head, their
-// weights and their token's angles while they go through a chunk of its heads.
-template <class T, int VEC, int LPH, bool NEIGH, bool BACK>
-__global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkArgs a) {
-  constexpr int TOKENS = kThreads / LPH;  // of a block
+// A wave takes a group of tokens at a time and goes through their queries and
+// then their keys in steps: LPH lanes a head, a vector of VEC elements a lane,
+// `wide` heads of each token a step.  So a step's loads are whole heads next to
+// each other, and a lane's place in them never changes.  The other members of a
+// vector's pairs are the vector of another lane (halves) or its own neighbours.
+// The lanes first compute the group's cosines and sines, each once, and share
+// them through LDS.
+// The next steps' loads run while these are computed: three steps forward, one
+// backward, which leave room for four waves a SIMD.  65536 tokens of 24 heads of
+// 64 forward / 16384 tokens of 40 heads of 128 backward: 84 / 109 us; with two
+// steps forward 92, four 93 (three waves); with two backward 121 (three waves) or
+// 152 (registers spill).  A wave with both sides of a token reads the projection's
+// row as it lies: with queries and keys in blocks of their own 94 / 110 us.
+template <class T, int VEC, int LPH, bool NEIGH, bool BACK, bool W>
+__global__ __launch_bounds__(kThreads, 4) void qk_norm_kernel(QkArgs a) {
+  constexpr int AHEAD = BACK ? 1 : 3, WAVES = kThreads / 64;
+  constexpr int ANGLES = NEIGH ? VEC / 2 : VEC;       // of a lane
+  constexpr int TABLE = LPH * VEC * (64 / LPH) / 2;   // of a wave's tokens, at most
   typedef typename Raw<T, VEC>::type raw_t;
-  const bool second = (int)blockIdx.x >= a.side[0].blocks;
-  const QkSide& s = second ? a.side[1] : a.side[0];
-  const int block = (int)blockIdx.x - (second ? a.side[0].blocks : 0);
-  const int u = threadIdx.x % LPH, slot = threadIdx.x / LPH;
+  __shared__ __align__(16) float table[WAVES][3][TABLE];  // cosines, sines and negative sines
+  __shared__ __align__(16) float weights[2][W ? LPH * VEC : 4];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int u = lane % LPH, lo = u * VEC;
+  const int my_head = lane / LPH & (a.wide - 1), my_token = lane / LPH >> a.wide_log;
+  const int tokens = (64 / LPH) >> a.wide_log;  // of a group
+  const bool on = lo < a.dim, turns = lo < a.rotated;
+  const int half = a.rotated / 2 / VEC;  // lanes of a half
+  const bool upper = !NEIGH && u >= half;
+  const int across = NEIGH || !turns ? 0 : upper ? -half : half;  // lanes to the partner
+  // where a lane's cosines and sines start, the latter with the sign that its vector takes them with
+  const int pairs = a.rotated / 2;
+  float* angles = table[wave][0];
+  const float* cosines = angles + my_token * pairs + (NEIGH ? u * ANGLES : (upper ? u - half : u) * ANGLES);
+  const float* sines = cosines + (upper != BACK ? TABLE : 2 * TABLE);
 
-  const int turning = a.rotated / (2 * VEC);  // lanes with pairs that turn
-  const bool turns = u < turning;
-  const int lo = turns && !NEIGH ? u * VEC : turns ? u * 2 * VEC : a.rotated + (u - turning) * 2 * VEC;
-  const int hi = turns && !NEIGH ? lo + a.rotated / 2 : lo + VEC;
-  const bool on_lo = lo < a.dim, on_hi = hi < a.dim;
-  float wa[VEC], wb[VEC], da[VEC], db[VEC];
-  uint64_t turn[VEC];
-  {
-    float w[2 * VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      w[e] = on_lo ? param(s.weight, a.p_bf16, lo + e) : 0.f;
-      w[VEC + e] = on_hi ? param(s.weight, a.p_bf16, hi + e) : 0.f;
-      turn[e] = turns ? a.turns[u * VEC + e] : 0;
-      da[e] = db[e] = 0.f;
-    }
-    to_pairs<VEC, NEIGH>(w, wa, wb);
-  }
-  const int64_t last = a.cu ? min(max((int64_t)*gv<int32_t>(a.cu + a.seqs), (int64_t)0), a.tokens) : a.tokens;
-  const float inv = 1.f / (float)a.dim;
-  const int chunks = (s.heads + s.chunk - 1) / s.chunk;
-  const int64_t items = (a.tokens + TOKENS - 1) / TOKENS * chunks;
-  for (int64_t item = block; item < items; item += s.blocks) {
-    const int64_t token = item / chunks * TOKENS + slot;
-    const int h0 = (int)(item % chunks) * s.chunk, h1 = min(h0 + s.chunk, s.heads);
-    if (token >= last) {
-      if (token < a.tokens && s.zero_tail)
-        for (int h = h0; h < h1; ++h) {
-          T* y = (T*)s.out.data + token * s.out.token + h * s.out.head;
-          if (on_lo) *gv<raw_t>(y + lo) = raw_t{};
-          if (on_hi) *gv<raw_t>(y + hi) = raw_t{};
-        }
-      continue;
-    }
-    float cs[VEC], sn[VEC];
-    if (turns) {
-      int64_t p = token;
-      if (a.positions)
-        p = a.pos64 ? *gv<int64_t>((const int64_t*)a.positions + token) : *gv<int32_t>((const int32_t*)a.positions + token);
-      else if (a.cu)
-        p = token - sequence_start(a.cu, a.seqs, token);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) turn_sincos((uint32_t)(((uint64_t)p * turn[e]) >> 32), sn[e], cs[e]);
-    }
-    for (int h = h0; h < h1; ++h) {
-      const T* x = (const T*)s.x.data + token * s.x.token + h * s.x.head;
-      float v[2 * VEC], xa[VEC], xb[VEC];
-#pragma unroll
-      for (int e = 0; e < 2 * VEC; ++e) v[e] = 0.f;
-      if (on_lo) unpack(*gv<raw_t>(x + lo), v);
-      if (on_hi) unpack(*gv<raw_t>(x + hi), v + VEC);
-      to_pairs<VEC, NEIGH>(v, xa, xb);
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(xa[e], xa[e], __builtin_fmaf(xb[e], xb[e], sum));
-      const float r = 1.f / sqrtf(__builtin_fmaf(lanes_sum<LPH>(sum), inv, a.eps));
-      float ya[VEC], yb[VEC];
-      if constexpr (BACK) {
-        const T* dy = (const T*)s.dy.data + token * s.dy.token + h * s.dy.head;
-#pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) v[e] = 0.f;
-        if (on_lo) unpack(*gv<raw_t>(dy + lo), v);
-        if (on_hi) unpack(*gv<raw_t>(dy + hi), v + VEC);
-        to_pairs<VEC, NEIGH>(v, ya, yb);
-        float gx = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (turns) {
-            const float t = __builtin_fmaf(ya[e], cs[e], yb[e] * sn[e]);
-            yb[e] = __builtin_fmaf(yb[e], cs[e], -(ya[e] * sn[e]));
-            ya[e] = t;
-          }
-          da[e] = __builtin_fmaf(ya[e] * r, xa[e], da[e]);
-          db[e] = __builtin_fmaf(yb[e] * r, xb[e], db[e]);
-          ya[e] *= wa[e];
-          yb[e] *= wb[e];
-          gx = __builtin_fmaf(ya[e], xa[e], __builtin_fmaf(yb[e], xb[e], gx));
-        }
-        const float c = lanes_sum<LPH>(gx) * inv * r * r;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          ya[e] = r * __builtin_fmaf(-xa[e], c, ya[e]);
-          yb[e] = r * __builtin_fmaf(-xb[e], c, yb[e]);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          ya[e] = xa[e] * r * wa[e];
-          yb[e] = xb[e] * r * wb[e];
-          if (turns) {
-            const float t = __builtin_fmaf(ya[e], cs[e], -(yb[e] * sn[e]));
-            yb[e] = __builtin_fmaf(yb[e], cs[e], ya[e] * sn[e]);
-            ya[e] = t;
-          }
-        }
-      }
-      from_pairs<VEC, NEIGH>(ya, yb, v);
-      T* y = (T*)s.out.data + token * s.out.token + h * s.out.head;
-      raw_t o;
-      pack(v, o);
-      if (on_lo) *gv<raw_t>(y + lo) = o;
-      pack(v + VEC, o);
-      if (on_hi) *gv<raw_t>(y + hi) = o;
-    }
-  }
-  if constexpr (BACK) {
-    if (!a.part) return;
-    // the block's sums: over the tokens of a wave, then over its waves, in a fixed order
-    __shared__ float red[kThreads / 64][LPH * 2 * VEC];
-#pragma unroll
-    for (int o = LPH; o < 64; o *= 2)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) da[e] += __shfl_xor(da[e], o), db[e] += __shfl_xor(db[e], o);
-    const int wave = threadIdx.x / 64;
-    if (threadIdx.x % 64 < LPH) {
-      float v[2 * VEC];
-      from_pairs<VEC, NEIGH>(da, db, v);
-#pragma unroll
-      for (int e = 0; e < 2 * VEC; ++e) red[wave][u * 2 * VEC + e] = v[e];
+  if constexpr (W) {
+    for (int i = threadIdx.x; i < 2 * LPH * VEC; i += kThreads) {
+      const void* p = a.side[i / (LPH * VEC)].weight;
+      const int at = i % (LPH * VEC);
+      weights[i / (LPH * VEC)][at] = at >= a.dim ? 0.f : !p ? 1.f : a.p_bf16 ? (float)*gv<__bf16>((const __bf16*)p + at)
+                                                                             : *gv<float>((const float*)p + at);
     }
     __syncthreads();
-    if (threadIdx.x >= LPH) return;
-    float* part = a.part + (int64_t)blockIdx.x * a.dim;
+  }
+  float w[VEC], wo[VEC], dw[2][VEC];  // own weights, and the partner's
 #pragma unroll
-    for (int e = 0; e < 2 * VEC; ++e) {
+  for (int e = 0; e < VEC; ++e) w[e] = wo[e] = dw[0][e] = dw[1][e] = 0.f;
+  // a lane computes the angles of one pair, of one token or several
+  const int pair = lane & ((1 << a.pair_lanes) - 1), pair_token = lane >> a.pair_lanes;
+  const uint64_t turn = pair < pairs ? a.turns[pair] : 0;
+  int64_t last = a.tokens;  // tokens that count
+  if (a.cu) last = min(max((int64_t)((const MUON_CONST int32_t*)(const void*)a.cu)[a.seqs], (int64_t)0), last);
+  const float inv = 1.f / (float)a.dim;
+
+  const T* x[2];
+  const T* dy[2];
+  T* out[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const QkSide& s = a.side[i];
+    x[i] = (const T*)s.x.data + my_token * s.x.token + my_head * s.x.head + lo;
+    dy[i] = (const T*)s.dy.data + my_token * s.dy.token + my_head * s.dy.head + lo;
+    out[i] = (T*)s.out.data + my_token * s.out.token + my_head * s.out.head + lo;
+  }
+  raw_t nx[AHEAD] = {}, ny[AHEAD] = {};  // the next steps as they were loaded
+  auto fetch = [&](auto side, int64_t first, int head) {
+    constexpr int S = decltype(side)::value;
+    const QkSide& s = a.side[S];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+      if (on && head + q * a.wide + my_head < s.heads && first + my_token < last) {
+        nx[q] = *gv<raw_t>(x[S] + (first * s.x.token + (head + q * a.wide) * s.x.head));
+        if constexpr (BACK) ny[q] = *gv<raw_t>(dy[S] + (first * s.dy.token + (head + q * a.wide) * s.dy.head));
+      }
+  };
+  typedef std::integral_constant<int, 0> queries;
+  typedef std::integral_constant<int, 1> keys;
+  // a block takes both sides, or where blocks are few one
+  const bool do_q = !a.apart || blockIdx.x % 2 == 0, do_k = !a.apart || blockIdx.x % 2 == 1;
+  const int64_t stride = (int64_t)(gridDim.x >> a.apart) * WAVES * tokens;
+  int64_t first = ((int64_t)(blockIdx.x >> a.apart) * WAVES + wave) * tokens;
+  Span span{0, 0};
+  if (do_q) fetch(queries{}, first, 0);
+  else fetch(keys{}, first, 0);
+  for (; first < a.tokens; first += stride) {
+    if (pairs) {
+      if (a.cu && !a.positions && first < last && (first < span.start || first >= span.end))
+        span = span_of(a.cu, a.seqs, first);
+      for (int t = pair_token; t < tokens && first + t < last; t += 64 >> a.pair_lanes) {
+        int64_t p = first + t;
+        if (a.positions)
+          p = a.pos64 ? *gv<int64_t>((const int64_t*)a.positions + p) : *gv<int32_t>((const int32_t*)a.positions + p);
+        else if (a.cu)
+          p -= p < span.end ? span.start : start_of(a.cu, a.seqs, p);
+        float sine, cosine;
+        turn_sincos((uint32_t)(((uint64_t)p * turn) >> 32), sine, cosine);
+        if (pair < pairs) {
+          float* c = angles + t * pairs + pair;
+          c[0] = cosine, c[TABLE] = sine, c[2 * TABLE] = -sine;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    float cs[ANGLES], sn[ANGLES];
+    if (turns) read_angles<ANGLES>(cosines, cs), read_angles<ANGLES>(sines, sn);
+    const bool counts = on && first + my_token < last;
+    auto heads_of = [&](auto side) {
+      constexpr int S = decltype(side)::value;
+      const QkSide& s = a.side[S];
+      if constexpr (W) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          unpack(*(const f32x4*)(weights[S] + lo + e), w + e);
+          if constexpr (!NEIGH && !BACK) unpack(*(const f32x4*)(weights[S] + lo + across * VEC + e), wo + e);
+        }
+      }
+      for (int head = 0; head < s.heads; head += AHEAD * a.wide) {
+        raw_t rx[AHEAD], ry[AHEAD];
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) rx[q] = nx[q], ry[q] = ny[q];
+        if (head + AHEAD * a.wide < s.heads) fetch(side, first, head + AHEAD * a.wide);
+        else if (S == 0 && do_k) fetch(keys{}, first, 0);
+        else if (S == 0 || do_q) fetch(queries{}, first + stride, 0);
+        else fetch(keys{}, first + stride, 0);
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+          if (head + q * a.wide >= s.heads) break;
+          float v[VEC], y[VEC], o[VEC];
+          unpack(rx[q], v);
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) sum = __builtin_fmaf(v[e], v[e], sum);
+          const float mean = __builtin_fmaf(lanes_sum<LPH>(sum), inv, a.eps);
+          const float r = sizeof(T) == 2 ? __builtin_amdgcn_rsqf(mean) : 1.f / sqrtf(mean);  // the former: off by 1 ulp
+          if constexpr (!NEIGH) unpack(from_lane(BACK ? ry[q] : rx[q], lane + across), o);
+          if constexpr (BACK) unpack(ry[q], y);
+          else if constexpr (W) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              y[e] = v[e] * w[e];
+              if constexpr (!NEIGH) o[e] *= wo[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = v[e];
+          }
+          // y_a = z_a cos - z_b sin and y_b = z_b cos + z_a sin, or back with the sines' sign changed
+          if (turns) {
+            if constexpr (NEIGH) {
+#pragma unroll
+              for (int e = 0; e < ANGLES; ++e) {
+                const float t = y[2 * e];
+                y[2 * e] = __builtin_fmaf(t, cs[e], y[2 * e + 1] * sn[e]);
+                y[2 * e + 1] = __builtin_fmaf(y[2 * e + 1], cs[e], -(t * sn[e]));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) y[e] = __builtin_fmaf(y[e], cs[e], o[e] * sn[e]);
+            }
+          }
+          const bool live = counts && head + q * a.wide + my_head < s.heads;
+          if constexpr (BACK) {
+            if (W && a.part && live) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) dw[S][e] = __builtin_fmaf(y[e] * r, v[e], dw[S][e]);
+            }
+            if constexpr (W) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) y[e] *= w[e];
+            }
+            float gx = 0.f;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) gx = __builtin_fmaf(y[e], v[e], gx);
+            const float c = lanes_sum<LPH>(gx) * inv * r * r;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = r * __builtin_fmaf(-v[e], c, y[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] *= r;
+          }
+          T* to = out[S] + (first * s.out.token + (head + q * a.wide) * s.out.head);
+          raw_t ro;
+          pack(y, ro);
+          if (live) *gv<raw_t>(to) = ro;
+          else if (s.zero_tail && on && first + my_token < a.tokens && head + q * a.wide + my_head < s.heads)
+            *gv<raw_t>(to) = raw_t{};
+        }
+      }
+    };
+    if (do_q) heads_of(queries{});
+    if (do_k) heads_of(keys{});
+  }
+  if constexpr (BACK && W) {
+    if (!a.part) return;
+    // the block's sums: over the heads of a wave, then over its waves, in a fixed order
+    __shared__ float red[WAVES][2][LPH * VEC];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = LPH; o < 64; o *= 2)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[i][e] += __shfl_xor(dw[i][e], o);
+      if (lane < LPH) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) red[wave][i][lo + e] = dw[i][e];
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.dim; c += kThreads) {
+      const int i = c >= a.dim, at = c - i * a.dim;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kThreads / 64; ++w) v += red[w][u * 2 * VEC + e];
-      const int at = e < VEC ? lo + e : hi + e - VEC;
-      if (e < VEC ? on_lo : on_hi) part[at] = v;
+      for (int j = 0; j < WAVES; ++j) v += red[j][i][at];
+      a.part[(int64_t)blockIdx.x * 2 * a.dim + c] = v;
     }
   }
 }
 
-// Sums of the blocks' weight gradients: a block for 32 elements of one side.
+// Sums of the blocks' weight gradients, 2 * dim columns: a block for 32 of them.
 constexpr int kSumThreads = 1024, kSumCols = 32;
 __global__ __launch_bounds__(kSumThreads) void qk_sum_kernel(QkSumArgs a) {
   constexpr int kGroups = kSumThreads / kSumCols;
   __shared__ float red[kGroups][kSumCols + 1];
-  const int tiles = (a.dim + kSumCols - 1) / kSumCols;
-  const int side = (int)blockIdx.x / tiles, col = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
-  const int c = (int)blockIdx.x % tiles * kSumCols + col;
-  const float* part = a.part + (side ? (int64_t)a.blocks[0] * a.dim : 0);
+  const int col = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols, n = 2 * a.dim;
+  const int c = (int)blockIdx.x * kSumCols + col;
   float s = 0.f;
-  if (c < a.dim)
+  if (c < n)
 #pragma unroll 16
-    for (int r = g; r < a.blocks[side]; r += kGroups) s += part[(int64_t)r * a.dim + c];
+    for (int r = g; r < a.blocks; r += kGroups) s += a.part[(int64_t)r * n + c];
   red[g][col] = s;
   __syncthreads();
-  if (g > 0 || c >= a.dim || !a.dweight[side]) return;
+  if (g > 0 || c >= n) return;
   s = 0.f;
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) s += red[r][col];
-  a.dweight[side][c] = s;
+  float* out = c < a.dim ? a.dweight[0] : a.dweight[1];
+  if (out) out[c < a.dim ? c : c - a.dim] = s;
 }
 
 // ----------------------------------------------------------------- launch --
-int vec_of(const QkArgs& a, bool bf16) { return bf16 && a.rotated % 16 == 0 ? 8 : 4; }
-int lanes_of(const QkArgs& a, int vec) {
-  const int units = (a.dim + 2 * vec - 1) / (2 * vec);
-  return vec == 8 ? (units <= 4 ? 4 : 8) : units <= 8 ? 8 : 16;
+// Halves have to be whole vectors.
+int vec_of(const QkArgs& a, bool bf16, int pairs) {
+  return bf16 && (pairs == kPairNeighbours || a.rotated % 16 == 0) ? 8 : 4;
 }
+int lanes_of(const QkArgs& a, int vec) { return a.dim <= 64 ? 64 / vec : 128 / vec; }
 
-template <class T, int VEC, int LPH, bool NEIGH>
-hipError_t run_qk(const QkArgs& a, bool backward, hipStream_t s) {
-  const int64_t grid = a.side[0].blocks + a.side[1].blocks;
-  return backward ? launch_kernel(qk_norm_kernel<T, VEC, LPH, NEIGH, true>, grid, kThreads, a, s)
-                  : launch_kernel(qk_norm_kernel<T, VEC, LPH, NEIGH, false>, grid, kThreads, a, s);
+template <class T, int VEC, bool NEIGH, int LPH, bool BACK>
+hipError_t run_qk(const QkArgs& a, hipStream_t s) {
+  return a.side[0].weight || a.side[1].weight || a.part
+             ? launch_kernel(qk_norm_kernel<T, VEC, LPH, NEIGH, BACK, true>, a.blocks, kThreads, a, s)
+             : launch_kernel(qk_norm_kernel<T, VEC, LPH, NEIGH, BACK, false>, a.blocks, kThreads, a, s);
 }
 template <class T, int VEC, bool NEIGH>
 hipError_t pick_lanes(const QkArgs& a, bool backward, hipStream_t s) {
-  constexpr int FEW = 32 / VEC;  // 4 lanes of 2 x 8 elements, or 8 of 2 x 4
-  return lanes_of(a, VEC) == FEW ? run_qk<T, VEC, FEW, NEIGH>(a, backward, s)
-                                 : run_qk<T, VEC, 2 * FEW, NEIGH>(a, backward, s);
-}
-template <bool NEIGH>
-hipError_t pick_type(const QkArgs& a, bool bf16, bool backward, hipStream_t s) {
-  if (!bf16) return pick_lanes<float, 4, NEIGH>(a, backward, s);
-  return vec_of(a, bf16) == 8 ? pick_lanes<__bf16, 8, NEIGH>(a, backward, s)
-                              : pick_lanes<__bf16, 4, NEIGH>(a, backward, s);
+  if (a.dim <= 64)
+    return backward ? run_qk<T, VEC, NEIGH, 64 / VEC, true>(a, s) : run_qk<T, VEC, NEIGH, 64 / VEC, false>(a, s);
+  return backward ? run_qk<T, VEC, NEIGH, 128 / VEC, true>(a, s) : run_qk<T, VEC, NEIGH, 128 / VEC, false>(a, s);
 }
 
 }  // namespace
 
-void plan_qk(QkArgs& a, bool bf16, bool backward) {
-  (void)backward;
-  const int tokens = kThreads / lanes_of(a, vec_of(a, bf16));
-  for (QkSide& s : a.side) {
-    s.chunk = s.heads < 8 ? s.heads : 8;
-    if (s.chunk < 1) s.chunk = 1;  // no tokens: no side is filled in
-    const int64_t items = (a.tokens + tokens - 1) / tokens * ((s.heads + s.chunk - 1) / s.chunk);
-    s.blocks = (int)(items < kQkBlocks ? items : kQkBlocks);
-  }
+void plan_qk(QkArgs& a, bool bf16, int pairs) {
+  const int at_once = 64 / lanes_of(a, vec_of(a, bf16, pairs));  // heads that a wave holds
+  a.pair_lanes = 0;
+  while (1 << a.pair_lanes < a.rotated / 2) ++a.pair_lanes;
+  // as many heads of a token at once as leave no more than an eighth of the steps' places empty
+  a.wide_log = 0;
+  while (2 << a.wide_log <= at_once) ++a.wide_log;
+  auto places = [&] {
+    int64_t n = 0;
+    for (const QkSide& s : a.side) n += (int64_t)((s.heads + (1 << a.wide_log) - 1) >> a.wide_log) << a.wide_log;
+    return n;
+  };
+  while (a.wide_log > 0 && places() * 8 > (int64_t)(a.side[0].heads + a.side[1].heads) * 9) --a.wide_log;
+  a.wide = 1 << a.wide_log;
+  const int64_t tokens = (int64_t)(at_once >> a.wide_log) * (kThreads / 64);
+  const int64_t need = (a.tokens + tokens - 1) / tokens;
+  // few blocks: half the work each (2048 tokens of 24 heads of 64 in fp32: 8.7 us forward instead of 10.3); where
+  // the GPU's 1024 places are full, both sides in one block (see the kernel)
+  a.apart = 2 * need <= kQkBlocks;
+  a.blocks = (int)(a.apart ? 2 * need : need < kQkBlocks ? need : kQkBlocks);
 }
 
 hipError_t launch_qk(const QkArgs& a, bool bf16, int pairs, bool backward, hipStream_t s) {
-  return pairs == kPairNeighbours ? pick_type<true>(a, bf16, backward, s) : pick_type<false>(a, bf16, backward, s);
+  const bool wide = vec_of(a, bf16, pairs) == 8;
+  if (pairs == kPairNeighbours)
+    return bf16 ? pick_lanes<__bf16, 8, true>(a, backward, s) : pick_lanes<float, 4, true>(a, backward, s);
+  if (!bf16) return pick_lanes<float, 4, false>(a, backward, s);
+  return wide ? pick_lanes<__bf16, 8, false>(a, backward, s) : pick_lanes<__bf16, 4, false>(a, backward, s);
 }
 hipError_t launch_qk_sum(const QkSumArgs& a, hipStream_t stream) {
-  return launch_kernel(qk_sum_kernel, 2 * ((a.dim + kSumCols - 1) / kSumCols), kSumThreads, a, stream);
+  return launch_kernel(qk_sum_kernel, (2 * a.dim + kSumCols - 1) / kSumCols, kSumThreads, a, stream);
 }
 
 }  // namespace muon
