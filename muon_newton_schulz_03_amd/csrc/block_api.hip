@@ -337,12 +337,12 @@ Area out_area(const muon_embedding_desc* d, const void* p) {
   return area(p, d->tokens, ld_of(d->ld_out, d->cols) * es, 1, 0, d->cols * es);
 }
 
-// The backward call's workspace: sorted entries twice, digit counts, a byte for
-// each row of the table, and two partial rows for each chunk.
+// The backward call's workspace: the sorted list, what sorting it takes, and two
+// partial rows for each chunk.
 EmbedGradArgs embed_layout(const muon_embedding_desc* d, void* workspace, size_t* bytes) {
   EmbedGradArgs a{};
   a.tokens = d->tokens, a.vocab = d->vocab, a.cols = (int32_t)d->cols;
-  plan_embed(a);
+  plan_embed(a, d->table_dtype == MUON_DTYPE_BF16, d->out_dtype == MUON_DTYPE_BF16);
   char* p = (char*)workspace;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -350,10 +350,14 @@ EmbedGradArgs embed_layout(const muon_embedding_desc* d, void* workspace, size_t
     at += align_up(n);
     return q;
   };
-  for (EmbedEntry*& e : a.entry) e = (EmbedEntry*)take((size_t)d->tokens * sizeof(EmbedEntry));
-  a.hist = (uint32_t*)take(((size_t)a.blocks << a.digit) * sizeof(uint32_t));
-  a.present = (uint8_t*)take((size_t)d->vocab);
-  const size_t chunks = ((size_t)d->tokens + kEmbedChunk - 1) / kEmbedChunk;
+  const size_t list = (size_t)d->tokens * sizeof(EmbedEntry);
+  a.sorted = (EmbedEntry*)take(list);
+  if (d->tokens > kOneBlock) {
+    for (int i = 0; i < 2; ++i)
+      if (a.passes > i + 1) a.entry[i] = (EmbedEntry*)take(list);
+    a.hist = (uint32_t*)take(((size_t)a.blocks << a.digit) * sizeof(uint32_t));
+  }
+  const size_t chunks = ((size_t)d->tokens + a.chunk - 1) / a.chunk;
   a.part = (float*)take(chunks * 2 * (size_t)d->cols * sizeof(float));
   *bytes = at;
   return a;

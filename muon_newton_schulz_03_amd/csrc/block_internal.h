@@ -161,18 +161,24 @@ struct EmbedGradArgs {
   int32_t accumulate;
   float scale;
   // workspace
-  EmbedEntry* entry[2];  // tokens each
-  uint32_t* hist;        // [blocks][1 << digit]
-  uint8_t* present;      // vocab
-  float* part;           // [chunks][2][cols]
-  // sort
+  EmbedEntry* sorted;       // the tokens by id
+  EmbedEntry* entry[2];     // between passes: after even ones, after odd ones
+  uint32_t* hist;           // [blocks][1 << digit]
+  float* part;              // [chunks][2][cols]
+  // layout
+  int32_t table_size;       // bytes of the table's elements
   int32_t blocks, segment;  // blocks of a pass, and tokens of each
   int32_t digit, passes;    // bits of a digit
   int32_t pass;             // this launch's
+  int32_t lanes;            // that sum a row's vectors
+  int32_t chunk;            // sorted tokens that a block sums
+  int32_t stream;           // dout is larger than what the caches keep
 };
-constexpr int kEmbedChunk = 32;   // sorted tokens a wave sums
-constexpr int kMaxDigit = 10;
-void plan_embed(EmbedGradArgs& a);
+constexpr int kEmbedEach = 8;         // sorted tokens that a row's lanes sum
+constexpr int kMaxDigit = 9;
+constexpr int64_t kOneBlock = 16384;  // tokens that one block sorts
+// Fills in the layout from tokens, vocab and cols.
+void plan_embed(EmbedGradArgs& a, bool table_bf16, bool out_bf16);
 hipError_t launch_embed_backward(const EmbedGradArgs& a, bool table_bf16, bool out_bf16, hipStream_t stream);
 
 }  // namespace muon

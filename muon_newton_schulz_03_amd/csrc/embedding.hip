@@ -3,7 +3,7 @@
 // Forward: y[t] = scale * table[id_t]; an id outside the table gives a row of zeros.
 // Backward: dtable[v] = scale * sum of dout[t] over the tokens t with id_t = v, in
 // fp32 and in an order that only the ids decide: the tokens are sorted by id
-// (stable radix sort, so in token order within an id), each wave sums a chunk
+// (stable radix sort, so in token order within an id), groups of lanes sum chunks
 // of the sorted list, and ids that reach over a chunk's end are joined in order.
 #include "block_internal.h"
 #include "device_common.h"
@@ -18,13 +18,20 @@ __device__ __forceinline__ uint32_t id_at(const void* ids, bool id64, int64_t t,
   return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
 }
 
+// Orders a wave's LDS accesses, which its lanes make in turn.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------- forward --
 // A block takes a.rows tokens, whose ids it holds in LDS, and its threads the
 // vectors of those rows in turn.
 constexpr int kMaxRows = 256;
 template <class T, class O, bool PART>
 __global__ __launch_bounds__(kThreads) void embed_forward_kernel(EmbedArgs a) {
-  constexpr int VEC = sizeof(T) == 4 && sizeof(O) == 4 ? 4 : 8;
+  constexpr int VEC = sizeof(T) == 4 && sizeof(O) == 4 ? 4 : 8, AHEAD = 4;
   __shared__ uint32_t id[kMaxRows];
   const uint32_t vectors = (uint32_t)(a.cols + VEC - 1) / VEC;
   for (int64_t first = (int64_t)blockIdx.x * a.rows; first < a.tokens; first += (int64_t)gridDim.x * a.rows) {
@@ -32,43 +39,166 @@ __global__ __launch_bounds__(kThreads) void embed_forward_kernel(EmbedArgs a) {
     __syncthreads();  // the ids before have been read
     for (int i = threadIdx.x; i < rows; i += kThreads) id[i] = id_at(a.ids, a.id64, first + i, a.vocab);
     __syncthreads();
-    for (uint32_t j = threadIdx.x; j < rows * vectors; j += kThreads) {
-      const uint32_t r = a.rows == 1 ? 0 : vectors == 1 ? j : __umulhi(j, a.magic);
-      const int c = (int)(j - r * vectors) * VEC, n = PART ? min(a.cols - c, VEC) : VEC;
-      float v[VEC];
-      if (id[r] < (uint32_t)a.vocab) {
-        load_part<T, VEC, PART>((const T*)a.table + id[r] * a.ld_table + c, n, v);
+    const uint32_t count = rows * vectors;
+    for (uint32_t j0 = threadIdx.x; j0 < count; j0 += AHEAD * kThreads) {
+      float v[AHEAD][VEC];
+      uint32_t row[AHEAD];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] *= a.scale;
-      } else {
+      for (int q = 0; q < AHEAD; ++q) {
+        const uint32_t j = j0 + q * kThreads;
+        row[q] = a.rows == 1 ? 0 : vectors == 1 ? j : __umulhi(j, a.magic);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = 0.f;
+        for (int e = 0; e < VEC; ++e) v[q][e] = 0.f;
+        if (j >= count || id[row[q]] >= (uint32_t)a.vocab) continue;
+        const int c = (int)(j - row[q] * vectors) * VEC;
+        load_part<T, VEC, PART>((const T*)a.table + id[row[q]] * a.ld_table + c, PART ? min(a.cols - c, VEC) : VEC, v[q]);
       }
-      store_part<O, VEC, PART>((O*)a.out + (first + r) * a.ld_out + c, n, v);
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) {
+        const uint32_t j = j0 + q * kThreads;
+        if (j >= count) break;
+        const int c = (int)(j - row[q] * vectors) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[q][e] *= a.scale;
+        store_part<O, VEC, PART>((O*)a.out + (first + row[q]) * a.ld_out + c, PART ? min(a.cols - c, VEC) : VEC, v[q]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- zeros --
+// Rows that no token has are zero, so the launches that sort, which leave most
+// of the GPU idle, set the whole gradient to zero in their other blocks: `part`
+// of `parts`.  What the sums write over is written twice, which costs less than
+// knowing it first.
+__device__ __forceinline__ void zero_table(const EmbedGradArgs& a, int es, int64_t block, int64_t blocks, int part,
+                                           int parts) {
+  const bool whole = a.ld_dtable == a.cols;  // one row of everything
+  const int64_t rows = whole ? 1 : a.vocab, bytes = (whole ? a.vocab : 1) * a.cols * es;
+  const int lane = threadIdx.x % 64, waves = blockDim.x / 64;
+  constexpr int kPiece = 64 * 16 * 4;  // of a wave
+  const int64_t pieces = (bytes + kPiece - 1) / kPiece, all = rows * pieces;
+  const int64_t end = all * (part + 1) / parts;
+  for (int64_t i = all * part / parts + block * waves + threadIdx.x / 64; i < end; i += blocks * waves) {
+    const int64_t row = whole ? 0 : i / pieces, at = (whole ? i : i - row * pieces) * kPiece;
+    char* p = (char*)a.dtable + row * a.ld_dtable * es + at;
+    const int64_t n = bytes - at;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int o = (q * 64 + lane) * 16;
+      if (o + 16 <= n) *gv<u32x4_any>(p + o) = u32x4{};
+      else
+        for (int e = o; e < n; e += 2) *gv<uint16_t>(p + e) = 0;
     }
   }
 }
 
 // ------------------------------------------------------------------- sort --
-// One pass sorts by `digit` bits of the id: every block counts its segment's
-// digits, then every block finds its places from all blocks' counts and moves
-// its entries there.  The last pass's output is sorted; the tokens' order is
-// kept among equals.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 
+// The rank of a lane's digit among equal ones of lower lanes, and their number in the wave.
+__device__ __forceinline__ int rank_of(uint32_t d, int bits, bool on, int lane, int& count) {
+  uint64_t same = __ballot(on);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot(d >> b & 1);
+    same &= d >> b & 1 ? set : ~set;
+  }
+  count = __popcll(same);
+  return __popcll(same & ((1ull << lane) - 1));
+}
+
+// Exclusive sums over the block's threads.
+__device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* wave_sum) {
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  uint32_t scan = v;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const uint32_t n = __shfl_up(scan, o);
+    if (lane >= o) scan += n;
+  }
+  if (lane == 63) wave_sum[wave] = scan;
+  __syncthreads();
+  uint32_t lower = scan - v;
+  for (int w = 0; w < wave; ++w) lower += wave_sum[w];
+  return lower;
+}
+
+// Few tokens: one block sorts them in LDS, in as many passes as the ids' bits
+// need.  A wave counts the digits of its own part of the list, so that the block
+// only meets to add the waves' counts and to move the entries.
+template <int ITEMS>
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGradArgs a) {
+  __shared__ EmbedEntry list[ITEMS * kSortThreads];
+  __shared__ uint16_t place[kSortWaves][1 << kMaxDigit];
+  __shared__ uint32_t wave_sum[kSortWaves];
+  if (blockIdx.x > 0) return zero_table(a, a.table_size, blockIdx.x - 1, gridDim.x - 1, 0, 1);
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, bins = 1 << a.digit, n = (int)a.tokens;
+  const int first = wave * ITEMS * 64 + lane;
+  EmbedEntry e[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int at = first + i * 64;
+    e[i] = EmbedEntry{0, (uint32_t)at};
+    if (at < n) e[i].id = id_at(a.ids, a.id64, at, a.vocab);
+  }
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.digit;
+    int rank[ITEMS];
+    for (int i = lane; i < bins; i += 64) place[wave][i] = 0;
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const bool on = first + i * 64 < n;
+      const uint32_t d = e[i].id >> shift & (bins - 1);
+      int count;
+      const int r = rank_of(d, a.digit, on, lane, count), before = place[wave][d];
+      wave_fence();
+      if (on && r == 0) place[wave][d] = (uint16_t)(before + count);
+      wave_fence();
+      rank[i] = before + r;
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    if ((int)threadIdx.x < bins)
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) total += place[w][threadIdx.x];
+    uint32_t base = scan_threads(total, wave_sum);
+    if ((int)threadIdx.x < bins)
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = place[w][threadIdx.x];
+        place[w][threadIdx.x] = (uint16_t)base;
+        base += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (first + i * 64 < n) list[place[wave][e[i].id >> shift & (bins - 1)] + rank[i]] = e[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (first + i * 64 < n) e[i] = list[first + i * 64];
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+    if (first + i * 64 < n) a.sorted[first + i * 64] = e[i];
+}
+
+// More tokens: a pass of two launches for each digit.  Every block counts its
+// segment's digits, then every block finds its places from all blocks' counts
+// and moves its entries there.  The tokens' order is kept among equals.
 __device__ __forceinline__ EmbedEntry entry_at(const EmbedGradArgs& a, int64_t i) {
   if (a.pass == 0) return EmbedEntry{id_at(a.ids, a.id64, i, a.vocab), (uint32_t)i};
   return a.entry[(a.pass + 1) & 1][i];
 }
 
 __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedGradArgs a) {
+  if ((int)blockIdx.x >= a.blocks)
+    return zero_table(a, a.table_size, blockIdx.x - a.blocks, gridDim.x - a.blocks, 2 * a.pass, 2 * a.passes);
   __shared__ uint32_t count[1 << kMaxDigit];
   const int bins = 1 << a.digit;
   for (int i = threadIdx.x; i < bins; i += kSortThreads) count[i] = 0;
-  if (a.pass == 0)
-    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < a.vocab; i += (int64_t)a.blocks * kSortThreads)
-      a.present[i] = 0;
   __syncthreads();
   const int64_t first = (int64_t)blockIdx.x * a.segment, last = min(first + a.segment, a.tokens);
   for (int64_t i = first + threadIdx.x; i < last; i += kSortThreads)
@@ -78,61 +208,56 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedGradArgs
 }
 
 __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedGradArgs a) {
-  __shared__ uint32_t base[1 << kMaxDigit];                // where the digit's next entry goes
-  __shared__ uint16_t place[kSortWaves][1 << kMaxDigit];   // a wave's count of a digit, then its place after base
+  if ((int)blockIdx.x >= a.blocks)
+    return zero_table(a, a.table_size, blockIdx.x - a.blocks, gridDim.x - a.blocks, 2 * a.pass + 1, 2 * a.passes);
+  __shared__ uint32_t base[1 << kMaxDigit];               // where the digit's next entry goes
+  __shared__ uint16_t place[kSortWaves][1 << kMaxDigit];  // a wave's count of a digit, then its place after base
   __shared__ uint32_t wave_sum[kSortWaves];
+  __shared__ uint32_t sums[2][kSortThreads];
   const int bins = 1 << a.digit, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   {
-    // a thread a digit (at most 1024): entries of lower digits, and of this digit in earlier blocks
+    // entries of lower digits, and of the same digit in earlier blocks: kSortThreads / bins threads a digit
+    const int bin = threadIdx.x & (bins - 1), share = threadIdx.x >> a.digit, shares = kSortThreads >> a.digit;
     uint32_t before = 0, total = 0;
-    if ((int)threadIdx.x < bins)
-      for (int b = 0; b < a.blocks; ++b) {
-        const uint32_t n = a.hist[(int64_t)b * bins + threadIdx.x];
-        before += b < (int)blockIdx.x ? n : 0;
-        total += n;
-      }
-    uint32_t scan = total;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-      const uint32_t n = __shfl_up(scan, o);
-      if (lane >= o) scan += n;
+#pragma unroll 16
+    for (int b = share; b < a.blocks; b += shares) {
+      const uint32_t n = a.hist[(int64_t)b * bins + bin];
+      before += b < (int)blockIdx.x ? n : 0;
+      total += n;
     }
-    if (lane == 63) wave_sum[wave] = scan;
+    sums[0][threadIdx.x] = before, sums[1][threadIdx.x] = total;
     __syncthreads();
-    uint32_t lower = scan - total;
-    for (int w = 0; w < wave; ++w) lower += wave_sum[w];
+    before = total = 0;
+    if ((int)threadIdx.x < bins)
+      for (int i = threadIdx.x; i < kSortThreads; i += bins) before += sums[0][i], total += sums[1][i];
+    const uint32_t lower = scan_threads(total, wave_sum);
     if ((int)threadIdx.x < bins) base[threadIdx.x] = lower + before;
   }
+  EmbedEntry* to = a.pass == a.passes - 1 ? a.sorted : a.entry[a.pass & 1];
   const int64_t first = (int64_t)blockIdx.x * a.segment, last = min(first + a.segment, a.tokens);
   for (int64_t at = first; at < last; at += kSortThreads) {
-    __syncthreads();  // base is written; the previous round's places are read
-    for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) place[i / bins][i % bins] = 0;
-    __syncthreads();
     const int64_t i = at + threadIdx.x;
     const bool on = i < last;
     const EmbedEntry e = on ? entry_at(a, i) : EmbedEntry{};
+    for (int b = lane; b < bins; b += 64) place[wave][b] = 0;
+    wave_fence();
     const uint32_t d = e.id >> (a.pass * a.digit) & (bins - 1);
-    uint64_t same = __ballot(on);
-    for (int b = 0; b < a.digit; ++b) {
-      const uint64_t set = __ballot(d >> b & 1);
-      same &= d >> b & 1 ? set : ~set;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (on && rank == 0) place[wave][d] = (uint16_t)__popcll(same);
+    int count;
+    const int rank = rank_of(d, a.digit, on, lane, count);
+    if (on && rank == 0) place[wave][d] = (uint16_t)count;
     __syncthreads();
     uint32_t sum = 0;
-    if ((int)threadIdx.x < bins)
+    if ((int)threadIdx.x < bins) {
+#pragma unroll
       for (int w = 0; w < kSortWaves; ++w) {
         const uint32_t n = place[w][threadIdx.x];
         place[w][threadIdx.x] = (uint16_t)sum;
         sum += n;
       }
-    __syncthreads();
-    if (on) {
-      a.entry[a.pass & 1][base[d] + place[wave][d] + rank] = e;
-      if (a.pass == 0 && e.id < (uint32_t)a.vocab) a.present[e.id] = 1;
     }
     __syncthreads();
+    if (on) to[base[d] + place[wave][d] + rank] = e;
+    __syncthreads();  // base and place have been read
     if ((int)threadIdx.x < bins) base[threadIdx.x] += sum;
   }
 }
@@ -152,110 +277,179 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t id, i
   store_part<T, VEC, PART>(p, n, v);
 }
 
-// A wave sums a chunk of the sorted list over 64 vectors of columns.  An id's
-// run goes to its row of the table if it lies within the chunk; otherwise to
-// part[chunk][0] if it came in from the chunk before, to [1] if it starts here.
-template <class T, class O, bool PART>
-__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a) {
-  constexpr int VEC = kVec<O>, AHEAD = 8;
-  const int lane = threadIdx.x % 64;
-  const int slices = (a.cols + 64 * VEC - 1) / (64 * VEC);
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
-  const int64_t chunk = unit / slices, first = chunk * kEmbedChunk;
-  if (first >= a.tokens) return;
-  const int c = ((int)(unit % slices) * 64 + lane) * VEC, n = min(a.cols - c, VEC);
-  const int count = (int)min((int64_t)kEmbedChunk, a.tokens - first);
-  const EmbedEntry* list = a.entry[(a.passes - 1) & 1];
-  const uint32_t none = 0xFFFFFFFFu;
-  EmbedEntry mine{none, 0};
-  const int64_t i = first - 1 + lane;  // one before the chunk, and one behind
-  if (lane < count + 2 && i >= 0 && i < a.tokens) mine = list[i];
-  float acc[VEC];
+// A vector of a row as it was loaded: whole ones of bf16 stay packed, in half the
+// registers.  Rows of more than the caches keep are read past them (whole
+// vectors): 65536 x 768 in bf16 30 us instead of 35, but 32768 x 128, which the
+// caches hold, 12 instead of 11.
+template <class O, bool PART, bool STREAM>
+struct Held {
+  float v[kVec<O>];
+  __device__ __forceinline__ void load(const O* p, int n) {
+    if constexpr (STREAM) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  uint32_t id = __builtin_amdgcn_readlane(mine.id, 1);
-  bool began = __builtin_amdgcn_readlane(mine.id, 0) == id;  // in the chunk before
-  for (int k = 0; k < count; k += AHEAD) {
-    float v[AHEAD][VEC];
-#pragma unroll
-    for (int q = 0; q < AHEAD; ++q) {
-      if (k + q >= count) break;
-      const uint32_t token = __builtin_amdgcn_readlane(mine.token, k + q + 1);
-      if (n > 0) load_part<O, VEC, PART>((const O*)a.dout + token * a.ld_dout + c, n, v[q]);
+      for (int e = 0; e < kVec<O>; e += 4) {
+        const f32x4 r = __builtin_nontemporal_load(gv<f32x4_any>(p + e));
+        v[e] = r[0], v[e + 1] = r[1], v[e + 2] = r[2], v[e + 3] = r[3];
+      }
+    } else {
+      load_part<O, kVec<O>, PART>(p, n, v);
     }
+  }
+  __device__ __forceinline__ void add_to(float* acc) const {
 #pragma unroll
-    for (int q = 0; q < AHEAD; ++q) {
-      if (k + q >= count) break;
-      if (id == (uint32_t)a.vocab) return;  // sorted last: nothing more counts
+    for (int e = 0; e < kVec<O>; ++e) acc[e] += v[e];
+  }
+};
+template <bool STREAM>
+struct Held<__bf16, false, STREAM> {
+  u32x4 r;
+  __device__ __forceinline__ void load(const __bf16* p, int) {
+    if constexpr (STREAM) r = __builtin_nontemporal_load(gv<u32x4_any>(p));
+    else r = *gv<u32x4_any>(p);
+  }
+  __device__ __forceinline__ void add_to(float* acc) const {
+    float v[8];
+    unpack8_bf16(r, v);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] += v[q][e];
-      const uint32_t next = __builtin_amdgcn_readlane(mine.id, k + q + 2);
-      const bool end = k + q + 1 == count;
-      if (next == id && !end) continue;
-      if (n > 0) {
-        if (began || next == id)
-          store_part<float, VEC, PART>(a.part + (chunk * 2 + (began ? 0 : 1)) * a.cols + c, n, acc);
-        else
-          write_row<T, VEC, PART>(a, id, c, n, acc);
+    for (int e = 0; e < 8; ++e) acc[e] += v[e];
+  }
+};
+
+// A block sums a chunk of the sorted list over LPR vectors of columns: each group
+// of LPR lanes eight entries, whose rows it loads at once.  An id's run that lies
+// within a group goes to its row of the table; parts of longer ones go to LDS,
+// where the group in which a run starts adds the others' (in order).  A run that
+// came in from the chunk before ends in part[chunk][0], one that goes on from
+// here in part[chunk][1].
+template <class T, class O, bool PART, int LPR, bool STREAM>
+__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedGradArgs a) {
+  constexpr int VEC = kVec<O>, GROUPS = kThreads / LPR, EACH = kEmbedEach, CHUNK = GROUPS * EACH;
+  __shared__ EmbedEntry list[CHUNK + 2];  // one entry before and behind the chunk
+  __shared__ __align__(16) float parts[2][GROUPS][LPR * VEC];  // of a group's run that came in, of one that goes on
+  const int u = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  const uint32_t none = (uint32_t)a.vocab;  // ids outside the table are sorted last, and what is behind the list follows
+  const int slices = (a.cols + LPR * VEC - 1) / (LPR * VEC);
+  const int64_t chunks = (a.tokens + CHUNK - 1) / CHUNK;
+  auto came_in = [&](int g) { return list[g * EACH].id == list[g * EACH + 1].id; };
+  auto goes_on = [&](int g) {  // and the run
+    const uint32_t id = list[(g + 1) * EACH].id;
+    return id == list[(g + 1) * EACH + 1].id && id < none;
+  };
+  auto passes = [&](int g) { return goes_on(g) && list[g * EACH + 1].id == list[(g + 1) * EACH].id; };
+  for (int64_t unit = blockIdx.x; unit < chunks * slices; unit += gridDim.x) {
+    const int64_t chunk = unit / slices, first = chunk * CHUNK - 1;
+    const int c = ((int)(unit % slices) * LPR + u) * VEC, n = min(a.cols - c, VEC);
+    __syncthreads();  // the unit before is done
+    for (int k = threadIdx.x; k < CHUNK + 2; k += kThreads)
+      list[k] = first + k >= 0 && first + k < a.tokens ? a.sorted[first + k] : EmbedEntry{none + 1 + (k == 0), 0};
+    __syncthreads();
+    const EmbedEntry* mine = list + group * EACH + 1;
+    Held<O, PART, STREAM> v[EACH];
+    float acc[VEC];
+#pragma unroll
+    for (int q = 0; q < EACH; ++q)
+      if (mine[q].id < none && n > 0) v[q].load((const O*)a.dout + mine[q].token * a.ld_dout + c, n);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+    bool started = !came_in(group);  // the run, in this group
+#pragma unroll
+    for (int q = 0; q < EACH; ++q) {
+      const uint32_t id = mine[q].id, next = mine[q + 1].id;
+      if (id >= none) break;
+      v[q].add_to(acc);
+      if (next == id && q + 1 < EACH) continue;
+      if (!started || next == id) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) parts[started][group][u * VEC + e] = acc[e];
+      } else if (n > 0) {
+        write_row<T, VEC, PART>(a, id, c, n, acc);
       }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-      id = next;
-      began = false;
+      started = true;
+    }
+    __syncthreads();
+    auto add = [&](int g) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] += parts[0][g][u * VEC + e];
+    };
+    if (goes_on(group) && !(came_in(group) && passes(group))) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = parts[1][group][u * VEC + e];
+      int g = group;
+      bool on = true;
+      while (on && ++g < GROUPS) add(g), on = passes(g);
+      if (n > 0) {
+        if (on) store_part<float, VEC, PART>(a.part + (chunk * 2 + 1) * a.cols + c, n, acc);
+        else write_row<T, VEC, PART>(a, mine[EACH - 1].id, c, n, acc);
+      }
+    }
+    if (group == 0 && came_in(0) && mine[0].id < none) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+      int g = 0;
+      do add(g);
+      while (passes(g) && ++g < GROUPS);
+      if (n > 0) store_part<float, VEC, PART>(a.part + chunk * 2 * a.cols + c, n, acc);
     }
   }
 }
 
-// Adds the parts of the ids that reach over chunks: the wave of the chunk where an id's run starts.
-template <class T, class O, bool PART>
+// Adds the parts of the ids that reach over chunks: a block for the chunk where
+// an id's run starts, and a slice of the columns; its groups share the parts
+// between them.
+template <class T, class O, bool PART, int LPR>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a) {
-  constexpr int VEC = kVec<O>;
-  const int lane = threadIdx.x % 64;
-  const int slices = (a.cols + 64 * VEC - 1) / (64 * VEC);
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
-  const int64_t chunk = unit / slices, first = chunk * kEmbedChunk, end = first + kEmbedChunk;
-  if (end >= a.tokens) return;
-  const EmbedEntry* list = a.entry[(a.passes - 1) & 1];
-  const uint32_t id = list[end - 1].id;
-  if (id == (uint32_t)a.vocab || list[end].id != id) return;                   // ends here
-  if (list[first].id == id && first > 0 && list[first - 1].id == id) return;  // came in from before
-  const int c = ((int)(unit % slices) * 64 + lane) * VEC, n = min(a.cols - c, VEC);
-  float acc[VEC], v[VEC];
+  constexpr int VEC = kVec<O>, GROUPS = kThreads / LPR, CHUNK = GROUPS * kEmbedEach;
+  __shared__ __align__(16) float red[GROUPS][LPR * VEC];
+  const int lane = threadIdx.x % 64, u = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  const int slices = (a.cols + LPR * VEC - 1) / (LPR * VEC);
+  for (int64_t unit = blockIdx.x;; unit += gridDim.x) {
+    const int64_t chunk = unit / slices, first = chunk * CHUNK, end = first + CHUNK;
+    if (end >= a.tokens) return;
+    const uint32_t before = first > 0 ? a.sorted[first - 1].id : 0xFFFFFFFFu, start = a.sorted[first].id,
+                   id = a.sorted[end - 1].id, next = a.sorted[end].id;
+    if (id == (uint32_t)a.vocab || next != id || (start == id && before == id)) continue;  // not the first of several
+    int64_t parts = 1;
+    for (;; parts += 64) {
+      const int64_t i = (chunk + parts + lane) * CHUNK;
+      const uint64_t on = __ballot(i < a.tokens && a.sorted[i].id == id);
+      if (~on) {
+        parts += __builtin_ctzll(~on);
+        break;
+      }
+    }
+    const int c = ((int)(unit % slices) * LPR + u) * VEC, n = min(a.cols - c, VEC);
+    float acc[VEC], v[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  if (n > 0) load_part<float, VEC, PART>(a.part + (chunk * 2 + 1) * a.cols + c, n, acc);
-  for (int64_t at = chunk + 1;; at += 64) {
-    const int64_t i = (at + lane) * kEmbedChunk;
-    const uint64_t on = __ballot(i < a.tokens && list[i].id == id);
-    const int more = __builtin_ctzll(~on | 1ull << 63);
-    const int parts = on == ~0ull ? 64 : more;
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
     if (n > 0)
-      for (int k = 0; k < parts; ++k) {
-        load_part<float, VEC, PART>(a.part + (at + k) * 2 * a.cols + c, n, v);
+#pragma unroll 8
+      for (int64_t k = group; k < parts; k += GROUPS) {
+        load_part<float, VEC, PART>(a.part + ((chunk + k) * 2 + (k == 0 ? 1 : 0)) * a.cols + c, n, v);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[e] += v[e];
       }
-    if (parts < 64) break;
+    __syncthreads();  // the unit before has been read
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) red[group][u * VEC + e] = acc[e];
+    __syncthreads();
+    if (group == 0 && n > 0) {
+      for (int g = 1; g < GROUPS && g < parts; ++g)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += red[g][u * VEC + e];
+      write_row<T, VEC, PART>(a, id, c, n, acc);
+    }
   }
-  if (n > 0) write_row<T, VEC, PART>(a, id, c, n, acc);
 }
 
-// Zeros in the rows that no token has: a wave a row.
-template <class T>
-__global__ __launch_bounds__(kThreads) void embed_zero_kernel(EmbedGradArgs a) {
-  constexpr int VEC = kVec<T>;
-  const int lane = threadIdx.x % 64;
-  const float zero[VEC] = {};
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64; row < a.vocab;
-       row += (int64_t)gridDim.x * (kThreads / 64)) {
-    if (a.tokens && a.present[row]) continue;
-    T* p = (T*)a.dtable + row * a.ld_dtable;
-    for (int c = lane * VEC; c < a.cols; c += 64 * VEC) store_part<T, VEC, true>(p + c, min(a.cols - c, VEC), zero);
-  }
+// The gradient of no tokens.
+__global__ __launch_bounds__(kSortThreads) void embed_zero_kernel(EmbedGradArgs a) {
+  zero_table(a, a.table_size, blockIdx.x, gridDim.x, 0, 1);
 }
 
 // ----------------------------------------------------------------- launch --
-constexpr int64_t kForwardBlocks = 1 << 20;  // what is left is taken in turn: a launch holds fewer than 2^32 threads
+constexpr int64_t kMostBlocks = 1 << 20;  // what is left is taken in turn: a launch holds fewer than 2^32 threads
 template <class T, class O>
 hipError_t run_forward(const EmbedArgs& args, hipStream_t s) {
   constexpr int VEC = sizeof(T) == 4 && sizeof(O) == 4 ? 4 : 8;
@@ -266,39 +460,66 @@ hipError_t run_forward(const EmbedArgs& args, hipStream_t s) {
   if (a.rows > kMaxRows) a.rows = kMaxRows;
   a.magic = (uint32_t)(((1ull << 32) + vectors - 1) / vectors);
   const int64_t blocks = (a.tokens + a.rows - 1) / a.rows;
-  const int64_t grid = blocks < kForwardBlocks ? blocks : kForwardBlocks;
+  const int64_t grid = blocks < kMostBlocks ? blocks : kMostBlocks;
   return a.cols % VEC ? launch_kernel(embed_forward_kernel<T, O, true>, grid, kThreads, a, s)
                       : launch_kernel(embed_forward_kernel<T, O, false>, grid, kThreads, a, s);
 }
 
-template <class T, class O, bool PART>
-hipError_t run_backward(EmbedGradArgs a, hipStream_t s) {
-  hipError_t e = hipSuccess;
-  if (a.tokens) {
-    for (a.pass = 0; a.pass < a.passes && e == hipSuccess; ++a.pass) {
-      e = launch_kernel(embed_count_kernel, a.blocks, kSortThreads, a, s);
-      if (e == hipSuccess) e = launch_kernel(embed_move_kernel, a.blocks, kSortThreads, a, s);
-    }
-    const int64_t chunks = (a.tokens + kEmbedChunk - 1) / kEmbedChunk;
-    const int64_t slices = (a.cols + 64 * kVec<O> - 1) / (64 * kVec<O>);
-    const int64_t grid = (chunks * slices + kThreads / 64 - 1) / (kThreads / 64);
-    if (e == hipSuccess) e = launch_kernel(embed_sum_kernel<T, O, PART>, grid, kThreads, a, s);
-    if (e == hipSuccess) e = launch_kernel(embed_join_kernel<T, O, PART>, grid, kThreads, a, s);
+// Blocks that set a launch's share of the table to zero: up to two for each CU, 64 KiB at least for each.
+int64_t zero_blocks(const EmbedGradArgs& a, int launches) {
+  if (a.accumulate) return 0;
+  const int64_t need = (a.vocab * a.cols * a.table_size / launches + 65535) / 65536;
+  return need < 512 ? need : 512;
+}
+
+hipError_t run_sort(EmbedGradArgs a, hipStream_t s) {
+  if (!a.tokens) {
+    const int64_t grid = zero_blocks(a, 1);
+    return grid ? launch_kernel(embed_zero_kernel, grid, kSortThreads, a, s) : hipSuccess;
   }
-  if (e == hipSuccess && !a.accumulate) {
-    const int64_t need = (a.vocab + kThreads / 64 - 1) / (kThreads / 64);
-    e = launch_kernel(embed_zero_kernel<T>, need < 4096 ? need : 4096, kThreads, a, s);
+  if (a.tokens <= 4 * kSortThreads) return launch_kernel(embed_sort_kernel<4>, 1 + zero_blocks(a, 1), kSortThreads, a, s);
+  if (a.tokens <= kOneBlock) return launch_kernel(embed_sort_kernel<16>, 1 + zero_blocks(a, 1), kSortThreads, a, s);
+  const int64_t grid = a.blocks + zero_blocks(a, 2 * a.passes);
+  hipError_t e = hipSuccess;
+  for (a.pass = 0; a.pass < a.passes && e == hipSuccess; ++a.pass) {
+    e = launch_kernel(embed_count_kernel, grid, kSortThreads, a, s);
+    if (e == hipSuccess) e = launch_kernel(embed_move_kernel, grid, kSortThreads, a, s);
   }
   return e;
 }
+
+template <class T, class O, bool PART, int LPR>
+hipError_t run_sums(const EmbedGradArgs& a, hipStream_t s) {
+  constexpr int CHUNK = kThreads / LPR * kEmbedEach;
+  const int64_t chunks = (a.tokens + CHUNK - 1) / CHUNK, slices = (a.cols + LPR * kVec<O> - 1) / (LPR * kVec<O>);
+  auto grid = [](int64_t units) { return units < kMostBlocks ? units : kMostBlocks; };
+  hipError_t e = a.stream && !PART
+                     ? launch_kernel(embed_sum_kernel<T, O, PART, LPR, !PART>, grid(chunks * slices), kThreads, a, s)
+                     : launch_kernel(embed_sum_kernel<T, O, PART, LPR, false>, grid(chunks * slices), kThreads, a, s);
+  if (e == hipSuccess && chunks > 1)
+    e = launch_kernel(embed_join_kernel<T, O, PART, LPR>, grid((chunks - 1) * slices), kThreads, a, s);
+  return e;
+}
+template <class T, class O, bool PART>
+hipError_t pick_lanes(const EmbedGradArgs& a, hipStream_t s) {
+  hipError_t e = run_sort(a, s);
+  if (e != hipSuccess || !a.tokens) return e;
+  switch (a.lanes) {
+    case 64: return run_sums<T, O, PART, 64>(a, s);
+    case 32: return run_sums<T, O, PART, 32>(a, s);
+    case 16: return run_sums<T, O, PART, 16>(a, s);
+    default: return run_sums<T, O, PART, 8>(a, s);
+  }
+}
 template <class T, class O>
 hipError_t pick_part(const EmbedGradArgs& a, hipStream_t s) {
-  return a.cols % kVec<O> ? run_backward<T, O, true>(a, s) : run_backward<T, O, false>(a, s);
+  return a.cols % kVec<O> ? pick_lanes<T, O, true>(a, s) : pick_lanes<T, O, false>(a, s);
 }
 
 }  // namespace
 
-void plan_embed(EmbedGradArgs& a) {
+void plan_embed(EmbedGradArgs& a, bool table_bf16, bool out_bf16) {
+  a.table_size = table_bf16 ? 2 : 4;
   const int64_t want = (a.tokens + kSortThreads - 1) / kSortThreads;
   const int64_t blocks = want < 1 ? 1 : want < 256 ? want : 256;
   const int64_t each = (a.tokens + blocks - 1) / blocks;
@@ -308,6 +529,12 @@ void plan_embed(EmbedGradArgs& a) {
   while (bits < 31 && a.vocab >> bits) ++bits;  // ids 0 .. vocab
   a.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   a.digit = (bits + a.passes - 1) / a.passes;
+  // the most lanes a row of which no more than an eighth stand idle
+  const int vectors = (a.cols + (out_bf16 ? 7 : 3)) / (out_bf16 ? 8 : 4);
+  a.lanes = 64;
+  while (a.lanes > 8 && (vectors + a.lanes - 1) / a.lanes * a.lanes * 8 > vectors * 9) a.lanes /= 2;
+  a.chunk = kThreads / a.lanes * kEmbedEach;
+  a.stream = a.tokens * a.cols * (out_bf16 ? 2 : 4) >= (int64_t)32 << 20;
 }
 
 hipError_t launch_embed_forward(const EmbedArgs& a, bool table_bf16, bool out_bf16, hipStream_t s) {
