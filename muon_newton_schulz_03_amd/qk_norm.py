@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._lib import QkNormDesc, RotationDesc
+from ._lib import Heads, QkNormDesc, RotationDesc
 from .block import _DTYPES, _check, _given, _heads, _On, _param, _recorded, _refuse_recorded, _stream, _written
 from .embedding import _INDEX
 
@@ -52,25 +52,35 @@ class Rotation:
         return f"Rotation({self.dim}, frequencies={self.frequencies}, pairs={self.pairs!r})"
 
 
+_DIMS = "{} must have shape (tokens, heads, head_dim)"
+
+
 def _inputs(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps):
     """The descriptor and pointers that both calls share, after their checks."""
     for name, t in (("q", q), ("k", k)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} is not a device tensor")
-        if t.dim() != 3:
-            raise ValueError(f"{name} must have shape (tokens, heads, head_dim)")
     dtype, dev, qs, ks = q.dtype, q.device, q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3:
+        raise ValueError(_DIMS.format("q" if len(qs) != 3 else "k"))
     if dtype not in _DTYPES:
         raise ValueError("q must be float32 or bfloat16")
-    if ks[0] != qs[0] or ks[2] != qs[2]:
-        raise ValueError(f"k has shape {tuple(ks)}, which does not go with q's {tuple(qs)}")
-    if rotation is not None and not isinstance(rotation, Rotation):
-        raise ValueError("rotation must be a Rotation or None")
     tokens, heads, dim = qs
+    if ks[0] != tokens or ks[2] != dim:
+        raise ValueError(f"k has shape {tuple(ks)}, which does not go with q's {tuple(qs)}")
+    if rotation is None:
+        turn = None
+    elif isinstance(rotation, Rotation):
+        turn = ctypes.byref(rotation._desc)
+    else:
+        raise ValueError("rotation must be a Rotation or None")
     hq, hk = _heads(q, "q", dev, dtype, qs), _heads(k, "k", dev, dtype, ks)
-    pt, wq = _param(q_weight, "q_weight", dim, dev, None)
-    pt, wk = _param(k_weight, "k_weight", dim, dev, pt)
-    cu, seqs, pos, index = None, 0, None, _lib.MUON_INDEX_I32
+    pt = wq = wk = cu = pos = None
+    seqs, index = 0, _lib.MUON_INDEX_I32
+    if q_weight is not None:
+        pt, wq = _param(q_weight, "q_weight", dim, dev, None)
+    if k_weight is not None:
+        pt, wk = _param(k_weight, "k_weight", dim, dev, pt)
     if cu_seqlens is not None:
         _check(cu_seqlens, "cu_seqlens", dev, torch.int32)
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or not cu_seqlens.is_contiguous():
@@ -85,7 +95,16 @@ def _inputs(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps):
         pos, index = positions.data_ptr(), _INDEX[positions.dtype]
     d = QkNormDesc(tokens, seqs, heads, ks[1], dim, _DTYPES[dtype],
                    _lib.MUON_DTYPE_F32 if pt is None else _DTYPES[pt], index, eps, 0)
-    return d, None if rotation is None else ctypes.byref(rotation._desc), cu, pos, hq, hk, wq, wk
+    return ctypes.byref(d), turn, cu, pos, hq, hk, wq, wk
+
+
+def _output(like, given, name):
+    """A result in the shape of `like`, and its descriptor: a new one, or the given one after its checks."""
+    shape = like.shape
+    if given is None:
+        new = like.new_empty(shape)
+        return new, Heads(new.data_ptr(), shape[1] * shape[2], shape[2])
+    return given, _heads(given, name, like.device, like.dtype, shape)
 
 
 def qk_norm_forward(q: torch.Tensor, k: torch.Tensor, rotation: Optional[Rotation] = None, *,
@@ -104,7 +123,7 @@ def qk_norm_forward(q: torch.Tensor, k: torch.Tensor, rotation: Optional[Rotatio
     cu_seqlens are zero in results that this call allocates and left as they
     were in those given.
     """
-    if _recorded(q, k, q_weight) or _recorded(k_weight, None, None):
+    if _recorded(q, k, q_weight) or k_weight is not None and _recorded(k_weight, None, None):
         _refuse_recorded(q_out=q_out, k_out=k_out)
         return _QkNorm.apply(q, k, q_weight, k_weight, rotation, cu_seqlens, positions, eps)
     return _forward(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps, q_out, k_out)
@@ -112,17 +131,16 @@ def qk_norm_forward(q: torch.Tensor, k: torch.Tensor, rotation: Optional[Rotatio
 
 def _forward(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps, q_out=None, k_out=None):
     lib = _lib.load()
-    d, rot, cu, pos, hq, hk, wq, wk = _inputs(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps)
-    dev, flags, given = q.device, 0, None if q_out is None and k_out is None else (q_out, k_out)
-    with _On(dev):
-        if q_out is None:
-            q_out, flags = q.new_empty(q.shape), flags | _lib.QK_ZERO_Q
-        if k_out is None:
-            k_out, flags = q.new_empty(k.shape), flags | _lib.QK_ZERO_K
-        oq, ok = _heads(q_out, "q_out", dev, q.dtype, q.shape), _heads(k_out, "k_out", dev, q.dtype, k.shape)
+    d, turn, cu, pos, hq, hk, wq, wk = _inputs(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps)
+    given = None if q_out is None and k_out is None else (q_out, k_out)
+    flags = (q_out is None) * _lib.QK_ZERO_Q | (k_out is None) * _lib.QK_ZERO_K
+    index = q.device.index
+    with _On(q.device):
+        q_out, oq = _output(q, q_out, "q_out")
+        k_out, ok = _output(k, k_out, "k_out")
         given = given and _given(*given)
-        _lib.check(lib.muon_qk_norm_forward(ctypes.byref(d), rot, cu, pos, ctypes.byref(hq), ctypes.byref(hk), wq, wk,
-                                            ctypes.byref(oq), ctypes.byref(ok), flags, _stream(dev.index)))
+        _lib.check(lib.muon_qk_norm_forward(d, turn, cu, pos, ctypes.byref(hq), ctypes.byref(hk), wq, wk,
+                                            ctypes.byref(oq), ctypes.byref(ok), flags, _stream(index)))
     if given:
         _written(given)
     return q_out, k_out
@@ -145,31 +163,31 @@ def qk_norm_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     allocates and left as they were in those given.
     """
     lib = _lib.load()
-    d, rot, cu, pos, hq, hk, wq, wk = _inputs(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps)
-    dev, dtype, flags, given = q.device, q.dtype, 0, (dq, dk)
+    d, turn, cu, pos, hq, hk, wq, wk = _inputs(q, k, rotation, q_weight, k_weight, cu_seqlens, positions, eps)
+    dev, dtype = q.device, q.dtype
     gq, gk = _heads(dq_out, "dq_out", dev, dtype, q.shape), _heads(dk_out, "dk_out", dev, dtype, k.shape)
+    given = None if dq is None and dk is None else (dq, dk)
+    flags = (dq is None) * _lib.QK_ZERO_Q | (dk is None) * _lib.QK_ZERO_K
     with _On(dev):
-        if dq is None:
-            dq, flags = q.new_empty(q.shape), flags | _lib.QK_ZERO_Q
-        if dk is None:
-            dk, flags = q.new_empty(k.shape), flags | _lib.QK_ZERO_K
-        oq, ok = _heads(dq, "dq", dev, dtype, q.shape), _heads(dk, "dk", dev, dtype, k.shape)
-        given = _given(*given)
-        dwq = dwk = ws = None
+        dq, oq = _output(q, dq, "dq")
+        dk, ok = _output(k, dk, "dk")
+        given = given and _given(*given)
+        dwq = dwk = pwq = pwk = ws = None
         nbytes = 0
         if wq is not None if need_q_weight is None else need_q_weight:
             dwq = q.new_empty(q.shape[2], dtype=torch.float32)
+            pwq = dwq.data_ptr()
         if wk is not None if need_k_weight is None else need_k_weight:
             dwk = q.new_empty(q.shape[2], dtype=torch.float32)
-        if dwq is not None or dwk is not None:
-            nbytes = lib.muon_qk_norm_workspace_size(ctypes.byref(d))
+            pwk = dwk.data_ptr()
+        if pwq or pwk:
+            nbytes = lib.muon_qk_norm_workspace_size(d)
             if nbytes == 0:
                 raise _lib.MuonError(_lib.MUON_E_INVAL, _lib.last_error())
             ws = q.new_empty(nbytes, dtype=torch.uint8)
         _lib.check(lib.muon_qk_norm_backward(
-            ctypes.byref(d), rot, cu, pos, ctypes.byref(gq), ctypes.byref(gk), ctypes.byref(hq), ctypes.byref(hk),
-            wq, wk, ctypes.byref(oq), ctypes.byref(ok), None if dwq is None else dwq.data_ptr(),
-            None if dwk is None else dwk.data_ptr(), flags, None if ws is None else ws.data_ptr(), nbytes,
+            d, turn, cu, pos, ctypes.byref(gq), ctypes.byref(gk), ctypes.byref(hq), ctypes.byref(hk), wq, wk,
+            ctypes.byref(oq), ctypes.byref(ok), pwq, pwk, flags, None if ws is None else ws.data_ptr(), nbytes,
             _stream(dev.index)))
     if given:
         _written(given)
