@@ -300,7 +300,7 @@ int muon_fused_limits(muon_plan* plan, int32_t spin_limit, int32_t dep_bias);
  * whose output or workspace shares memory with another of its operands is
  * refused (MUON_E_INVAL).  Operands may lie between each other's rows in one
  * buffer if they step through it alike.
- * Results are bitwise reproducible (no atomics).  NaN and infinities are not
+ * Results are bitwise reproducible (no floating-point atomics).  NaN and infinities are not
  * inspected; they propagate as in the formulas. */
 
 /* Layer norm of `rows` rows of `cols` elements (cols <= 2^20).  Leading

@@ -97,6 +97,8 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, vocab: int, *, sca
         raise ValueError("dout must be float32 or bfloat16")
     if dout.dim() != ids.dim() + 1 or dout.shape[:-1] != ids.shape:
         raise ValueError(f"dout has shape {tuple(dout.shape)}, which does not go with ids of {tuple(ids.shape)}")
+    if not vocab > 0:
+        raise ValueError("vocab must be positive")
     _, cols, ld_out = _rows(dout, "dout")
     given, ld = None, 0
     with _On(dev):
