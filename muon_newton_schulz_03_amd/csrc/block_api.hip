@@ -350,6 +350,8 @@ EmbedGradArgs embed_layout(const muon_embedding_desc* d, void* workspace, size_t
     at += align_up(n);
     return q;
   };
+  *bytes = kAlign;  // never 0, which means an error
+  if (a.direct) return a;
   const size_t list = (size_t)d->tokens * sizeof(EmbedEntry);
   a.sorted = (EmbedEntry*)take(list);
   if (d->tokens > kOneBlock) {
@@ -359,7 +361,7 @@ EmbedGradArgs embed_layout(const muon_embedding_desc* d, void* workspace, size_t
   }
   const size_t chunks = ((size_t)d->tokens + a.chunk - 1) / a.chunk;
   a.part = (float*)take(chunks * 2 * (size_t)d->cols * sizeof(float));
-  *bytes = at;
+  *bytes += at;
   return a;
 }
 
@@ -394,7 +396,7 @@ size_t muon_embedding_workspace_size(const muon_embedding_desc* d) {
   if (check_embedding(d)) return 0;
   size_t bytes;
   embed_layout(d, nullptr, &bytes);
-  return bytes + kAlign;
+  return bytes;
 }
 
 int muon_embedding_backward(const muon_embedding_desc* d, const void* ids, const void* dout, void* dtable,
