@@ -13,6 +13,12 @@
 // 2^64 is exact, so up to position 2^32 only the fraction's own rounding, 2^-65,
 // counts, and the eighth of a turn that is left for sine and cosine is exact to
 // 2^-31 turns.
+//
+// Bound by memory: each operand moves once a call.  65536 tokens of 24 heads of
+// 64 in bf16 forward 83 us (403 MB, 4.8 TB/s, where a copy of 1 GiB reaches 5.1
+// and vector operations take 42% of the time); 16384 tokens of 40 heads of 128
+// forward 62 us and backward 108 (335 and 503 MB, 5.4 and 4.7 TB/s), and 5 us for
+// the weight gradients' second stage.
 #include "block_internal.h"
 #include "device_common.h"
 

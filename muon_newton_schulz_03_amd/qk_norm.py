@@ -48,8 +48,15 @@ class Rotation:
         self._host = (ctypes.c_double * max(1, dim // 2))(*self.frequencies)
         self._desc = RotationDesc(self._host, dim, _PAIRS[pairs])
 
+    def __reduce__(self):  # copied and saved with the model that holds it; the host array is not
+        return _rebuilt, (self.dim, self.frequencies, self.pairs)
+
     def __repr__(self):
         return f"Rotation({self.dim}, frequencies={self.frequencies}, pairs={self.pairs!r})"
+
+
+def _rebuilt(dim, frequencies, pairs):
+    return Rotation(dim, frequencies=frequencies, pairs=pairs)
 
 
 _DIMS = "{} must have shape (tokens, heads, head_dim)"

@@ -332,6 +332,22 @@ def test_embedding_nan_stays_in_its_row():
     assert bad[ids[1234]] and bad.sum() == 1
 
 
+@pytest.mark.parametrize("T", [300, 3000, 30000])
+def test_embedding_padding_may_hold_anything(T):
+    """What stands in dout at ids outside the table is not read; without any other id the gradient is zero."""
+    ids = randint(0, 40, (T,), 397)
+    pad = torch.arange(T) % 3 == 0
+    dout = randn((T, 24), 398)
+    clean = torch.where(pad[:, None], 0.0, dout)
+    want = lib.embedding_backward(clean.to(DEV), torch.where(pad, -1, ids).to(DEV), 40)
+    dout[pad] = float("nan")
+    for outside in (-1, 40, 1 << 40):
+        got = lib.embedding_backward(dout.to(DEV), torch.where(pad, outside, ids).to(DEV), 40)
+        assert torch.equal(got, want)
+    dout.fill_(float("inf"))
+    assert (lib.embedding_backward(dout.to(DEV), torch.full((T,), -5, device=DEV), 40) == 0).all()
+
+
 def test_embedding_gradient_is_reproducible():
     ids = randint(0, 3000, (50000,), 395).to(DEV)
     dout = randn((50000, 96), 396, BF).to(DEV)

@@ -2,9 +2,11 @@
 
 Every call here is rejected by argument checks before any HIP call, or is host-only.
 """
+import copy
 import ctypes
 import math
 import os
+import pickle
 
 import pytest
 import torch
@@ -153,6 +155,9 @@ def test_rotation_arguments():
     assert r.frequencies == tuple(100.0 ** (-i / 8) for i in range(8)) and r.pairs == "halves"
     assert pkg.Rotation(8, frequencies=torch.zeros(4)).frequencies == (0.0,) * 4
     assert pkg.Rotation(0).frequencies == ()
+    for again in (copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert (again.dim, again.frequencies, again.pairs) == (r.dim, r.frequencies, r.pairs)
+        assert again._desc.dim == 16 and again._desc.frequencies[1] == r.frequencies[1]
     for bad in (dict(dim=12), dict(dim=-8), dict(dim=8, pairs="both"), dict(dim=8, frequencies=[1.0]),
                 dict(dim=8, base=0.0), dict(dim=8, base=-2.0)):
         with pytest.raises(ValueError):
