@@ -225,6 +225,9 @@ def test_embedding_widths(C, table_dtype, dtype):
     say(f"[gpu] embedding width {C} {table_dtype} -> {dtype}")
     ids = randint(-1, 42, (133,), 300, torch.int32)  # -1 and 41 lie outside
     worst = embed_case(ids, 41, C, table_dtype, dtype, 301, scale=1.7)
+    ids = randint(-1, 3000, (1100,), 302)  # sorted, with runs over the chunks' ends
+    ids[100:400] = 1234
+    worst = max(worst, embed_case(ids, 2999, C, table_dtype, dtype, 303, scale=0.6))
     say(f"[gpu]   worst error {worst:.3f} of its bound")
 
 
@@ -245,10 +248,13 @@ def test_embedding_long_runs(T):
     embed_case(torch.arange(T) // 33, 70000 // 33 + 1, 16, BF, F32, 324)
 
 
-@pytest.mark.parametrize("T,V,C", [(300001, 3001, 8), (1100000, 50304, 4), (5000, (1 << 20) - 1, 4),
-                                   (5000, 1 << 20, 4), (3000, (1 << 22) + 5, 2), (500, (1 << 29) + 3, 1)])
+@pytest.mark.parametrize("T,V,C", [(300001, 3001, 8), (1100000, 50304, 4), (6000, 200, 8), (6000, 1, 8),
+                                   (6000, 511, 8), (6000, 512, 8), (9000, (1 << 18) - 1, 4), (9000, 1 << 18, 4),
+                                   (7000, (1 << 22) + 5, 2), (7000, (1 << 28) + 3, 1), (5000, (1 << 20) - 1, 4),
+                                   (5000, 1 << 20, 4), (3000, (1 << 22) + 5, 2), (3000, (1 << 28) + 3, 1),
+                                   (500, (1 << 29) + 3, 1)])
 def test_embedding_sort_passes(T, V, C):
-    """Segments of several rounds, and one to three passes over the ids' bits."""
+    """Segments of several rounds, and one to four passes over the ids' bits, in one block and in several."""
     say(f"[gpu] embedding sort T={T} V={V}")
     if V < 1 << 25:
         embed_case(randint(0, V, (T,), 330), V, C, F32, F32, 331)
@@ -260,6 +266,16 @@ def test_embedding_sort_passes(T, V, C):
     want = torch.zeros(rows.numel(), C, dtype=torch.float64).index_add_(0, at, dout.double())
     assert (g[rows.to(DEV)].double().cpu() - want).abs().max() < 1e-5
     assert int((g != 0).sum()) == int((want != 0).sum())
+
+
+@pytest.mark.parametrize("T,C,dtype", [(70000, 512, BF), (50000, 768, BF), (140000, 128, BF), (270000, 64, BF),
+                                       (40000, 264, F32), (36000, 260, F32)])
+def test_embedding_of_more_than_the_caches_hold(T, C, dtype):
+    """Gradients of 32 MiB and more are read past the caches."""
+    say(f"[gpu] embedding {T}x{C} {dtype}")
+    ids = randint(0, 700, (T,), 335)
+    ids[randint(0, T, (T // 3,), 336)] = 77
+    embed_case(ids, 700, C, dtype, dtype, 337)
 
 
 def test_embedding_ids_outside():
@@ -294,6 +310,14 @@ def test_embedding_shapes_and_strides():
         lib.embedding_backward(dout, ids.reshape(-1).to(DEV), 50, dtable=grad[:, cols])
         assert torch.equal(grad[:, cols], want)
         assert (grad[:, :off] == 3).all() and (grad[:, off + 64:] == 3).all()
+        for T in (2000, 20000):  # each way to sort
+            many, dout = randint(0, 60, (T,), 364).to(DEV), randn((T, 120), 365, dtype).to(DEV)[:, cols]
+            many = torch.where(many < 50, many, -1)
+            want = lib.embedding_backward(dout.contiguous(), many, 70, dtype=dtype)
+            grad = torch.full((70, 120), 3.0, dtype=dtype, device=DEV)
+            lib.embedding_backward(dout, many, 70, dtable=grad[:, cols])
+            assert torch.equal(grad[:, cols], want) and (want[50:] == 0).all()
+            assert (grad[:, :off] == 3).all() and (grad[:, off + 64:] == 3).all()
 
 
 def test_embedding_without_tokens():
@@ -322,6 +346,12 @@ def test_embedding_offsets_past_32_bits():
     assert torch.equal(lib.embedding_backward(far, ids, 5, dtype=BF), want)
     lib.embedding_backward(src, ids, 5, dtable=far)
     assert torch.equal(far, want)
+    for T in (3000, 20000):
+        many, dout = randint(0, 4, (T,), 381).to(DEV), randn((T, cols), 382, BF).to(DEV)
+        want = lib.embedding_backward(dout, many, 5, dtype=BF)
+        far.fill_(7.0)
+        lib.embedding_backward(dout, many, 5, dtable=far)
+        assert torch.equal(far, want)
 
 
 def test_embedding_nan_stays_in_its_row():
