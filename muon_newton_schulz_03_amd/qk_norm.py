@@ -109,7 +109,7 @@ def _output(like, given, name):
     """A result in the shape of `like`, and its descriptor: a new one, or the given one after its checks."""
     shape = like.shape
     if given is None:
-        new = like.new_empty(shape)
+        new = torch.empty_like(like, memory_format=torch.contiguous_format)  # 1.2 us, like.new_empty(shape) 1.6
         return new, Heads(new.data_ptr(), shape[1] * shape[2], shape[2])
     return given, _heads(given, name, like.device, like.dtype, shape)
 
