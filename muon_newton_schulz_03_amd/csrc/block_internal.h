@@ -177,6 +177,7 @@ struct EmbedGradArgs {
   int32_t stream;           // dout is larger than what the caches keep
 };
 constexpr int kEmbedEach = 8;         // sorted tokens that a row's lanes sum
+constexpr int kFewEach = 4;           // the same while blocks are few
 constexpr int kDirect = 512;          // tokens that the one launch takes
 constexpr int kDirectRows = 1024;     // of a block
 constexpr int kMaxDigit = 9;
