@@ -13,6 +13,7 @@
 #include "block_internal.h"
 #include "device_common.h"
 #include "row_vectors.h"
+#include "wave.h"
 
 namespace muon {
 namespace {
@@ -21,13 +22,6 @@ namespace {
 __device__ __forceinline__ uint32_t id_at(const void* ids, bool id64, int64_t t, int64_t vocab) {
   const int64_t id = id64 ? *gv<int64_t>((const int64_t*)ids + t) : *gv<int32_t>((const int32_t*)ids + t);
   return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
-}
-
-// Orders a wave's LDS accesses, which its lanes make in turn.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // ---------------------------------------------------------------- forward --

@@ -21,6 +21,7 @@
 // the weight gradients' second stage.
 #include "block_internal.h"
 #include "device_common.h"
+#include "wave.h"
 
 namespace muon {
 namespace {
@@ -216,6 +217,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_kernel(QkArgs a) {
   else fetch(keys{}, first, 0);
   for (; first < a.tokens; first += stride) {
     if (pairs) {
+      wave_fence();  // the angles before have been read
       if (a.cu && !a.positions && first < last && (first < span.start || first >= span.end))
         span = span_of(a.cu, a.seqs, first);
       for (int t = pair_token; t < tokens && first + t < last; t += 64 >> a.pair_lanes) {
@@ -231,9 +233,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_kernel(QkArgs a) {
           c[0] = cosine, c[TABLE] = sine, c[2 * TABLE] = -sine;
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_fence();
     }
     float cs[ANGLES], sn[ANGLES];
     if (turns) read_angles<ANGLES>(cosines, cs), read_angles<ANGLES>(sines, sn);
