@@ -181,7 +181,7 @@ constexpr int kFewEach = 4;           // the same while blocks are few
 constexpr int kDirect = 512;          // tokens that the one launch takes
 constexpr int kDirectRows = 1024;     // of a block
 constexpr int kMaxDigit = 9;
-constexpr int64_t kOneBlock = 5120;    // tokens that one block sorts
+constexpr int64_t kOneBlock = 8192;    // tokens that one block sorts
 // Fills in the layout from tokens, vocab and cols.
 void plan_embed(EmbedGradArgs& a, bool table_bf16, bool out_bf16);
 hipError_t launch_embed_backward(const EmbedGradArgs& a, bool table_bf16, bool out_bf16, hipStream_t stream);

@@ -97,14 +97,17 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 
 // The rank of a lane's digit among equal ones of lower lanes, and their number in the wave.
-__device__ __forceinline__ int rank_of(uint32_t d, int bits, bool on, int lane, int& count) {
-  uint64_t same = __ballot(on);
+__device__ __forceinline__ int rank_of(uint32_t d, int bits, bool on, int& count) {
+  const uint64_t all = __ballot(on);
+  uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
   for (int b = 0; b < bits; ++b) {
-    const uint64_t set = __ballot(d >> b & 1);
-    same &= d >> b & 1 ? set : ~set;
+    const uint32_t bit = (uint32_t)__builtin_amdgcn_sbfe((int)d, b, 1);  // 0 or all ones
+    const uint64_t set = __ballot(bit);
+    lo &= ~((uint32_t)set ^ bit);
+    hi &= ~((uint32_t)(set >> 32) ^ bit);
   }
-  count = __popcll(same);
-  return __popcll(same & ((1ull << lane) - 1));
+  count = __popc(lo) + __popc(hi);
+  return __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
 }
 
 // Exclusive sums over the block's threads.
@@ -126,9 +129,9 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* wave_sum)
 // Not many tokens: one block sorts them in LDS, in as many passes as the ids' bits
 // need.  A wave counts the digits of its own part of the list, so that the block
 // only meets to add the waves' counts and to move the entries.  The whole
-// backward pass of 4096 tokens takes 26 us for 50304 x 768 in bf16 and 22 for
-// 5000 x 64 (35 and 26 with the launches below), of 8192 tokens 34 and 29 (37
-// and 27).
+// backward pass of 4096 tokens takes 23 us for 50304 x 768 in bf16 and 20 for
+// 5000 x 64 (35 and 26 with the launches below), of 8192 tokens 30 and 24 (35
+// and 25; for a small table of 64 x 768 22 and 19).
 template <int ITEMS>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGradArgs a) {
   __shared__ EmbedEntry list[ITEMS * kSortThreads];
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGradArgs 
       const bool on = first + i * 64 < n;
       const uint32_t d = e[i].id >> shift & (bins - 1);
       int count;
-      const int r = rank_of(d, a.digit, on, lane, count), before = place[wave][d];
+      const int r = rank_of(d, a.digit, on, count), before = place[wave][d];
       wave_fence();
       if (on && r == 0) place[wave][d] = (uint16_t)(before + count);
       wave_fence();
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedGradArgs 
     wave_fence();
     const uint32_t d = e.id >> (a.pass * a.digit) & (bins - 1);
     int count;
-    const int rank = rank_of(d, a.digit, on, lane, count);
+    const int rank = rank_of(d, a.digit, on, count);
     if (on && rank == 0) place[wave][d] = (uint16_t)count;
     __syncthreads();
     uint32_t sum = 0;
@@ -452,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a) {
 // above), and write every row, sum or zero.  A row of many tokens is shared by
 // all groups of lanes.  Alone on the GPU, against the launches that sort: 512
 // tokens for 50304 x 768 in bf16 17 us instead of 22, for 5000 x 256 7 instead
-// of 17, for 64 x 768 8 instead of 13; all of them of one id 34 instead of 23
+// of 17, for 64 x 768 8 instead of 12; all of them of one id 34 instead of 23
 // (50304 x 768; 256 tokens 24 instead of 22).  1024 tokens took 19 instead of 23
 // and 61 instead of 23, so they are sorted.
 constexpr int kDirectItems = kDirect / kThreads, kDirectWaves = kThreads / 64, kShared = 8;
@@ -485,7 +488,7 @@ __global__ __launch_bounds__(kThreads) void embed_direct_kernel(EmbedGradArgs a)
 #pragma unroll
   for (int i = 0; i < kDirectItems; ++i) {
     int count;
-    const int r = rank_of(row[i], a.digit, on[i], lane, count), before = place[wave][row[i]];
+    const int r = rank_of(row[i], a.digit, on[i], count), before = place[wave][row[i]];
     wave_fence();
     if (on[i] && r == 0) place[wave][row[i]] = (uint16_t)(before + count);
     wave_fence();
