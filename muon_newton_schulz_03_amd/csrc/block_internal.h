@@ -173,7 +173,6 @@ struct EmbedGradArgs {
   int32_t lanes;            // that sum a row's vectors
   int32_t chunk;            // sorted tokens that a block sums
   int32_t direct;           // one launch does it all; segment: rows of a block
-  uint32_t magic;           // and 2^32 / 16-byte units of a row, rounded up
   int32_t stream;           // dout is larger than what the caches keep
 };
 constexpr int kEmbedEach = 8;         // sorted tokens that a row's lanes sum

@@ -19,9 +19,14 @@ namespace muon {
 namespace {
 
 // The id of a token as the table's row, or `vocab` outside it.
-__device__ __forceinline__ uint32_t id_at(const void* ids, bool id64, int64_t t, int64_t vocab) {
-  const int64_t id = id64 ? *gv<int64_t>((const int64_t*)ids + t) : *gv<int32_t>((const int32_t*)ids + t);
+__device__ __forceinline__ int64_t load_id(const void* ids, bool id64, int64_t t) {
+  return id64 ? *gv<int64_t>((const int64_t*)ids + t) : *gv<int32_t>((const int32_t*)ids + t);
+}
+__device__ __forceinline__ uint32_t row_of(int64_t id, int64_t vocab) {
   return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
+}
+__device__ __forceinline__ uint32_t id_at(const void* ids, bool id64, int64_t t, int64_t vocab) {
+  return row_of(load_id(ids, id64, t), vocab);
 }
 
 // ---------------------------------------------------------------- forward --
@@ -452,12 +457,12 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a) {
 // ------------------------------------------------------------------ direct --
 // Few tokens: one launch, whose blocks each take some rows of the table, look
 // through all ids for those of their rows (stably sorted by row in LDS, as
-// above), and write every row, sum or zero.  A row of many tokens is shared by
+// above), and write every row, zeros first.  A row of many tokens is shared by
 // all groups of lanes.  Alone on the GPU, against the launches that sort: 512
-// tokens for 50304 x 768 in bf16 17 us instead of 22, for 5000 x 256 7 instead
-// of 17, for 64 x 768 8 instead of 12; all of them of one id 34 instead of 23
-// (50304 x 768; 256 tokens 24 instead of 22).  1024 tokens took 19 instead of 23
-// and 61 instead of 23, so they are sorted.
+// tokens for 50304 x 768 in bf16 16 us instead of 22, for 5000 x 256 7 instead
+// of 17, for 64 x 768 8 instead of 12; all of them of one id 32 instead of 23
+// (50304 x 768; 256 tokens 22 and 22).  1024 tokens took 19 instead of 23 and 61
+// instead of 23, so they are sorted.
 constexpr int kDirectItems = kDirect / kThreads, kDirectWaves = kThreads / 64, kShared = 8;
 template <class T, class O, bool PART, int LPR>
 __global__ __launch_bounds__(kThreads) void embed_direct_kernel(EmbedGradArgs a) {
@@ -472,12 +477,33 @@ __global__ __launch_bounds__(kThreads) void embed_direct_kernel(EmbedGradArgs a)
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, u = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const int n = (int)a.tokens, rows = (int)min((int64_t)a.segment, a.vocab - (int64_t)blockIdx.x * a.segment);
   const uint32_t row0 = blockIdx.x * (uint32_t)a.segment;
+  int64_t id[kDirectItems];
+#pragma unroll
+  for (int i = 0; i < kDirectItems; ++i) {
+    const int t = (wave * kDirectItems + i) * 64 + lane;
+    id[i] = t < n ? load_id(a.ids, a.id64, t) : -1;
+  }
+  if (!a.accumulate) {  // all of the block's rows, while the ids are on their way; sums are written over them
+    char* p = (char*)a.dtable + row0 * a.ld_dtable * a.table_size;
+    const int64_t width = (int64_t)a.cols * a.table_size, bytes = rows * width;
+    if (a.ld_dtable == a.cols) {
+      for (int64_t o = threadIdx.x * 16; o < bytes; o += kThreads * 16) {
+        if (o + 16 <= bytes) *gv<u32x4_any>(p + o) = u32x4{};
+        else
+          for (int64_t e = o; e < bytes; e += 2) *gv<uint16_t>(p + e) = 0;
+      }
+    } else {
+      const float zero[VEC] = {};
+      for (int r = group; r < rows; r += GROUPS)
+        for (int c = u * VEC; c < a.cols; c += LPR * VEC)
+          store_part<T, VEC, PART>((T*)p + r * a.ld_dtable + c, min(a.cols - c, VEC), zero);
+    }
+  }
   uint32_t row[kDirectItems];
   bool on[kDirectItems];
 #pragma unroll
   for (int i = 0; i < kDirectItems; ++i) {
-    const int t = (wave * kDirectItems + i) * 64 + lane;
-    row[i] = t < n ? id_at(a.ids, a.id64, t, a.vocab) - row0 : 0xFFFFFFFFu;
+    row[i] = row_of(id[i], a.vocab) - row0;
     on[i] = row[i] < (uint32_t)rows;
     row[i] = on[i] ? row[i] : 0;
   }
@@ -526,22 +552,6 @@ __global__ __launch_bounds__(kThreads) void embed_direct_kernel(EmbedGradArgs a)
     const int count = start[r + 1] - start[r];
     if (count > 0 && count <= kShared) present[atomicAdd(&counts[0], 1)] = (uint16_t)r;
     if (count > kShared) present[kDirectRows - 1 - atomicAdd(&counts[1], 1)] = (uint16_t)r;
-  }
-  if (!a.accumulate) {
-    char* p = (char*)a.dtable + row0 * a.ld_dtable * a.table_size;
-    const uint32_t units = (uint32_t)(a.cols * a.table_size) / 16;  // of a row
-    if (a.ld_dtable == a.cols && a.cols * a.table_size % 16 == 0) {
-      for (uint32_t i = threadIdx.x; i < rows * units; i += kThreads) {
-        const uint32_t r = a.segment == 1 ? 0 : units == 1 ? i : __umulhi(i, a.magic);
-        if (start[r] == start[r + 1]) *gv<u32x4_any>(p + (int64_t)i * 16) = u32x4{};
-      }
-    } else {
-      const float zero[VEC] = {};
-      for (int r = group; r < rows; r += GROUPS)
-        if (start[r] == start[r + 1])
-          for (int c = u * VEC; c < a.cols; c += LPR * VEC)
-            store_part<T, VEC, PART>((T*)p + r * a.ld_dtable + c, min(a.cols - c, VEC), zero);
-    }
   }
   __syncthreads();
   auto sum = [&](auto ahead, int from, int to, int step, int c, int cn, float* acc) {
@@ -701,8 +711,6 @@ void plan_embed(EmbedGradArgs& a, bool table_bf16, bool out_bf16) {
     a.segment = (int32_t)rows;
     a.digit = 0;
     while (1 << a.digit < rows) ++a.digit;
-    const int64_t units = row / 16;  // a block's, below 4096, are divided exactly by the multiplication
-    a.magic = units > 1 ? (uint32_t)(((1ull << 32) + units - 1) / units) : 0;
   }
   a.stream = a.tokens * a.cols * (out_bf16 ? 2 : 4) >= (int64_t)32 << 20;  // 1024 blocks of 8 at least
 }
