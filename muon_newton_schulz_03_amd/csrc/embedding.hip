@@ -698,7 +698,7 @@ void plan_embed(EmbedGradArgs& a, bool table_bf16, bool out_bf16) {
   while (a.lanes > 8 && (vectors + a.lanes - 1) / a.lanes * a.lanes * 8 > vectors * 9) a.lanes /= 2;
   // fewer entries a group while blocks are few: sums of 32768 x 128 in bf16 8.6 us instead of 11.0 (256 blocks of 8),
   // of 4099 x 1001 in fp32 8.0 instead of 10.5 (516); but with the runs' joining, 42 us instead of 37 for 65536 x 768
-  // (3072)
+  // (over 3000)
   a.chunk = kThreads / a.lanes * kEmbedEach;
   const int64_t blocks8 = (a.tokens + a.chunk - 1) / a.chunk * ((vectors + a.lanes - 1) / a.lanes);
   if (blocks8 < 1024) a.chunk = kThreads / a.lanes * kFewEach;
