@@ -38,6 +38,11 @@ def _table(t: torch.Tensor, name: str, device) -> Tuple[int, int, int]:
     return _rows(t, name)
 
 
+def _check_scale(scale) -> None:
+    if isinstance(scale, torch.Tensor):  # no gradient would reach it, and the call would wait for one on a device
+        raise ValueError("scale must be a number, not a tensor (multiply the result by it instead)")
+
+
 def embedding_forward(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
                       dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """scale * table[ids], of shape ids.shape + (columns,).
@@ -45,8 +50,10 @@ def embedding_forward(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 
     table (vocab, columns): float32 or bfloat16, with contiguous columns.
     ids: int32 or int64; one outside [0, vocab), such as the padding of a
     batch, has a row of zeros and passes no gradient on.  dtype: the result's,
-    default the table's (or that of a given out).
+    default the table's (or that of a given out).  scale: a number; a tensor
+    is refused, for its gradient would be lost.
     """
+    _check_scale(scale)
     if _recorded(table, None, None):
         _refuse_recorded(out=out)
         return _Embedding.apply(table, ids, scale, dtype)
@@ -89,6 +96,7 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, vocab: int, *, sca
     and values alone.  A given dtable (whose dtype counts then) is overwritten,
     or with accumulate added to, where rows that no id names stay as they are.
     """
+    _check_scale(scale)
     lib = _lib.load()
     _check_ids(ids)
     dev = ids.device
