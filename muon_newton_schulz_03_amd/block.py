@@ -7,7 +7,8 @@ the forward calls take part: y and out carry a graph whose backward pass is
 the backward call.  It is differentiable once, and the statistics (mean, rstd,
 lse) pass no gradient on: one that arrives there raises.  The backward calls
 themselves return plain values.  A given output cannot be recorded, so with
-such inputs it is refused.
+such inputs it is refused, and so is a tensor that requires grad in place of a
+number (eps, scale).
 A recorded backward pass may be captured in a graph under torch's own rule:
 forward and backward in the same capture, and no eager graph of the same
 leaves alive (torch ends the process otherwise, whatever the operators).
@@ -109,6 +110,12 @@ def _recorded(a, b, c) -> bool:
         isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in (a, b, c))
 
 
+def _refuse_number(name: str, value) -> None:
+    """A tensor in place of a number: refused where torch would differentiate with respect to it."""
+    if _recorded(value, None, None):
+        raise ValueError(f"{name} is a number, which no gradient reaches (detach it)")
+
+
 def _refuse_recorded(**given) -> None:
     for name, t in given.items():
         if t is not None:
@@ -141,6 +148,8 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, b
     x: float32 or bfloat16, with a contiguous last dimension and rows of one
     stride.  weight and bias (one dtype, float32 or bfloat16) may be None.
     """
+    if isinstance(eps, torch.Tensor):
+        _refuse_number("eps", eps)
     if _recorded(x, weight, bias):
         _refuse_recorded(out=out)
         return _LayerNorm.apply(x, weight, bias, eps)
@@ -307,6 +316,8 @@ def packed_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     the backward call.  Rows behind the last sequence are zero in results that
     this call allocates and left as they were in those given.
     """
+    if isinstance(scale, torch.Tensor):
+        _refuse_number("scale", scale)
     if _recorded(q, k, v):
         _refuse_recorded(out=out, lse=lse)
         return _Attention.apply(q, k, v, cu_seqlens, scale)

@@ -16,7 +16,8 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import Heads, QkNormDesc, RotationDesc
-from .block import _DTYPES, _check, _given, _heads, _On, _param, _recorded, _refuse_recorded, _stream, _written
+from .block import (_DTYPES, _check, _given, _heads, _On, _param, _recorded, _refuse_number, _refuse_recorded, _stream,
+                    _written)
 from .embedding import _INDEX
 
 _PAIRS = {"halves": _lib.PAIRS_HALVES, "neighbours": _lib.PAIRS_NEIGHBOURS}
@@ -43,6 +44,8 @@ class Rotation:
             frequencies = [base ** (-2 * i / dim) for i in range(dim // 2)]
         if len(frequencies) != dim // 2:
             raise ValueError(f"{dim} elements need {dim // 2} frequencies, not {len(frequencies)}")
+        if any(_recorded(f, None, None) for f in frequencies):
+            raise ValueError("base and frequencies are numbers, which no gradient reaches (detach them)")
         self.dim, self.pairs = dim, pairs
         self.frequencies = tuple(float(f) for f in frequencies)
         self._host = (ctypes.c_double * max(1, dim // 2))(*self.frequencies)
@@ -130,6 +133,8 @@ def qk_norm_forward(q: torch.Tensor, k: torch.Tensor, rotation: Optional[Rotatio
     cu_seqlens are zero in results that this call allocates and left as they
     were in those given.
     """
+    if isinstance(eps, torch.Tensor):
+        _refuse_number("eps", eps)
     if _recorded(q, k, q_weight) or k_weight is not None and _recorded(k_weight, None, None):
         _refuse_recorded(q_out=q_out, k_out=k_out)
         return _QkNorm.apply(q, k, q_weight, k_weight, rotation, cu_seqlens, positions, eps)

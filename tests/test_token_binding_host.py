@@ -23,3 +23,36 @@ def test_a_tensor_is_no_scale_of_the_embedding(grad):
             pkg.embedding_forward(table, ids, scale=s)
         with pytest.raises(ValueError, match="device tensor"):
             pkg.embedding_backward(dout, ids, 4, scale=s)
+
+
+def test_gradients_of_numbers_are_not_lost():
+    """A tensor that records gradients, where the operators take a number, is refused; a plain one counts as its value."""
+    q, x, cu = torch.zeros(4, 2, 8), torch.zeros(4, 8), torch.zeros(2, dtype=torch.int32)
+    g = torch.full((), 0.5, requires_grad=True)
+    for name, call in (("eps", lambda t: pkg.qk_norm_forward(q, q, eps=t)),
+                       ("eps", lambda t: pkg.layer_norm_forward(x, eps=t)),
+                       ("scale", lambda t: pkg.packed_attention_forward(q, q, q, cu, scale=t))):
+        for t in (g, g * 2, torch.nn.Parameter(torch.ones(()))):
+            with pytest.raises(ValueError, match=f"{name} is a number"):
+                call(t)
+            with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):
+                call(t)
+        for t in (0.5, g.detach()):
+            with pytest.raises(ValueError, match="device tensor"):
+                call(t)
+        with torch.autograd.forward_ad.dual_level(), pytest.raises(ValueError, match=f"{name} is a number"):
+            call(torch.autograd.forward_ad.make_dual(g.detach(), torch.ones(())))
+
+
+def test_gradients_of_frequencies_are_not_lost():
+    f = torch.tensor([1.0, 0.5, 0.25, 0.125], requires_grad=True)
+    for bad in (dict(frequencies=f), dict(frequencies=list(f)), dict(frequencies=[1.0, 0.5, 0.25, f[3]]),
+                dict(base=torch.tensor(100.0, requires_grad=True))):
+        with pytest.raises(ValueError, match="frequencies are numbers"):
+            pkg.Rotation(8, **bad)
+        with torch.no_grad():
+            pkg.Rotation(8, **bad)
+    want = tuple(f.tolist())
+    assert pkg.Rotation(8, frequencies=f.detach()).frequencies == want
+    assert pkg.Rotation(8, frequencies=want).frequencies == want
+    assert pkg.Rotation(0, base=torch.tensor(100.0, requires_grad=True)).frequencies == ()
