@@ -283,6 +283,16 @@ def _heads(t: torch.Tensor, name: str, device, dtype, shape) -> Heads:
     return Heads(t.data_ptr(), token, head)
 
 
+def _readable(g: torch.Tensor) -> torch.Tensor:
+    """A (tokens, heads, head_dim) gradient as the library reads it: itself, or a copy where its strides or its start do
+    not suit (the gradient of a sum, for example, repeats one value; one through torch.cat may start anywhere)."""
+    token, head, elem = g.stride()
+    size = g.element_size()
+    if elem != 1 or token > 1 << 24 or head > 1 << 31 or any([n % 16 for n in (token * size, head * size, g.data_ptr())]):
+        return g.clone(memory_format=torch.contiguous_format)
+    return g
+
+
 def _attention(q, k, v, cu_seqlens, scale):
     for name, t in (("q", q), ("k", k)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -408,9 +418,5 @@ class _Attention(torch.autograd.Function):
         if dout is None:
             return None, None, None, None, None
         q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
-        token, head, elem = dout.stride()
-        size = dout.element_size()
-        if elem != 1 or token > 1 << 24 or any(n % 16 for n in (token * size, head * size, dout.data_ptr())):
-            dout = dout.contiguous()  # the gradient of a sum, for example, repeats one value
-        grads = packed_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=ctx.scale)
+        grads = packed_attention_backward(_readable(dout), q, k, v, out, lse, cu_seqlens, scale=ctx.scale)
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None)

@@ -16,8 +16,8 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import Heads, QkNormDesc, RotationDesc
-from .block import (_DTYPES, _check, _given, _heads, _On, _param, _recorded, _refuse_number, _refuse_recorded, _stream,
-                    _written)
+from .block import (_DTYPES, _check, _given, _heads, _On, _param, _readable, _recorded, _refuse_number, _refuse_recorded,
+                    _stream, _written)
 from .embedding import _INDEX
 
 _PAIRS = {"halves": _lib.PAIRS_HALVES, "neighbours": _lib.PAIRS_NEIGHBOURS}
@@ -206,13 +206,6 @@ def qk_norm_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     return dq, dk, dwq, dwk
 
 
-def _usable(t: torch.Tensor) -> bool:
-    """Whether the library takes this gradient's strides as they are."""
-    token, head, elem = t.stride()
-    size = t.element_size()
-    return elem == 1 and token <= 1 << 24 and not any(n % 16 for n in (token * size, head * size, t.data_ptr()))
-
-
 class _QkNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, rotation, cu_seqlens, positions, eps):
@@ -227,10 +220,8 @@ class _QkNorm(torch.autograd.Function):
         q, k, q_weight, k_weight, cu_seqlens, positions = ctx.saved_tensors
         rotation, eps = ctx.how
         need = ctx.needs_input_grad
-        # the gradient of a sum, for example, repeats one value
-        dq_out, dk_out = (g if _usable(g) else g.contiguous() for g in (dq_out, dk_out))
-        dq, dk, dwq, dwk = qk_norm_backward(dq_out, dk_out, q, k, rotation, q_weight=q_weight, k_weight=k_weight,
-                                            cu_seqlens=cu_seqlens, positions=positions, eps=eps,
+        dq, dk, dwq, dwk = qk_norm_backward(_readable(dq_out), _readable(dk_out), q, k, rotation, q_weight=q_weight,
+                                            k_weight=k_weight, cu_seqlens=cu_seqlens, positions=positions, eps=eps,
                                             need_q_weight=need[2], need_k_weight=need[3])
         dwq, dwk = (g if g is None else g.to(w.dtype) for g, w in ((dwq, q_weight), (dwk, k_weight)))
         return dq if need[0] else None, dk if need[1] else None, dwq, dwk, None, None, None, None

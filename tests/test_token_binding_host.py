@@ -56,3 +56,25 @@ def test_gradients_of_frequencies_are_not_lost():
     assert pkg.Rotation(8, frequencies=f.detach()).frequencies == want
     assert pkg.Rotation(8, frequencies=want).frequencies == want
     assert pkg.Rotation(0, base=torch.tensor(100.0, requires_grad=True)).frequencies == ()
+
+
+def test_gradients_are_read_as_they_are_or_copied():
+    """What the attention's and the query/key norm's backward pass reads starts, and steps, at multiples of 16 bytes."""
+    from muon_newton_schulz_03_amd.block import _readable
+
+    def fits(t):
+        return t.stride(2) == 1 and not any(n * t.element_size() % 16 for n in t.stride()[:2]) and t.data_ptr() % 16 == 0
+
+    for dtype in (torch.float32, torch.bfloat16):
+        flat = torch.arange(8 + 5 * 3 * 8).to(dtype)
+        flat = flat[(-flat.data_ptr() // flat.element_size()) % 8:]  # at a multiple of 16 bytes
+        whole, wide = flat[:120].view(5, 3, 8), torch.ones(5, 3, 24, dtype=dtype)
+        for t in (whole, wide[..., 8:16], whole.transpose(0, 1).contiguous().transpose(0, 1), whole[:, :1].expand(5, 3, 8),
+                  whole[:1].expand(5, 3, 8), whole[:0]):
+            assert _readable(t) is t
+        for t in (flat[1:121].view(5, 3, 8), wide[..., 1:9], torch.ones((), dtype=dtype).expand(5, 3, 8),
+                  whole.transpose(1, 2).contiguous().transpose(1, 2), flat[3:11].view(1, 1, 8),
+                  torch.ones(5, 3, 9, dtype=dtype)[..., :8]):
+            got = _readable(t)
+            assert torch.equal(got, t) and got.is_contiguous() and fits(got) and got.data_ptr() != t.data_ptr()
+    assert flat[1:121].view(5, 3, 8).is_contiguous()  # and yet does not start there
