@@ -3,7 +3,11 @@ out."""
 import pytest
 import torch
 
+import block_reference as B
 import muon_newton_schulz_03_amd as lib
+import token_reference as R
+import token_sums as S
+from muon_harness import say
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -40,3 +44,75 @@ def test_recorded_gradients_may_start_anywhere(dtype, off):
     leaves = [t.clone().requires_grad_(True) for t in (qn, kn, v)]
     lib.packed_attention_forward(*leaves, cu)[0].backward(dq)
     assert all(torch.equal(t.grad, w) for t, w in zip(leaves, want))
+
+
+# --------------------------------------------------------------- sums of many terms --
+@pytest.mark.parametrize("cols,dtype,tokens", [(64, BF, 70000), (128, BF, 140000), (256, BF, 70000), (512, BF, 70000),
+                                               (505, BF, 70000), (33, BF, 70000), (40, F32, 270000), (9, F32, 70000),
+                                               (128, F32, 70000), (256, F32, 40000)])
+def test_embedding_sums_of_integers_are_exact(cols, dtype, tokens):
+    """Every lane layout, 4 and 8 entries a group, streamed or not: no token of a run over many chunks is lost or added
+    twice, whatever the chunk in which it starts or ends."""
+    dout = S.small_integers((tokens, cols), 20, dtype)
+    dev = dout.to(DEV)
+    for i, (_, before, behind) in enumerate(S.RUNS):
+        say(f"[gpu] embedding sums {tokens}x{cols} {dtype}: {before} entries before the run, {behind} behind it")
+        ids = S.run_ids(tokens, before, behind, 30 + i)
+        want = S.embedding_sums(ids, dout, 41)
+        for index in (torch.int32, torch.int64):
+            got = lib.embedding_backward(dev, ids.to(index).to(DEV), 41, scale=0.5)
+            assert torch.equal(got.cpu(), want.float() * 0.5)
+        low = lib.embedding_backward(dev, ids.to(DEV), 41, dtype=BF, scale=-2.0)
+        assert torch.equal(low.cpu(), (want.float() * -2.0).to(BF))  # the exact sum, rounded once
+        old = S.small_integers((41, cols), 40 + i, F32)
+        got = old.to(DEV)
+        lib.embedding_backward(dev, ids.to(DEV), 41, dtable=got, accumulate=True)
+        assert torch.equal(got.cpu(), S.embedding_sums(ids, dout, 41, old).float())
+
+
+@pytest.mark.parametrize("tokens", [600, 3000, 8192, 8193, 20000])
+def test_embedding_sums_of_integers_over_many_rows(tokens):
+    """Runs of every length at once, in one block's sort and in several blocks'."""
+    g = torch.Generator().manual_seed(50)
+    for cols, dtype in ((24, BF), (136, BF), (768, BF), (20, F32), (1001, F32)):
+        say(f"[gpu] embedding sums of rows {tokens}x{cols} {dtype}")
+        ids = (torch.rand(tokens, generator=g) ** 6 * 4000).long() - 1  # -1 is padding
+        dout = S.small_integers((tokens, cols), 51, dtype)
+        dev = dout.to(DEV)
+        dev[ids.to(DEV) < 0] = float("nan")
+        want = S.embedding_sums(ids, dout, 4000)
+        assert torch.equal(lib.embedding_backward(dev, ids.to(DEV), 4000).cpu(), want.float())
+
+
+@pytest.mark.parametrize("tokens,heads,kv_heads,dim", S.DW_CASES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weight_gradients_of_integers_are_exact(tokens, heads, kv_heads, dim, dtype):
+    """Heads of ones and minus ones have r = 1, so with integer gradients and no turn every sum is exact."""
+    x = S.small_integers((tokens, heads + kv_heads, dim), 60, dtype, top=1)
+    dy = S.small_integers(x.shape, 61, dtype)
+    dev, ddy = x.to(DEV), dy.to(DEV)
+    still = [None] + [lib.Rotation(dim, frequencies=[0.0] * (dim // 2), pairs=p) for p in ("halves", "neighbours")]
+    for used in (tokens, tokens - 1, tokens // 2 + 1):
+        cu = None if used == tokens else torch.tensor([0, used // 3, used], dtype=torch.int32, device=DEV)
+        terms = (x[:used].long() * dy[:used].long())
+        want = terms[:, :heads].sum((0, 1)).float(), terms[:, heads:].sum((0, 1)).float()
+        for rotation in still:
+            got = lib.qk_norm_backward(ddy[:, :heads], ddy[:, heads:], dev[:, :heads], dev[:, heads:], rotation,
+                                       cu_seqlens=cu, eps=0.0, need_q_weight=True, need_k_weight=True)[2:]
+            assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1]), (used, rotation)
+
+
+@pytest.mark.parametrize("case", range(len(S.DW_CASES)))
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weight_gradients_within_their_depth(case, dtype):
+    """Turned heads of every scale: as far off as the additions that a term goes through, not as their number."""
+    T, H, G, D = S.DW_CASES[case]
+    f = [0.9 ** i for i in range(D // 2)]
+    turns, rot = R.angles(range(T), f), lib.Rotation(D, frequencies=f)
+    (q, gq), (k, gk) = S.dw_inputs(T, H, D, dtype, 10 + case), S.dw_inputs(T, G, D, dtype, 70 + case)
+    got = lib.qk_norm_backward(gq.to(DEV), gk.to(DEV), q.to(DEV), k.to(DEV), rot, need_q_weight=True,
+                               need_k_weight=True)[2:]
+    for name, dw, x, dy in (("dq_weight", got[0], q, gq), ("dk_weight", got[1], k, gk)):
+        depth = S.dw_depth(T, x.shape[1], D, 8 if dtype == BF else 4)
+        worst = B.check(name, dw, *S.dw_bound(x, None, turns, D, "halves", 1e-6, dy, depth))
+        say(f"[gpu] {name} {T}x{x.shape[1]}x{D} {dtype}: depth {depth}, worst error {worst:.3f} of its bound")
