@@ -116,3 +116,68 @@ def test_weight_gradients_within_their_depth(case, dtype):
         depth = S.dw_depth(T, x.shape[1], D, 8 if dtype == BF else 4)
         worst = B.check(name, dw, *S.dw_bound(x, None, turns, D, "halves", 1e-6, dy, depth))
         say(f"[gpu] {name} {T}x{x.shape[1]}x{D} {dtype}: depth {depth}, worst error {worst:.3f} of its bound")
+
+
+# --------------------------------------------------------------- few tokens, rows of many --
+def crowded(tokens, vocab, rows, seed):
+    """Ids of which many fall on neighbouring rows: with `rows` rows a block, 40, 1, 8, 9 and 200 on the first three, a
+    middle and the last row of one block, 17 and 9 on the first and last row of the table's last, partial block (9 where
+    that is one row)."""
+    at, end = 3 * rows, (vocab - 1) // rows * rows
+    assert rows >= 5 and end > at + rows and vocab - end < rows
+    counts = {at: 40, at + 1: 1, at + 2: 8, at + rows // 2 + 1: 9, at + rows - 1: 200, end: 17, vocab - 1: 9}
+    ids = torch.cat([torch.full((n,), v) for v, n in counts.items()])
+    g = torch.Generator().manual_seed(seed)
+    rest = torch.randint(-2, vocab + 2, (tokens - len(ids),), generator=g)  # some outside the table
+    return torch.cat([ids, rest])[torch.randperm(tokens, generator=g)]
+
+
+# columns and dtype of the gradient, and the lanes of a row that go with them; 64 KiB of the table a block, but at least
+# 512 blocks
+CROWDED = [(64, BF, 8), (72, BF, 8), (33, BF, 8), (128, BF, 16), (256, BF, 32), (768, BF, 32), (505, BF, 64), (512, BF, 64),
+           (32, F32, 8), (61, F32, 16), (128, F32, 32), (768, F32, 64), (1001, F32, 64)]
+
+
+@pytest.mark.parametrize("cols,dtype,lanes", CROWDED)
+@pytest.mark.parametrize("vocab", [5000, 50257])
+def test_embedding_gradient_of_few_tokens_on_neighbouring_rows(cols, dtype, lanes, vocab):
+    """Rows of more than 8 tokens, several in a block and beside rows of fewer, and both sides of the rule: 512 tokens
+    go in one launch, 513 are sorted."""
+    say(f"[gpu] crowded rows {vocab}x{cols} {dtype}, {lanes} lanes")
+    for table in (BF, F32):
+        size = 2 if table == BF else 4
+        rows = min(65536 // (cols * size), vocab // 512, 1024)
+        for tokens in (511, 512, 513):
+            ids = crowded(tokens, vocab, rows, tokens)
+            dout = S.small_integers((tokens, cols), 80, dtype)
+            known = (ids >= 0) & (ids < vocab)
+            at, back = torch.unique(ids[known], return_inverse=True)
+            total = torch.zeros(len(at), cols, dtype=torch.int64).index_add_(0, back, dout[known].long())
+            dev, ddev = ids.to(DEV), dout.to(DEV)
+            ddev[~known.to(DEV)] = float("nan")  # not read
+            want = torch.zeros(vocab, cols, dtype=table, device=DEV)
+            want[at.to(DEV)] = total.float().to(table).to(DEV)
+            assert torch.equal(lib.embedding_backward(ddev, dev, vocab, dtype=table), want), (table, tokens)
+            wide = torch.full((vocab, cols + 3), 5.0, dtype=table, device=DEV)  # rows of a wider table
+            lib.embedding_backward(ddev, dev.int(), vocab, dtable=wide[:, 1:1 + cols])
+            assert torch.equal(wide[:, 1:1 + cols], want), (table, tokens)
+            assert (wide[:, 0] == 5).all() and (wide[:, 1 + cols:] == 5).all()
+            old = S.small_integers((vocab, cols), 81, table).to(DEV)
+            want = old.clone()
+            want[at.to(DEV)] = (total.float() * 0.5 + old[at.to(DEV)].cpu().float()).to(table).to(DEV)
+            lib.embedding_backward(ddev, dev, vocab, scale=0.5, dtable=old, accumulate=True)
+            assert torch.equal(old, want), (table, tokens)
+
+
+@pytest.mark.parametrize("cols,dtype,lanes", CROWDED[::2])
+def test_embedding_gradient_of_few_tokens_against_fp64(cols, dtype, lanes):
+    for table, tokens in ((BF, 512), (F32, 512), (F32, 513)):
+        size = 2 if table == BF else 4
+        ids = crowded(tokens, 5000, min(65536 // (cols * size), 9, 1024), 90)
+        dout, weight, old = randn((tokens, cols), 91, dtype), randn((5000, cols), 92, table), randn((5000, cols), 93, table)
+        for given in (None, old):
+            ref = R.embedding(weight.cpu(), ids, 0.7, dtype, dout.cpu(), table, None if given is None else given.cpu())
+            got = lib.embedding_backward(dout, ids.to(DEV), 5000, scale=0.7, dtype=table,
+                                         dtable=None if given is None else given.clone(), accumulate=given is not None)
+            say(f"[gpu] crowded rows {tokens} tokens x{cols} {dtype} into {table}: worst error "
+                f"{B.check('dtable', got, *ref['dtable']):.3f} of its bound")

@@ -40,3 +40,27 @@ def test_sums_of_integers_see_a_lost_or_doubled_token():
     old = S.small_integers((41, 4), 5, torch.float32)
     assert torch.equal(S.embedding_sums(ids, dout, 41, old), want + old.long())
     assert torch.equal(S.embedding_sums(torch.tensor([-1, 41, 1]), dout[:3], 41)[1], dout[2].long())
+
+
+def test_crowded_ids_fall_where_they_are_meant_to():
+    from test_gpu_token_gradients import CROWDED, crowded
+
+    lanes_seen = set()
+    for cols, dtype, lanes in CROWDED:
+        vectors = -(-cols // (8 if dtype == torch.bfloat16 else 4))
+        most = 64
+        while most > 8 and -(-vectors // most) * most * 8 > vectors * 9:
+            most //= 2
+        assert lanes == most, (cols, dtype, most)
+        lanes_seen.add(lanes)
+        for vocab in (5000, 50257):
+            for size in (2, 4):
+                rows = min(65536 // (cols * size), vocab // 512, 1024)
+                for tokens in (511, 512, 513):
+                    ids = crowded(tokens, vocab, rows, tokens)
+                    assert len(ids) == tokens
+                    n = torch.bincount(ids[(ids >= 0) & (ids < vocab)], minlength=vocab)
+                    block = n[3 * rows:4 * rows]
+                    assert block[0] >= 40 and block[-1] >= 200 and (block > 8).sum() >= 3 and (block[1:3] > 0).all()
+                    assert n[vocab - 1] >= 9 and vocab % rows and n[vocab // rows * rows] >= (17 if vocab % rows > 1 else 9)
+    assert lanes_seen == {8, 16, 32, 64}
