@@ -431,9 +431,10 @@ int muon_attention_backward(const muon_attention_desc* desc, const int32_t* cu_s
  * flag is given.  cu_seqlens is not checked: with offsets that are not in
  * order, positions are undefined, but no access leaves the operands.
  *
- * Arithmetic is fp32, results are rounded once.  Angles are exact to 2^-31
- * turns at positions of magnitude up to 2^32, and off by up to 2^-63 turns
- * times a farther position.  Squares are fp32 numbers, too: mean(x^2) + eps has
+ * Arithmetic is fp32, results are rounded once.  A position's angle is exact to
+ * 2^-31 turns at magnitudes up to 2^32, and off by up to 2^-63 turns times a
+ * farther position; its cosine and sine are taken in fp32 and off by up to
+ * 2^-23 besides.  Squares are fp32 numbers, too: mean(x^2) + eps has
  * to lie between 2^-120 and 2^120. */
 typedef struct muon_qk_norm_desc {
   int64_t tokens;
