@@ -2,14 +2,15 @@
 //
 // Forward: y[t] = scale * table[id_t]; an id outside the table gives a row of zeros.
 // Backward: dtable[v] = scale * sum of dout[t] over the tokens t with id_t = v, in
-// fp32 and in an order that only the ids decide: the tokens are sorted by id
-// (stable radix sort, so in token order within an id), groups of lanes sum chunks
-// of the sorted list, and ids that reach over a chunk's end are joined in order.
+// fp32 and in an order that only the ids and sizes decide: the tokens are sorted
+// by id (stable radix sort, so in token order within an id), groups of lanes sum
+// chunks of the sorted list, and ids that reach over a chunk's end are joined in
+// order.
 //
 // Bound by memory: forward, 65536 rows of 768 in bf16 out of 50304 take 26 to 31
 // us (126 MB, 4.1 to 4.9 TB/s).  Backward, the table's zeros (77 MB: 12 us alone)
 // are written while the tokens are sorted, 26 us in four launches that latency
-// bounds; sums 30 us (100 MB read in the ids' order, 3.3 TB/s), joining 8.
+// bounds; sums 30 us (100 MB read in the ids' order, 25 written, 4.2 TB/s), joining 8.
 #include "block_internal.h"
 #include "device_common.h"
 #include "row_vectors.h"
@@ -291,7 +292,8 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, uint32_t id, i
 // A vector of a row as it was loaded: whole ones of bf16 stay packed, in half the
 // registers.  Rows of more than the caches keep are read past them (whole
 // vectors): 65536 x 768 in bf16 30 us instead of 35, but 32768 x 128, which the
-// caches hold, 12 instead of 11.
+// caches hold, 12 instead of 11 (96 and 8 MiB; the rule's 32 lies between them, no
+// size between was measured).
 template <class O, bool PART, bool STREAM>
 struct Held {
   float v[kVec<O>];
@@ -462,7 +464,10 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedGradArgs a) {
 // tokens for 50304 x 768 in bf16 16 us instead of 22, for 5000 x 256 7 instead
 // of 17, for 64 x 768 8 instead of 12; all of them of one id 32 instead of 23
 // (50304 x 768; 256 tokens 22 and 22).  1024 tokens took 19 instead of 23 and 61
-// instead of 23, so they are sorted.
+// instead of 23, so they are sorted.  The tokens alone decide, which loses for
+// tables of few wide rows (512 tokens of 2 x 4096 61 us, 513, which are sorted, 14)
+// and for adding to very large ones (one token into 2^24 x 64 in fp32 143 us, 513
+// tokens 15; into 2^20 x 64 12 and 14).
 constexpr int kDirectItems = kDirect / kThreads, kDirectWaves = kThreads / 64, kShared = 8;
 template <class T, class O, bool PART, int LPR>
 __global__ __launch_bounds__(kThreads) void embed_direct_kernel(EmbedGradArgs a) {
@@ -698,7 +703,7 @@ void plan_embed(EmbedGradArgs& a, bool table_bf16, bool out_bf16) {
   while (a.lanes > 8 && (vectors + a.lanes - 1) / a.lanes * a.lanes * 8 > vectors * 9) a.lanes /= 2;
   // fewer entries a group while blocks are few: sums of 32768 x 128 in bf16 8.6 us instead of 11.0 (256 blocks of 8),
   // of 4099 x 1001 in fp32 8.0 instead of 10.5 (516); but with the runs' joining, 42 us instead of 37 for 65536 x 768
-  // (over 3000)
+  // (over 3000; nothing between 516 and 3000 was measured)
   a.chunk = kThreads / a.lanes * kEmbedEach;
   const int64_t blocks8 = (a.tokens + a.chunk - 1) / a.chunk * ((vectors + a.lanes - 1) / a.lanes);
   if (blocks8 < 1024) a.chunk = kThreads / a.lanes * kFewEach;

@@ -48,10 +48,10 @@ def embedding_forward(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 
     """scale * table[ids], of shape ids.shape + (columns,).
 
     table (vocab, columns): float32 or bfloat16, with contiguous columns.
-    ids: int32 or int64; one outside [0, vocab), such as the padding of a
-    batch, has a row of zeros and passes no gradient on.  dtype: the result's,
-    default the table's (or that of a given out).  scale: a number; a tensor
-    is refused, for its gradient would be lost.
+    ids: int32 or int64, contiguous; one outside [0, vocab), such as the
+    padding of a batch, has a row of zeros and passes no gradient on.  dtype:
+    the result's, default the table's (or that of a given out).  scale: a
+    number; a tensor is refused, for its gradient would be lost.
     """
     _check_scale(scale)
     if _recorded(table, None, None):
